@@ -51,7 +51,7 @@ typedef enum {
     SPEC_EHIP = -4          /* a HIP runtime call (launch) failed */
 } spec_status;
 
-typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1, SPEC_F64 = 2 } spec_dtype;
+typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1, SPEC_F64 = 2, SPEC_I32 = 3, SPEC_I64 = 4 } spec_dtype;
 
 /* Human-readable text of a status code (static storage, never NULL). */
 const char *spec_strerror(int status);
@@ -530,6 +530,98 @@ enum {
 int spec_timing_enable(unsigned kernels);
 
 int spec_timing_read(int kernel, double *total_ms, int64_t *launches);
+
+/* ------------------------------------------------------------------------
+ * Training a projected student.  [RMT] section 4.1 trains the compressed layers
+ * W' = P^T W P on the task's loss; the entry points below are the two ends of
+ * such a step that hold the vocabulary, and the update of its matrices:
+ *   embedding lookup and its gradient, the softmax cross entropy of the
+ *   vocabulary head with its gradients, Newton-Schulz orthogonalisation.
+ * Token ids are device arrays of SPEC_I32 or SPEC_I64 (idt / tt).  An id outside
+ * [0, V) is no token: padding, a masked prompt.  Its row of the lookup is zero,
+ * its loss and lse are 0, and it adds to no gradient, whatever its rows of dY or
+ * H hold (NaN included).  Results are the same in every run (no floating-point
+ * atomics).
+ * ---------------------------------------------------------------------- */
+
+/* Embedding lookup:  Y[i] = scale * E[ids[i]]  (computed in f32, rounded once).
+ * E: [V][lde], Y: [n][ldy], both of type t = SPEC_BF16 or SPEC_F32 (else
+ * SPEC_EUNSUPPORTED), d values per row; Y must not overlap E.
+ * Requires 1 <= V < 2^31, 1 <= d <= 2^20, 0 <= n < 2^31, lde, ldy >= d; else SPEC_EINVAL. */
+int spec_embed(void *stream, const void *E, int t, int64_t V, int64_t d, int64_t lde, const void *ids, int idt,
+               int64_t n, double scale, void *Y, int64_t ldy);
+
+/* Its gradient:  dE[v] = beta dE[v] + scale * sum over ids[i] = v of dY[i].
+ * The positions are sorted by id and added in f32 in order of position.
+ * beta == 0: all V rows are written (zeros where no token is v; the previous
+ * contents are ignored).  beta == 1: only the rows of tokens present are read
+ * and written (e.g. into the dW of spec_linear_xent_grad when the head is tied).
+ * Other values of beta: SPEC_EUNSUPPORTED.
+ * dY: [n][ldy] of type yt; dE: [V][ldd] of type et.  (yt, et) is
+ * (SPEC_BF16, SPEC_BF16), (SPEC_BF16, SPEC_F32) or (SPEC_F32, SPEC_F32).
+ * ws: device workspace of spec_embed_grad_workspace(n, V, d) bytes (256-byte aligned).
+ * Requires the sizes of spec_embed with ldy, ldd >= d; else SPEC_EINVAL. */
+int spec_embed_grad_workspace(int64_t n, int64_t V, int64_t d, size_t *bytes);
+
+int spec_embed_grad(void *stream, const void *dY, int yt, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
+                    int idt, double scale, double beta, void *dE, int et, int64_t ldd, void *ws, size_t ws_bytes);
+
+/* Softmax cross entropy of a linear head, the logits formed tile by tile and
+ * never stored:
+ *   z_tv = scale <H_t, W_v>,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target
+ * H: [T][ldh], W: [V][ldw], both of type t = SPEC_BF16 (MFMA bf16, f32
+ * accumulation) or SPEC_F32 (MFMA f32); target: ids [T]; loss, lse: f32 [T].
+ * A row whose logits hold NaN or +inf has loss and lse NaN.
+ * ws: device workspace of spec_linear_xent_workspace(T, V, d, t) bytes (256-byte
+ * aligned): packed H, one (max, sum) pair per row and 128 logits.
+ * Requires 1 <= V < 2^31, 1 <= d <= 2^20, 0 <= T <= 2^22, ldh, ldw >= d and
+ * <= 2^20 + 64; else SPEC_EINVAL.  16-byte aligned rows of W are read in place,
+ * others are copied a piece at a time. */
+int spec_linear_xent_workspace(int64_t T, int64_t V, int64_t d, int t, size_t *bytes);
+
+int spec_linear_xent(void *stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d, int64_t ldh,
+                     int64_t ldw, const void *target, int tt, double scale, float *loss, float *lse, void *ws,
+                     size_t ws_bytes);
+
+/* Its gradients for weights dloss (f32 [T]) on the rows' losses (1 / number of
+ * targets for the mean):
+ *   G_tv = scale dloss_t (exp(z_tv - lse_t) - [v = target_t]),
+ *   dH = G W,  dW = beta dW + G^T H
+ * lse: as spec_linear_xent returned it for the same H, W, target and scale.
+ * The vocabulary is taken in pieces whose T x piece matrix G (type t) is held in
+ * the workspace; the logits are formed again, the sums are f32.
+ * dH: [T][lddh], dW: [V][lddw], type t; beta == 0 ignores dW's previous contents.
+ * Outputs must not overlap inputs or ws.
+ * ws: device workspace of spec_linear_xent_grad_workspace(T, V, d, t) bytes
+ * (256-byte aligned).  Requires the conditions of spec_linear_xent. */
+int spec_linear_xent_grad_workspace(int64_t T, int64_t V, int64_t d, int t, size_t *bytes);
+
+int spec_linear_xent_grad(void *stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d,
+                          int64_t ldh, int64_t ldw, const void *target, int tt, double scale, const float *lse,
+                          const float *dloss, double beta, void *dH, int64_t lddh, void *dW, int64_t lddw, void *ws,
+                          size_t ws_bytes);
+
+/* Orthogonalisation of `batch` updates by Newton-Schulz products (the update of
+ * the Muon optimiser):
+ *   X = G / (|G|_F + eps);  per step k: A = X X^T, X <- a_k X + (b_k A + c_k A^2) X;  O = scale X
+ * (X^T X from the right when m > n).  A step multiplies every singular value s
+ * of X by a + b s^2 + c s^4 and keeps the singular vectors.
+ * G: element (i, r, c) at G[i*sg + r*ldg + c], m x n, type t = SPEC_BF16 or
+ * SPEC_F32; O likewise with so, ldo, type t.  O may be G itself.
+ * coeffs: HOST array of steps x 3 doubles (a, b, c), read before the call returns.
+ * SPEC_BF16: f16 MFMA products with X held to 22 bits and the diagonals of A and
+ * bA + cA^2 in f32; SPEC_F32: f32 MFMA.  A zero G gives a zero O.
+ * ws: device workspace of spec_orthogonalize_workspace(batch, m, n, t) bytes
+ * (256-byte aligned).
+ * Requires 1 <= m, n <= 65536 with min(m, n) <= 32768, 1 <= batch <= 65535, ldg, ldo >= n,
+ * sg >= m*ldg and so >= m*ldo when batch > 1, 1 <= steps <= 32, eps >= 0,
+ * finite coefficients and scale, and (SPEC_BF16) coefficients that keep every s in
+ * [0, 1] below 2^7; else SPEC_EINVAL. */
+int spec_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int t, size_t *bytes);
+
+int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
+                       const double *coeffs, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so,
+                       void *ws, size_t ws_bytes);
 
 #ifdef __cplusplus
 }

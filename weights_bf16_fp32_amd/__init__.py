@@ -13,6 +13,11 @@ fallback of any kind.
     rec = spec.descriptors(w, n_samples=n, p_dim=d, k=1)      # structured numpy array
     sm = spec.desc_smooth(raw_records, streams=S, W=W, alpha=0.3)  # smoothed descriptor series
     rb = spec.spectrum_robust(w, n_samples=n, p_dim=d)        # median/MAD/winsor/log/KL statistics
+    X = spec.embed(E, ids, scale=d ** 0.5)                    # scale * E[ids]
+    loss, lse = spec.linear_xent(H, W, target)                # cross entropy of the rows of H W^T
+    dH, dW = spec.linear_xent_grad(H, W, target, lse, dloss)  # its gradients
+    spec.embed_grad(dX, ids, V, scale=d ** 0.5, beta=1.0, dE=dW)  # into a tied table's gradient
+    O = spec.orthogonalize(G)                                 # Newton-Schulz: G with its singular values near one
 """
 from __future__ import annotations
 
@@ -26,12 +31,14 @@ __all__ = [
     "eigvalsh_batched_band", "eigvalsh_large", "eigvalsh_large_workspace", "descriptors",
     "descriptors_workspace", "DESC_DTYPE", "desc_smooth", "spectrum_robust", "ROBUST_DTYPE", "eigvalsh_topk",
     "eigvecs_topk", "project_weight", "project_weight_workspace",
+    "embed", "embed_grad", "embed_grad_workspace", "linear_xent", "linear_xent_workspace", "linear_xent_grad",
+    "linear_xent_grad_workspace", "orthogonalize", "orthogonalize_workspace", "NS_COEFFS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspec.so")
 
-BF16, F32, F64 = 0, 1, 2
+BF16, F32, F64, I32, I64 = 0, 1, 2, 3, 4
 GRAM_BAND, GRAM_DENSE = 0, 1
 SRC_DENSE, SRC_BAND = 0, 1
 MODE_EIG, MODE_SINGULAR = 0, 1
@@ -98,7 +105,10 @@ EXPORTS = ["spec_strerror", "spec_version", "spec_cov_accumulate", "spec_gram_wi
            "spec_descriptors_workspace", "spec_descriptors", "spec_desc_smooth", "spec_spectrum_robust",
            "spec_eigvalsh_topk", "spec_eigvecs_topk", "spec_project_weight_workspace",
            "spec_project_weight", "spec_timing_enable", "spec_timing_read", "spec_descriptors_static", "spec_tail_pair_screen", "spec_eigvalsh_batched_desc",
-           "spec_eigvalsh_sliding", "spec_eigh_large_workspace", "spec_eigh_large", "spec_eigh_batched"]
+           "spec_eigvalsh_sliding", "spec_eigh_large_workspace", "spec_eigh_large", "spec_eigh_batched",
+           "spec_embed", "spec_embed_grad_workspace", "spec_embed_grad", "spec_linear_xent_workspace",
+           "spec_linear_xent", "spec_linear_xent_grad_workspace", "spec_linear_xent_grad",
+           "spec_orthogonalize_workspace", "spec_orthogonalize"]
 
 _lib = None
 
@@ -140,6 +150,18 @@ def lib() -> ctypes.CDLL:
         L.spec_descriptors_static.argtypes = [vp, vp, i32, i64, i64, i64, ctypes.POINTER(DescParams), vp]
         L.spec_eigvalsh_sliding.argtypes = [vp, ctypes.POINTER(BatchSrc), i64, i32, i32, vp, vp]
         L.spec_eigh_batched.argtypes = [vp, ctypes.POINTER(BatchSrc), i64, i32, vp, vp, vp]
+        sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.spec_embed.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i64, dbl, vp, i64]
+        L.spec_embed_grad_workspace.argtypes = [i64, i64, i64, szp]
+        L.spec_embed_grad.argtypes = [vp, vp, i32, i64, i64, i64, i64, vp, i32, dbl, dbl, vp, i32, i64, vp, sz]
+        L.spec_linear_xent_workspace.argtypes = [i64, i64, i64, i32, szp]
+        L.spec_linear_xent.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i64, vp, i32, dbl, vp, vp, vp, sz]
+        L.spec_linear_xent_grad_workspace.argtypes = [i64, i64, i64, i32, szp]
+        L.spec_linear_xent_grad.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i64, vp, i32, dbl, vp, vp, dbl, vp,
+                                            i64, vp, i64, vp, sz]
+        L.spec_orthogonalize_workspace.argtypes = [i64, i64, i64, i32, szp]
+        L.spec_orthogonalize.argtypes = [vp, vp, i32, i64, i64, i64, i64, i64, ctypes.POINTER(dbl), i32, dbl, dbl,
+                                         vp, i64, i64, vp, sz]
         L.spec_timing_enable.argtypes = [ctypes.c_uint]
         L.spec_timing_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
         for f in EXPORTS[2:]:
@@ -580,3 +602,175 @@ def eigvalsh_batched_dense_desc(A, *, n_samples: int, p_dim: int, k: int = 1, w=
     _check(lib().spec_eigvalsh_batched_desc(_stream(), ctypes.byref(src), batch, n, _dev(w), _dev(info),
                                             ctypes.byref(p), _dev(out), _dev(ws), ws.numel()))
     return w, info, out.cpu().numpy().view(DESC_DTYPE).reshape(batch)
+
+
+# ---------------------------------------------------------------- training a projected student
+
+#: Five equal steps a s + b s^3 + c s^5 that take singular values from (0, 1] to
+#: about 0.7 .. 1.2 (Muon's coefficients).
+NS_COEFFS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _ids(ids, n=None):
+    torch = _torch()
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise SpecError(-2, f"token ids must be int32 or int64, not {ids.dtype}")
+    if ids.dim() != 1 or not ids.is_contiguous() or (n is not None and ids.shape[0] != n):
+        raise SpecError(-1, "token ids must be a contiguous vector, one per row")
+    return _dev(ids), I32 if ids.dtype == torch.int32 else I64
+
+
+def _rows(*ts):
+    for t in ts:
+        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+            raise SpecError(-1, "matrices must be 2-D with a contiguous inner dimension")
+
+
+def _ld(t):
+    """Row stride; of a single row its length, whatever stride it carries."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vec32(t, n):
+    if t.dtype != _torch().float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise SpecError(-1, "per-row values must be a contiguous float32 vector, one per row")
+    return _dev(t)
+
+
+def _matrix(t, shape, dtype):
+    """An output the caller passed: its shape and type must be the result's."""
+    _rows(t)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise SpecError(-1, f"output must be {tuple(shape)} of {dtype}")
+
+
+def _bytes(query, *args):
+    b = ctypes.c_size_t(0)
+    _check(query(*args, ctypes.byref(b)))
+    return b.value
+
+
+def _ws(ws, size, device):
+    return _torch().empty((size,), dtype=_torch().uint8, device=device) if ws is None else ws
+
+
+def embed(E, ids, scale: float = 1.0, out=None):
+    """scale * E[ids] [n, d] for token ids [n] (int32 or int64); a zero row where
+    an id is no row of E [V, d]."""
+    _rows(E)
+    V, d = E.shape
+    p, idt = _ids(ids)
+    n = ids.shape[0]
+    if out is None:
+        out = _torch().empty((n, d), dtype=E.dtype, device=E.device)
+    _matrix(out, (n, d), E.dtype)
+    _check(lib().spec_embed(_stream(), _dev(E), _dt(E), V, d, _ld(E), p, idt, n, float(scale), _dev(out), _ld(out)))
+    return out
+
+
+def embed_grad_workspace(n: int, V: int, d: int) -> int:
+    return _bytes(lib().spec_embed_grad_workspace, n, V, d)
+
+
+def embed_grad(dY, ids, V: int, scale: float = 1.0, beta: float = 0.0, dE=None, ws=None):
+    """dE[v] = beta dE[v] + scale * sum of the rows dY[i] with ids[i] = v, [V, d].
+    beta 0 writes every row, beta 1 adds to the rows present.  dE is of dY's type,
+    or float32 for a bfloat16 dY."""
+    torch = _torch()
+    _rows(dY)
+    n, d = dY.shape
+    p, idt = _ids(ids, n)
+    if dE is None:
+        if beta != 0.0:
+            raise SpecError(-1, "beta needs the dE to add to")
+        dE = torch.empty((V, d), dtype=dY.dtype, device=dY.device)
+    _matrix(dE, (V, d), dE.dtype)
+    ws = _ws(ws, embed_grad_workspace(n, V, d), dY.device)
+    _check(lib().spec_embed_grad(_stream(), _dev(dY), _dt(dY), n, V, d, _ld(dY), p, idt, float(scale), float(beta),
+                                 _dev(dE), _dt(dE), _ld(dE), _dev(ws), ws.numel()))
+    return dE
+
+
+def _head(H, W):
+    _rows(H, W)
+    if H.shape[1] != W.shape[1] or H.dtype != W.dtype:
+        raise SpecError(-1, "H [T, d] and W [V, d] must agree in d and type")
+    return H.shape[0], W.shape[0], W.shape[1]
+
+
+def linear_xent_workspace(T: int, V: int, d: int, dtype) -> int:
+    return _bytes(lib().spec_linear_xent_workspace, T, V, d, _dt(_torch().empty(0, dtype=dtype)))
+
+
+def linear_xent(H, W, target, scale: float = 1.0, loss=None, lse=None, ws=None):
+    """Softmax cross entropy of the logits scale * H W^T: (loss, lse), float32
+    [T], both 0 where target is no row of W.  H [T, d], W [V, d]."""
+    torch = _torch()
+    T, V, d = _head(H, W)
+    p, tt = _ids(target, T)
+    if loss is None:
+        loss = torch.empty((T,), dtype=torch.float32, device=H.device)
+    if lse is None:
+        lse = torch.empty((T,), dtype=torch.float32, device=H.device)
+    t = _dt(H)
+    ws = _ws(ws, _bytes(lib().spec_linear_xent_workspace, T, V, d, t), H.device)
+    _check(lib().spec_linear_xent(_stream(), _dev(H), _dev(W), t, T, V, d, _ld(H), _ld(W), p, tt, float(scale),
+                                  _vec32(loss, T), _vec32(lse, T), _dev(ws), ws.numel()))
+    return loss, lse
+
+
+def linear_xent_grad_workspace(T: int, V: int, d: int, dtype) -> int:
+    return _bytes(lib().spec_linear_xent_grad_workspace, T, V, d, _dt(_torch().empty(0, dtype=dtype)))
+
+
+def linear_xent_grad(H, W, target, lse, dloss, scale: float = 1.0, beta: float = 0.0, dH=None, dW=None, ws=None):
+    """Gradients of sum(dloss * loss) of linear_xent, with its lse: dH [T, d] and
+    dW = beta dW + ... [V, d].  dloss: float32 [T]."""
+    torch = _torch()
+    T, V, d = _head(H, W)
+    p, tt = _ids(target, T)
+    if dH is None:
+        dH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+    if dW is None:
+        if beta != 0.0:
+            raise SpecError(-1, "beta needs the dW to add to")
+        dW = torch.empty((V, d), dtype=W.dtype, device=W.device)
+    _matrix(dH, (T, d), H.dtype)
+    _matrix(dW, (V, d), W.dtype)
+    t = _dt(H)
+    ws = _ws(ws, _bytes(lib().spec_linear_xent_grad_workspace, T, V, d, t), H.device)
+    _check(lib().spec_linear_xent_grad(_stream(), _dev(H), _dev(W), t, T, V, d, _ld(H), _ld(W), p, tt, float(scale),
+                                       _vec32(lse, T), _vec32(dloss, T), float(beta), _dev(dH), _ld(dH), _dev(dW),
+                                       _ld(dW), _dev(ws), ws.numel()))
+    return dH, dW
+
+
+def orthogonalize_workspace(batch: int, m: int, n: int, dtype) -> int:
+    return _bytes(lib().spec_orthogonalize_workspace, batch, m, n, _dt(_torch().empty(0, dtype=dtype)))
+
+
+def orthogonalize(G, coeffs=NS_COEFFS, eps: float = 1e-7, scale: float = 1.0, out=None, ws=None):
+    """Newton-Schulz orthogonalisation of G [m, n] or [batch, m, n]: one step
+    X <- a X + (b X X^T + c (X X^T)^2) X per (a, b, c) of coeffs, from
+    X = G / (|G|_F + eps); returns scale * X in G's type (out may be G)."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    if G.dim() not in (2, 3) or out.shape != G.shape or out.dtype != G.dtype:
+        raise SpecError(-1, "G must be [m, n] or [batch, m, n] and out of its shape and type")
+    g, o = (G.unsqueeze(0), out.unsqueeze(0)) if G.dim() == 2 else (G, out)
+    batch, m, n = g.shape
+    if (g.stride(2) != 1 or o.stride(2) != 1) and n != 1:
+        raise SpecError(-1, "inner dimension must be contiguous")
+
+    def strides(t):
+        ld = t.stride(1) if m > 1 else n
+        return ld, (t.stride(0) if batch > 1 else m * ld)
+    (ldg, sg), (ldo, so) = strides(g), strides(o)
+    steps = len(coeffs)
+    co = (ctypes.c_double * (3 * max(steps, 1)))(*[float(x) for c in coeffs for x in c])
+    t = _dt(G)
+    ws = _ws(ws, _bytes(lib().spec_orthogonalize_workspace, batch, m, n, t), G.device)
+    _check(lib().spec_orthogonalize(_stream(), _dev(G), t, batch, m, n, ldg, sg, co, steps, float(eps), float(scale),
+                                    _dev(out), ldo, so, _dev(ws), ws.numel()))
+    return out

@@ -45,6 +45,36 @@ int check_descriptors(const void *w, int wt, int64_t batch, int64_t r, int64_t l
     return SPEC_OK;
 }
 
+// sizes shared by the vocabulary operators, and the type of a token id array
+int check_rows(int64_t n, int64_t V, int64_t d)
+{
+    const int64_t lim = (int64_t)1 << 31;
+    if (n < 0 || n >= lim || V < 1 || V >= lim - 1 || d < 1 || d > ((int64_t)1 << 20)) return SPEC_EINVAL;
+    return SPEC_OK;
+}
+
+int check_ids(const void *ids, int idt, int64_t n)
+{
+    if (idt != SPEC_I32 && idt != SPEC_I64) return SPEC_EUNSUPPORTED;
+    if (n > 0 && (ids == nullptr || !aligned(ids, idt == SPEC_I32 ? 4 : 8))) return SPEC_EINVAL;
+    return SPEC_OK;
+}
+
+int check_xent_sizes(int64_t T, int64_t V, int64_t d, int t)
+{
+    if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    if (T > ((int64_t)1 << 22)) return SPEC_EINVAL;
+    return check_rows(T, V, d);
+}
+
+int check_ortho_sizes(int64_t batch, int64_t m, int64_t n, int t)
+{
+    if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    if (batch < 1 || batch > 65535 || m < 1 || n < 1 || m > 65536 || n > 65536 || (m > 32768 && n > 32768))
+        return SPEC_EINVAL;
+    return SPEC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -341,6 +371,138 @@ int spec_tail_pair_screen(void *stream, const void *U, const void *V, int dt, in
     if ((absdot != nullptr && !aligned(absdot, 8)) || (count != nullptr && !aligned(count, 8))) return SPEC_EINVAL;
     return from_hip(launch_tail_pair_screen((hipStream_t)stream, U, V, dt, n, ldu, ldv, i0, t, head_dim, eps, absdot,
                                             ldo, keep, ldk, count));
+}
+
+int spec_embed(void *stream, const void *E, int t, int64_t V, int64_t d, int64_t lde, const void *ids, int idt,
+               int64_t n, double scale, void *Y, int64_t ldy)
+{
+    if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    int st = check_rows(n, V, d);
+    if (st != SPEC_OK) return st;
+    st = check_ids(ids, idt, n);
+    if (st != SPEC_OK) return st;
+    if (E == nullptr || (Y == nullptr && n > 0) || lde < d || ldy < d || !isfinite(scale)) return SPEC_EINVAL;
+    if (!aligned(E, elt_size(t)) || !aligned(Y, elt_size(t))) return SPEC_EINVAL;
+    return from_hip(launch_embed((hipStream_t)stream, E, t, V, d, lde, ids, idt == SPEC_I64, n, (float)scale, Y, ldy));
+}
+
+int spec_embed_grad_workspace(int64_t n, int64_t V, int64_t d, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_rows(n, V, d);
+    if (st != SPEC_OK) return st;
+    *bytes = embed_grad_workspace_bytes(n, V, d);
+    return SPEC_OK;
+}
+
+int spec_embed_grad(void *stream, const void *dY, int yt, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
+                    int idt, double scale, double beta, void *dE, int et, int64_t ldd, void *ws, size_t ws_bytes)
+{
+    const bool pair_ok = (yt == SPEC_BF16 && (et == SPEC_BF16 || et == SPEC_F32)) || (yt == SPEC_F32 && et == SPEC_F32);
+    if (!pair_ok) return SPEC_EUNSUPPORTED;
+    int st = check_rows(n, V, d);
+    if (st != SPEC_OK) return st;
+    st = check_ids(ids, idt, n);
+    if (st != SPEC_OK) return st;
+    if (dE == nullptr || (dY == nullptr && n > 0) || ldy < d || ldd < d || !isfinite(scale)) return SPEC_EINVAL;
+    if (!aligned(dY, elt_size(yt)) || !aligned(dE, elt_size(et))) return SPEC_EINVAL;
+    if (beta != 0.0 && beta != 1.0) return isfinite(beta) ? SPEC_EUNSUPPORTED : SPEC_EINVAL;
+    if (ws == nullptr || ws_bytes < embed_grad_workspace_bytes(n, V, d)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_embed_grad((hipStream_t)stream, dY, yt, n, V, d, ldy, ids, idt == SPEC_I64, (float)scale,
+                                      beta == 1.0, dE, et, ldd, ws));
+}
+
+int spec_linear_xent_workspace(int64_t T, int64_t V, int64_t d, int t, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_xent_sizes(T, V, d, t);
+    if (st != SPEC_OK) return st;
+    *bytes = linear_xent_workspace_bytes(T, V, d, t);
+    return SPEC_OK;
+}
+
+// what both directions of the cross entropy ask of H, W and the targets
+static int check_xent(const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d, int64_t ldh, int64_t ldw,
+                      const void *target, int tt, double scale)
+{
+    int st = check_xent_sizes(T, V, d, t);
+    if (st != SPEC_OK) return st;
+    st = check_ids(target, tt, T);
+    if (st != SPEC_OK) return st;
+    const int64_t most = ((int64_t)1 << 20) + 64;
+    if (W == nullptr || (H == nullptr && T > 0) || ldh < d || ldw < d || ldh > most || ldw > most || !isfinite(scale))
+        return SPEC_EINVAL;
+    if (!aligned(H, elt_size(t)) || !aligned(W, elt_size(t))) return SPEC_EINVAL;
+    return SPEC_OK;
+}
+
+int spec_linear_xent(void *stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d, int64_t ldh,
+                     int64_t ldw, const void *target, int tt, double scale, float *loss, float *lse, void *ws,
+                     size_t ws_bytes)
+{
+    const int st = check_xent(H, W, t, T, V, d, ldh, ldw, target, tt, scale);
+    if (st != SPEC_OK) return st;
+    if (T > 0 && (loss == nullptr || lse == nullptr)) return SPEC_EINVAL;
+    if (!aligned(loss, 4) || !aligned(lse, 4)) return SPEC_EINVAL;
+    if (ws == nullptr || ws_bytes < linear_xent_workspace_bytes(T, V, d, t)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_linear_xent((hipStream_t)stream, H, W, t, T, V, d, ldh, ldw, target, tt == SPEC_I64,
+                                       (float)scale, loss, lse, ws));
+}
+
+int spec_linear_xent_grad_workspace(int64_t T, int64_t V, int64_t d, int t, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_xent_sizes(T, V, d, t);
+    if (st != SPEC_OK) return st;
+    *bytes = linear_xent_grad_workspace_bytes(T, V, d, t);
+    return SPEC_OK;
+}
+
+int spec_linear_xent_grad(void *stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d,
+                          int64_t ldh, int64_t ldw, const void *target, int tt, double scale, const float *lse,
+                          const float *dloss, double beta, void *dH, int64_t lddh, void *dW, int64_t lddw, void *ws,
+                          size_t ws_bytes)
+{
+    const int st = check_xent(H, W, t, T, V, d, ldh, ldw, target, tt, scale);
+    if (st != SPEC_OK) return st;
+    if (T > 0 && (lse == nullptr || dloss == nullptr || dH == nullptr)) return SPEC_EINVAL;
+    if (dW == nullptr || lddh < d || lddw < d || !isfinite(beta)) return SPEC_EINVAL;
+    if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dH, elt_size(t)) || !aligned(dW, elt_size(t)))
+        return SPEC_EINVAL;
+    if (ws == nullptr || ws_bytes < linear_xent_grad_workspace_bytes(T, V, d, t)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_linear_xent_grad((hipStream_t)stream, H, W, t, T, V, d, ldh, ldw, target, tt == SPEC_I64,
+                                            (float)scale, lse, dloss, dH, lddh, dW, lddw, (float)beta, ws));
+}
+
+int spec_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int t, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_ortho_sizes(batch, m, n, t);
+    if (st != SPEC_OK) return st;
+    *bytes = orthogonalize_workspace_bytes(batch, m, n, t);
+    return SPEC_OK;
+}
+
+int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
+                       const double *coeffs, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so,
+                       void *ws, size_t ws_bytes)
+{
+    const int st = check_ortho_sizes(batch, m, n, t);
+    if (st != SPEC_OK) return st;
+    if (G == nullptr || O == nullptr || coeffs == nullptr || ldg < n || ldo < n) return SPEC_EINVAL;
+    if (batch > 1 && (sg < m * ldg || so < m * ldo)) return SPEC_EINVAL;
+    if (steps < 1 || steps > 32 || !(eps >= 0.0) || !isfinite(eps) || !isfinite(scale)) return SPEC_EINVAL;
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!isfinite(coeffs[i])) return SPEC_EINVAL;
+    if (t == SPEC_BF16 && !orthogonalize_bounded(coeffs, steps)) return SPEC_EINVAL;
+    if (!aligned(G, elt_size(t)) || !aligned(O, elt_size(t))) return SPEC_EINVAL;
+    if (ws == nullptr || ws_bytes < orthogonalize_workspace_bytes(batch, m, n, t)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_orthogonalize((hipStream_t)stream, G, t, batch, m, n, ldg, sg, coeffs, steps, eps, scale, O,
+                                         ldo, so, ws));
 }
 
 }  // extern "C"

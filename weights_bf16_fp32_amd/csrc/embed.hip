@@ -1,0 +1,358 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens, gfx950.
+//
+//   Y[i] = scale E[ids[i]];   dE[v] = scale sum_{ids[i] = v} dY[i]  (+ dE[v])
+//
+// A position whose id is no row of E gives a zero row and takes no gradient.
+// Both are bound by memory: one read and one write per element.
+//
+// Gradient: the positions are sorted by id (stable, least significant digit
+// first), so that the rows to be added lie next to each other, in the order of
+// their positions; sums are formed in f32 in that order and are the same in
+// every run.  Text repeats its frequent tokens thousands of times, so the
+// sorted positions, not the vocabulary rows, are dealt out: a workgroup adds a
+// fixed number of consecutive positions, writes the rows that end inside its
+// share, and leaves the sums of the first and last row, where those continue
+// in a neighbour's share, to be joined by a second pass.
+//
+//   k_embed      lookup
+//   k_sort_hist  digits per share of the positions
+//   k_sort_scan  first place of every (digit, share)
+//   k_sort_move  positions to their places
+//   k_eg_fill    zero rows
+//   k_eg_sum     sums over sorted positions
+//   k_eg_join    sums of rows that cross shares
+#include <algorithm>
+
+#include "internal.h"
+#include "mm.h"
+
+namespace {
+
+inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
+
+SPEC_DEVICE int64_t load_id(const void *p, int is64, int64_t i)
+{
+    return is64 ? reinterpret_cast<const int64_t *>(p)[i] : (int64_t) reinterpret_cast<const int32_t *>(p)[i];
+}
+
+// VEC elements of type S as one memory access
+template <typename S, int VEC>
+struct __attribute__((aligned(VEC * sizeof(S)))) Pack {
+    S v[VEC];
+};
+
+// grid (column blocks, rows / RPB): a wave per row
+template <typename E, int VEC>
+__global__ __launch_bounds__(256) void k_embed(const typename E::st *__restrict__ tab, int64_t V, int64_t d, int64_t lde,
+                                               const void *__restrict__ ids, int is64, int64_t n, float scale,
+                                               typename E::st *__restrict__ Y, int64_t ldy)
+{
+    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (i >= n) return;
+    const int64_t v = load_id(ids, is64, i);
+    const bool ok = v >= 0 && v < V;
+    const typename E::st *src = tab + (ok ? v : 0) * lde;
+    typename E::st *dst = Y + i * ldy;
+    for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64) {
+        Pack<typename E::st, VEC> x{};
+        if (ok) x = *reinterpret_cast<const Pack<typename E::st, VEC> *>(src + c);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x.v[e] = ok ? E::round(scale * E::wide(x.v[e])) : (typename E::st)0;
+        *reinterpret_cast<Pack<typename E::st, VEC> *>(dst + c) = x;
+    }
+}
+
+// ------------------------------------------------------------------ sort
+
+constexpr int SORT_SHARE = 2048;  // positions per workgroup (4 waves of 8 x 64)
+constexpr int SORT_ROUNDS = SORT_SHARE / 256;
+constexpr int DIGIT_MAX = 10;
+
+// the sort key of position i: its id, or V (after every row) where it has none
+SPEC_DEVICE int first_key(const void *ids, int is64, int64_t i, int64_t V)
+{
+    const int64_t v = load_id(ids, is64, i);
+    return (int)(v >= 0 && v < V ? v : V);
+}
+
+__global__ __launch_bounds__(256) void k_sort_hist(const int *__restrict__ keys, const void *__restrict__ ids, int is64,
+                                                   int64_t V, int64_t n, int shift, int bits, int nshare,
+                                                   int *__restrict__ hist)
+{
+    __shared__ int cnt[1 << DIGIT_MAX];
+    const int nd = 1 << bits;
+    for (int i = threadIdx.x; i < nd; i += 256) cnt[i] = 0;
+    __syncthreads();
+    const int64_t b = (int64_t)blockIdx.x * SORT_SHARE;
+    for (int k = threadIdx.x; k < SORT_SHARE; k += 256)
+        if (b + k < n) {
+            const int key = keys != nullptr ? keys[b + k] : first_key(ids, is64, b + k, V);
+            atomicAdd(&cnt[(key >> shift) & (nd - 1)], 1);  // counts: the order does not matter
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nd; i += 256) hist[i * nshare + blockIdx.x] = cnt[i];
+}
+
+// exclusive sums of hist[0 .. m) by one workgroup
+__global__ __launch_bounds__(1024) void k_sort_scan(int *__restrict__ hist, int m)
+{
+    __shared__ int wsum[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (m + 1023) / 1024;
+    const int b = tid * per, e = min(m, b + per);
+    int s = 0;
+    for (int i = b; i < e; ++i) s += hist[i];
+    int inc = s;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 63) wsum[wave] = inc;
+    __syncthreads();
+    int base = inc - s;
+    for (int w = 0; w < wave; ++w) base += wsum[w];
+    for (int i = b; i < e; ++i) {
+        const int x = hist[i];
+        hist[i] = base;
+        base += x;
+    }
+}
+
+__global__ __launch_bounds__(256) void k_sort_move(const int *__restrict__ keys, const int *__restrict__ idx,
+                                                   const void *__restrict__ ids, int is64, int64_t V, int64_t n,
+                                                   int shift, int bits, int nshare, const int *__restrict__ base,
+                                                   int *__restrict__ okeys, int *__restrict__ oidx)
+{
+    __shared__ int cnt[4][1 << DIGIT_MAX];
+    const int nd = 1 << bits;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < 4 * nd; i += 256) cnt[i >> bits][i & (nd - 1)] = 0;
+    __syncthreads();
+    const int64_t b = (int64_t)blockIdx.x * SORT_SHARE + wave * (SORT_SHARE / 4);
+    int key[SORT_ROUNDS], rank[SORT_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const int64_t i = b + r * 64 + lane;
+        const bool in = i < n;
+        key[r] = !in ? 0 : (keys != nullptr ? keys[i] : first_key(ids, is64, i, V));
+        const int dg = (key[r] >> shift) & (nd - 1);
+        uint64_t same = __ballot(in);  // lanes with this lane's digit
+        for (int k = 0; k < bits; ++k) {
+            const uint64_t m = __ballot((dg >> k) & 1);
+            same &= (dg >> k) & 1 ? m : ~m;
+        }
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        rank[r] = in ? cnt[wave][dg] + before : 0;
+        wave_sync();
+        if (in && before == 0) cnt[wave][dg] += __popcll(same);
+        wave_sync();
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const int64_t i = b + r * 64 + lane;
+        if (i >= n) continue;
+        const int dg = (key[r] >> shift) & (nd - 1);
+        int at = base[dg * nshare + blockIdx.x] + rank[r];
+        for (int w = 0; w < wave; ++w) at += cnt[w][dg];
+        okeys[at] = key[r];
+        oidx[at] = idx != nullptr ? idx[i] : (int)i;
+    }
+}
+
+// ------------------------------------------------------------------ sums
+
+constexpr int EG_SHARE = 32;  // sorted positions per workgroup
+
+template <typename O, int VEC>
+__global__ __launch_bounds__(256) void k_eg_fill(typename O::st *__restrict__ dE, int64_t V, int64_t d, int64_t ldd)
+{
+    const int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (v >= V) return;
+    const Pack<typename O::st, VEC> z{};
+    for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64)
+        *reinterpret_cast<Pack<typename O::st, VEC> *>(dE + v * ldd + c) = z;
+}
+
+template <typename O, int VEC>
+SPEC_DEVICE void eg_put(typename O::st *row, int64_t c, const float (&s)[VEC], float scale, int add)
+{
+    Pack<typename O::st, VEC> x;
+    if (add) x = *reinterpret_cast<const Pack<typename O::st, VEC> *>(row + c);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x.v[e] = O::round(add ? O::wide(x.v[e]) + scale * s[e] : scale * s[e]);
+    *reinterpret_cast<Pack<typename O::st, VEC> *>(row + c) = x;
+}
+
+// grid (shares, column blocks of 256 VEC).  head[share] / tail[share]: the sum
+// of the share's first / last row where it began before / goes on after
+template <typename E, typename O, int VEC>
+__global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict__ dY, int64_t d, int64_t ldy,
+                                                const int *__restrict__ keys, const int *__restrict__ idx, int64_t n,
+                                                int64_t V, float scale, int add, typename O::st *__restrict__ dE,
+                                                int64_t ldd, float *__restrict__ head, float *__restrict__ tail)
+{
+    const int64_t b = (int64_t)blockIdx.x * EG_SHARE, e = min<int64_t>(n, b + EG_SHARE);
+    const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
+    if (c >= d) return;
+    float s[VEC];
+    bool open = b > 0 && keys[b - 1] == keys[b];  // the row began before this share
+    int64_t i = b;
+    while (i < e) {
+        const int key = keys[i];
+        if (key >= V) return;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+        for (; i < e && keys[i] == key; ++i) {
+            const Pack<typename E::st, VEC> x =
+                *reinterpret_cast<const Pack<typename E::st, VEC> *>(dY + (int64_t)idx[i] * ldy + c);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) s[k] += E::wide(x.v[k]);
+        }
+        const bool goes_on = i == e && e < n && keys[e] == key;
+        if (open || goes_on) {
+            float *p = (open ? head : tail) + (int64_t)blockIdx.x * d + c;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) p[k] = s[k];
+        } else {
+            eg_put<O, VEC>(dE + key * ldd, c, s, scale, add);
+        }
+        open = false;
+    }
+}
+
+// a row that begins in this share and goes on: its tail here and the heads after it
+template <typename O, int VEC>
+__global__ __launch_bounds__(256) void k_eg_join(int64_t d, const int *__restrict__ keys, int64_t n, int64_t V,
+                                                 float scale, int add, typename O::st *__restrict__ dE, int64_t ldd,
+                                                 const float *__restrict__ head, const float *__restrict__ tail)
+{
+    const int64_t b = (int64_t)blockIdx.x * EG_SHARE, e = b + EG_SHARE;
+    const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
+    if (c >= d || e >= n) return;
+    const int key = keys[e - 1];
+    if (key >= V || keys[e] != key) return;
+    if (keys[b] == key && b > 0 && keys[b - 1] == key) return;  // began earlier
+    float s[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[k] = tail[(int64_t)blockIdx.x * d + c + k];
+    for (int64_t f = e; f < n && keys[f] == key; f += EG_SHARE) {
+        const float *p = head + f / EG_SHARE * d + c;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] += p[k];
+    }
+    eg_put<O, VEC>(dE + key * ldd, c, s, scale, add);
+}
+
+struct EgPlan {
+    int nshare, passes, bits;
+    int64_t key[2], idx[2], hist, head, tail, total;
+};
+
+EgPlan eg_plan(int64_t n, int64_t V, int64_t d)
+{
+    EgPlan p{};
+    int kb = 1;  // bits of the largest key, V
+    while ((V >> kb) != 0) ++kb;
+    p.passes = (int)cdiv_h(kb, DIGIT_MAX);
+    p.bits = (int)cdiv_h(kb, p.passes);
+    const int64_t nn = std::max<int64_t>(n, 1);
+    p.nshare = (int)cdiv_h(nn, SORT_SHARE);
+    int64_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = o;
+        o += up_h(bytes, 256);
+        return at;
+    };
+    for (int i = 0; i < 2; ++i) {
+        p.key[i] = take(4 * nn);
+        p.idx[i] = take(4 * nn);
+    }
+    p.hist = take((int64_t)4 * p.nshare << p.bits);
+    p.head = take(4 * cdiv_h(nn, EG_SHARE) * d);
+    p.tail = take(4 * cdiv_h(nn, EG_SHARE) * d);
+    p.total = o;
+    return p;
+}
+
+template <typename E, typename O, int VEC>
+hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
+                  int is64, float scale, int add, void *dE, int64_t ldd, char *ws)
+{
+    const EgPlan p = eg_plan(n, V, d);
+    typename O::st *out = (typename O::st *)dE;
+    if (!add) {
+        hipLaunchKernelGGL((k_eg_fill<O, VEC>), dim3((unsigned)cdiv_h(V, 4)), dim3(256), 0, stream, out, V, d, ldd);
+        SPEC_LAUNCH_CHECK();
+    }
+    if (n == 0) return hipSuccess;
+    int *hist = (int *)(ws + p.hist);
+    for (int k = 0; k < p.passes; ++k) {
+        const int *keys = k == 0 ? nullptr : (const int *)(ws + p.key[(k + 1) & 1]);
+        const int *idx = k == 0 ? nullptr : (const int *)(ws + p.idx[(k + 1) & 1]);
+        hipLaunchKernelGGL(k_sort_hist, dim3((unsigned)p.nshare), dim3(256), 0, stream, keys, ids, is64, V, n, k * p.bits,
+                           p.bits, p.nshare, hist);
+        SPEC_LAUNCH_CHECK();
+        hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(1024), 0, stream, hist, p.nshare << p.bits);
+        SPEC_LAUNCH_CHECK();
+        hipLaunchKernelGGL(k_sort_move, dim3((unsigned)p.nshare), dim3(256), 0, stream, keys, idx, ids, is64, V, n,
+                           k * p.bits, p.bits, p.nshare, hist, (int *)(ws + p.key[k & 1]), (int *)(ws + p.idx[k & 1]));
+        SPEC_LAUNCH_CHECK();
+    }
+    const int *keys = (const int *)(ws + p.key[(p.passes + 1) & 1]), *idx = (const int *)(ws + p.idx[(p.passes + 1) & 1]);
+    const dim3 grid((unsigned)cdiv_h(n, EG_SHARE), (unsigned)cdiv_h(d, 256 * VEC));
+    float *head = (float *)(ws + p.head), *tail = (float *)(ws + p.tail);
+    hipLaunchKernelGGL((k_eg_sum<E, O, VEC>), grid, dim3(256), 0, stream, (const typename E::st *)dY, d, ldy, keys, idx, n,
+                       V, scale, add, out, ldd, head, tail);
+    SPEC_LAUNCH_CHECK();
+    hipLaunchKernelGGL((k_eg_join<O, VEC>), grid, dim3(256), 0, stream, d, keys, n, V, scale, add, out, ldd, head, tail);
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t embed_run(hipStream_t stream, const void *tab, int64_t V, int64_t d, int64_t lde, const void *ids, int is64,
+                     int64_t n, float scale, void *Y, int64_t ldy)
+{
+    using st = typename E::st;
+    constexpr int VEC = 16 / sizeof(st);
+    const dim3 grid((unsigned)cdiv_h(n, 4));
+    const bool vec = (uintptr_t)tab % 16 == 0 && (uintptr_t)Y % 16 == 0 && d % VEC == 0 && lde % VEC == 0 && ldy % VEC == 0;
+    if (vec)
+        hipLaunchKernelGGL((k_embed<E, VEC>), grid, dim3(256), 0, stream, (const st *)tab, V, d, lde, ids, is64, n, scale,
+                           (st *)Y, ldy);
+    else
+        hipLaunchKernelGGL((k_embed<E, 1>), grid, dim3(256), 0, stream, (const st *)tab, V, d, lde, ids, is64, n, scale,
+                           (st *)Y, ldy);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t embed_grad_workspace_bytes(int64_t n, int64_t V, int64_t d) { return (size_t)eg_plan(n, V, d).total; }
+
+hipError_t launch_embed(hipStream_t stream, const void *E, int t, int64_t V, int64_t d, int64_t lde, const void *ids,
+                        int is64, int64_t n, float scale, void *Y, int64_t ldy)
+{
+    if (n == 0) return hipSuccess;
+    return t == SPEC_BF16 ? embed_run<ElBF16>(stream, E, V, d, lde, ids, is64, n, scale, Y, ldy)
+                          : embed_run<ElF32>(stream, E, V, d, lde, ids, is64, n, scale, Y, ldy);
+}
+
+hipError_t launch_embed_grad(hipStream_t stream, const void *dY, int yt, int64_t n, int64_t V, int64_t d, int64_t ldy,
+                             const void *ids, int is64, float scale, int add, void *dE, int et, int64_t ldd, void *ws)
+{
+    const int64_t ys = yt == SPEC_BF16 ? 2 : 4, es = et == SPEC_BF16 ? 2 : 4;
+    char *w = (char *)ws;
+    // four elements per thread where both sides allow it
+    const bool vec = d % 4 == 0 && ldy % 4 == 0 && ldd % 4 == 0 && (uintptr_t)dY % (4 * ys) == 0 &&
+                     (uintptr_t)dE % (4 * es) == 0;
+    if (yt == SPEC_BF16 && et == SPEC_BF16)
+        return vec ? eg_run<ElBF16, ElBF16, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+                   : eg_run<ElBF16, ElBF16, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+    if (yt == SPEC_BF16)
+        return vec ? eg_run<ElBF16, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+                   : eg_run<ElBF16, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+    return vec ? eg_run<ElF32, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+               : eg_run<ElF32, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+}

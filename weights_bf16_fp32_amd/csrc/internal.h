@@ -74,6 +74,36 @@ size_t project_weight_workspace_bytes(int64_t d);
 hipError_t launch_project_weight(hipStream_t stream, const void *W, int wt, int64_t d, int64_t ldw, const float *P,
                                  int64_t ldp, int k, float *Wp, int64_t ldo, float *X, int64_t ldx, void *ws);
 
+hipError_t launch_embed(hipStream_t stream, const void *E, int t, int64_t V, int64_t d, int64_t lde, const void *ids,
+                        int is64, int64_t n, float scale, void *Y, int64_t ldy);
+
+size_t embed_grad_workspace_bytes(int64_t n, int64_t V, int64_t d);
+
+// add: onto the rows present; else all rows are written
+hipError_t launch_embed_grad(hipStream_t stream, const void *dY, int yt, int64_t n, int64_t V, int64_t d, int64_t ldy,
+                             const void *ids, int is64, float scale, int add, void *dE, int et, int64_t ldd, void *ws);
+
+size_t linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t d, int t);
+size_t linear_xent_grad_workspace_bytes(int64_t T, int64_t V, int64_t d, int t);
+
+hipError_t launch_linear_xent(hipStream_t stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d,
+                              int64_t ldh, int64_t ldw, const void *target, int is64, float scale, float *loss,
+                              float *lse, void *ws);
+
+hipError_t launch_linear_xent_grad(hipStream_t stream, const void *H, const void *W, int t, int64_t T, int64_t V,
+                                   int64_t d, int64_t ldh, int64_t ldw, const void *target, int is64, float scale,
+                                   const float *lse, const float *dloss, void *dH, int64_t lddh, void *dW, int64_t lddw,
+                                   float beta, void *ws);
+
+size_t orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int t);
+
+// whether f16 holds the iterates of these coefficients
+bool orthogonalize_bounded(const double *coeffs, int steps);
+
+hipError_t launch_orthogonalize(hipStream_t stream, const void *G, int t, int64_t batch, int64_t m, int64_t n,
+                                int64_t ldg, int64_t sg, const double *coeffs, int steps, double eps, double scale,
+                                void *O, int64_t ldo, int64_t so, void *ws);
+
 // Kernel timing brackets (timing.cpp): ktimer_begin returns a slot (or -1 when
 // the kernel is not being timed); ktimer_end records the matching end event.
 int ktimer_begin(hipStream_t stream, int id);

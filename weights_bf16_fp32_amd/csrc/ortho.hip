@@ -1,0 +1,416 @@
+// Orthogonalisation of an update by Newton-Schulz products, gfx950.
+//
+//   X_0 = G / (|G|_F + eps);  A = X X^T,  X <- a X + (b A + c A^2) X  per step;  O = scale X
+//
+// (on the shorter side: for m > n the Gram matrix is X^T X and the factor acts
+// from the right).  One step multiplies every singular value s by
+// a + b s^2 + c s^4, so all of them move towards one and the singular vectors
+// stay.
+//
+// Arithmetic for bf16 updates: f16 operands on MFMA (the iterates are bounded,
+// so f16's range suffices with powers of two as scales, and its eight times
+// finer rounding costs nothing), f32 accumulation.  Two things keep the
+// rounding of an operand from being amplified by the later steps (a small
+// singular value grows by up to a per step, and an error in its direction with
+// it):
+//   - X is kept as the sum of two f16 numbers (22 bits).  The products take the
+//     leading one; the term a X, the only one that small singular values live
+//     on, takes both.
+//   - A = D + E and b A + c A^2 = D' + E' are kept as an f32 diagonal and an f16
+//     off-diagonal part.  When X is nearly orthogonal A is nearly diagonal, so
+//     what is rounded is small:
+//       B_ij = (b + c (d_i + d_j)) E_ij + c (E E)_ij,  B_ii = b d_i + c (d_i^2 + (E E)_ii)
+//       X_i <- (a + B_ii) X_i + sum_k E'_ik X_k
+// f32 updates run the same products on f32 MFMA.
+//
+// A and B are symmetric: only tiles on and below the diagonal are computed, and
+// each is written to both places.
+//
+//   k_ns_norm   partial sums of squares (f64)
+//   k_ns_load   X_0
+//   k_ns_gram   A and its diagonal
+//   k_ns_poly   B and its diagonal
+//   k_ns_apply  the next X, or O
+#include <algorithm>
+#include <math.h>
+
+#include "internal.h"
+#include "mm.h"
+
+namespace {
+
+inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
+
+constexpr int NORM_BLOCKS = 64;  // partial sums of squares per matrix
+
+#define MM_STAGES(M)                                                                                           \
+    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]
+
+struct Cfg128 {
+    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
+};
+
+template <typename E, typename C, bool PS, bool QS>
+using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
+
+// grid (NORM_BLOCKS, batch)
+template <typename G>
+__global__ __launch_bounds__(256) void k_ns_norm(const typename G::st *__restrict__ X, int64_t m, int64_t n, int64_t ld,
+                                                 int64_t stride, double *__restrict__ part)
+{
+    __shared__ double red[4];
+    const typename G::st *x = X + blockIdx.y * stride;
+    double s = 0.0;
+    for (int64_t i = blockIdx.x; i < m; i += NORM_BLOCKS)
+        for (int64_t j = threadIdx.x; j < n; j += 256) {
+            const double v = (double)G::wide(x[i * ld + j]);
+            s += v * v;
+        }
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) part[(int64_t)blockIdx.y * NORM_BLOCKS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+}
+
+// X as the kernels hold it: leading part and, for f16, the rest
+template <typename E>
+SPEC_DEVICE void put_x(typename E::st *hi, typename E::st *lo, int64_t at, const float (&v)[4])
+{
+    Vec4<E> h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h.v[e] = E::round(v[e]);
+        if (sizeof(typename E::st) == 2) l.v[e] = E::round(v[e] - E::wide(h.v[e]));
+    }
+    *reinterpret_cast<Vec4<E> *>(hi + at) = h;
+    if (sizeof(typename E::st) == 2) *reinterpret_cast<Vec4<E> *>(lo + at) = l;
+}
+
+template <typename E>
+SPEC_DEVICE void get_x(const typename E::st *hi, const typename E::st *lo, int64_t at, float (&v)[4])
+{
+    const Vec4<E> h = *reinterpret_cast<const Vec4<E> *>(hi + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = E::wide(h.v[e]);
+    if (sizeof(typename E::st) == 2) {
+        const Vec4<E> l = *reinterpret_cast<const Vec4<E> *>(lo + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += E::wide(l.v[e]);
+    }
+}
+
+// X = G * sx / (norm + eps), padding columns zero.  grid (rows, batch)
+template <typename G, typename E>
+__global__ __launch_bounds__(256) void k_ns_load(const typename G::st *__restrict__ X, int64_t n, int64_t ld,
+                                                 int64_t stride, const double *__restrict__ part, double eps, float sx,
+                                                 typename E::st *__restrict__ hi, typename E::st *__restrict__ lo,
+                                                 int64_t xp, int64_t xs)
+{
+    double s = part[(int64_t)blockIdx.y * NORM_BLOCKS + (threadIdx.x & 63)];
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    const float inv = (float)((double)sx / (sqrt(s) + eps));
+    const int64_t i = blockIdx.x;
+    const typename G::st *x = X + blockIdx.y * stride + i * ld;
+    for (int64_t j = 4 * threadIdx.x; j < xp; j += 1024) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = j + e < n ? G::wide(x[j + e]) * inv : 0.f;
+        put_x<E>(hi, lo, blockIdx.y * xs + i * xp + j, v);
+    }
+}
+
+// One matrix of the batch: X (rows x cols at pitch xp), the r x r matrices at pitch ap.
+struct NsDims {
+    int64_t rows, cols, xp, xs;  // X
+    int64_t r, ap, as;           // A, B
+    int nt;                      // tiles per side of A
+};
+
+// stores four entries (row i, columns j..j+3) of a symmetric matrix with zero
+// diagonal, mirrored for tiles below the diagonal; di receives the diagonal
+template <typename E>
+SPEC_DEVICE void put_sym(typename E::st *A, float *diag, const NsDims &D, int64_t i, int64_t j, bool below,
+                         const float (&v)[4], float scale)
+{
+    Vec4<E> o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (!below && i == j + e && i < D.r) diag[i] = v[e];
+        o.v[e] = !below && i == j + e ? (typename E::st)0 : E::round(v[e] * scale);
+    }
+    if (i < D.r && j < D.ap) *reinterpret_cast<Vec4<E> *>(A + i * D.ap + j) = o;
+    if (below && i < D.ap) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[(j + e) * D.ap + i] = o.v[e];
+    }
+}
+
+// grid (tiles on and below the diagonal, batch).  real: 1 / sx^2
+template <typename E, typename C, bool TALL>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_gram(const typename E::st *__restrict__ X, NsDims D,
+                                                                    float real, float sa,
+                                                                    typename E::st *__restrict__ A,
+                                                                    float *__restrict__ diag)
+{
+    using M = MmOf<E, C, TALL, TALL>;
+    MM_STAGES(M);
+    int ti, tj;
+    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), D.nt, ti, tj);
+    const int64_t i0 = (int64_t)ti * C::BQ, j0 = (int64_t)tj * C::BP;
+    const typename E::st *x = X + blockIdx.y * D.xs;
+    const int64_t step = TALL ? 1 : D.xp, K = TALL ? D.rows : round_up(D.cols, M::EPC);
+    const MmSrc P{(const char *)(x + j0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
+    const MmSrc Q{(const char *)(x + i0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
+    M mm;
+    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.each4([&](int p, int q, float (&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= real;
+        put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i0 + q, j0 + p, ti != tj, v, sa);
+    });
+}
+
+// B = b A + c A^2 with A = diag(da) + E; ea = 1 / sa
+template <typename E, typename C>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_poly(const typename E::st *__restrict__ A,
+                                                                    const float *__restrict__ da, NsDims D, float b,
+                                                                    float c, float ea, float sb,
+                                                                    typename E::st *__restrict__ B,
+                                                                    float *__restrict__ diag)
+{
+    using M = MmOf<E, C, false, false>;
+    MM_STAGES(M);
+    int ti, tj;
+    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), D.nt, ti, tj);
+    const int64_t i0 = (int64_t)ti * C::BQ, j0 = (int64_t)tj * C::BP;
+    const typename E::st *a = A + blockIdx.y * D.as;
+    const float *d = da + blockIdx.y * D.r;
+    const int64_t K = round_up(D.r, M::EPC);
+    const MmSrc P{(const char *)(a + j0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
+    const MmSrc Q{(const char *)(a + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
+    M mm;
+    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.each4([&](int p, int q, float (&v)[4]) {
+        const int64_t i = i0 + q, j = j0 + p;
+        if (i < D.r && j < D.ap) {
+            const float di = d[i];
+            const Vec4<E> x = *reinterpret_cast<const Vec4<E> *>(a + i * D.ap + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float dj = j + e < D.r ? d[j + e] : 0.f;
+                const float aa = c * (v[e] * ea * ea);
+                v[e] = i == j + e ? b * di + (c * di * di + aa) : (b + c * (di + dj)) * (E::wide(x.v[e]) * ea) + aa;
+            }
+        }
+        put_sym<E>(B + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti != tj, v, sb);
+    });
+}
+
+// The next X (scaled by sx1), or O = scale X in the last step.
+// ex = 1 / sx of the current X, eb = 1 / sb.
+template <typename E, typename C, bool TALL, typename O, bool LAST>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_apply(
+    const typename E::st *__restrict__ hi, const typename E::st *__restrict__ lo, const typename E::st *__restrict__ B,
+    const float *__restrict__ db, NsDims D, int np, int nq, float a, float ex, float eb, float sx1,
+    typename E::st *__restrict__ hi1, typename E::st *__restrict__ lo1, typename O::st *__restrict__ out, int64_t ldo,
+    int64_t os, int vec)
+{
+    using M = MmOf<E, C, !TALL, false>;
+    MM_STAGES(M);
+    int tp, tq;
+    mm_tile(blockIdx.x, np, nq, tp, tq);
+    const int64_t j0 = (int64_t)tp * C::BP, i0 = (int64_t)tq * C::BQ;
+    const int64_t xb = blockIdx.y * D.xs;
+    const typename E::st *bm = B + blockIdx.y * D.as;
+    const float *d = db + blockIdx.y * D.r;
+    const int64_t K = round_up(D.r, M::EPC);
+    MmSrc P, Q;
+    if (TALL) {  // rows of B (symmetric) against rows of X
+        P = MmSrc{(const char *)(bm + j0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
+        Q = MmSrc{(const char *)(hi + xb + i0 * D.xp), D.xp * M::SZ, (int)min<int64_t>(C::BQ, D.rows - i0), K};
+    } else {  // columns of X against rows of B
+        P = MmSrc{(const char *)(hi + xb + j0), D.xp * M::SZ, (int)min<int64_t>(C::BP, D.cols - j0), D.r};
+        Q = MmSrc{(const char *)(bm + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
+    }
+    M mm;
+    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.each4([&](int p, int q, float (&v)[4]) {
+        const int64_t i = i0 + q, j = j0 + p;
+        if (i >= D.rows || j >= D.xp) return;
+        float x[4];
+        get_x<E>(hi, lo, xb + i * D.xp + j, x);
+        const float di = TALL ? 0.f : d[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = a + (TALL ? (j + e < D.cols ? d[j + e] : 0.f) : di);
+            v[e] = (f * x[e] + eb * v[e]) * ex * sx1;
+        }
+        if (!LAST) {
+            put_x<E>(hi1, lo1, xb + i * D.xp + j, v);
+        } else {
+            typename O::st *o = out + blockIdx.y * os + i * ldo + j;
+            if (vec && j + 4 <= D.cols) {
+                Vec4<O> r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.v[e] = O::round(v[e]);
+                *reinterpret_cast<Vec4<O> *>(o) = r;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < D.cols) o[e] = O::round(v[e]);
+            }
+        }
+    });
+}
+
+struct NsPlan {
+    NsDims D;
+    int64_t part, da, db, a, b, x[2], xl[2], total;
+};
+
+NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int t)
+{
+    NsPlan p{};
+    const int64_t es = t == SPEC_BF16 ? 2 : 4;
+    NsDims &D = p.D;
+    D.rows = m;
+    D.cols = n;
+    D.xp = up_h(n, 64);
+    D.xs = D.rows * D.xp;
+    D.r = std::min(m, n);
+    D.ap = up_h(D.r, 64);
+    D.as = D.r * D.ap;
+    int64_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = o;
+        o += up_h(bytes, 256);
+        return at;
+    };
+    p.part = take(8 * batch * NORM_BLOCKS);
+    p.da = take(4 * batch * D.r);
+    p.db = take(4 * batch * D.r);
+    p.a = take(es * batch * D.as);
+    p.b = take(es * batch * D.as);
+    for (int i = 0; i < 2; ++i) {
+        p.x[i] = take(es * batch * D.xs);
+        p.xl[i] = es == 2 ? take(2 * batch * D.xs) : 0;
+    }
+    p.total = o;
+    return p;
+}
+
+// largest |s (a + b s^2 + c s^4)| over 0 <= s <= top: at the end or at a root
+// of a + 3 b u + 5 c u^2, u = s^2
+double step_bound(const double *co, double top)
+{
+    const double a = co[0], b = co[1], c = co[2];
+    auto f = [&](double s) { return fabs(s * (a + s * s * (b + c * s * s))); };
+    double best = f(top);
+    double u[2];
+    int nu = 0;
+    if (c != 0.0) {
+        const double q = 9.0 * b * b - 20.0 * a * c;
+        if (q >= 0.0) {
+            u[nu++] = (-3.0 * b + sqrt(q)) / (10.0 * c);
+            u[nu++] = (-3.0 * b - sqrt(q)) / (10.0 * c);
+        }
+    } else if (b != 0.0) {
+        u[nu++] = -a / (3.0 * b);
+    }
+    for (int k = 0; k < nu; ++k)
+        if (u[k] > 0.0 && u[k] < top * top) best = std::max(best, f(sqrt(u[k])));
+    return best;
+}
+
+// the power of two that takes `bound` to at most 2^14 (f16 holds 65504), at most `most`
+double scale16(double bound, double most)
+{
+    return std::min(most, exp2(floor(14.0 - log2(std::max(bound, 1e-300)))));
+}
+
+template <typename GT, typename E, bool TALL>
+hipError_t ns_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
+                  const double *co, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so, char *ws)
+{
+    using C = Cfg128;
+    using st = typename E::st;
+    using gst = typename GT::st;
+    constexpr bool F16 = sizeof(st) == 2;
+    NsPlan pl = ns_plan(batch, m, n, F16 ? SPEC_BF16 : SPEC_F32);
+    NsDims &D = pl.D;
+    D.nt = (int)cdiv_h(D.r, C::BP);
+    double *part = (double *)(ws + pl.part);
+    float *da = (float *)(ws + pl.da), *db = (float *)(ws + pl.db);
+    st *A = (st *)(ws + pl.a), *B = (st *)(ws + pl.b);
+    // entries of X are about 1 / sqrt(m n) at first and at most the largest singular value
+    const double want = exp2(floor(0.5 * log2((double)m * (double)n)));
+    double top = 1.0, sx = F16 ? scale16(1.0, want) : 1.0;
+    hipLaunchKernelGGL(k_ns_norm<GT>, dim3(NORM_BLOCKS, (unsigned)batch), dim3(256), 0, stream, (const gst *)G, m, n, ldg,
+                       sg, part);
+    SPEC_LAUNCH_CHECK();
+    hipLaunchKernelGGL((k_ns_load<GT, E>), dim3((unsigned)m, (unsigned)batch), dim3(256), 0, stream, (const gst *)G, n, ldg,
+                       sg, part, eps, (float)sx, (st *)(ws + pl.x[0]), (st *)(ws + pl.xl[0]), D.xp, D.xs);
+    SPEC_LAUNCH_CHECK();
+    const int tri = D.nt * (D.nt + 1) / 2, np = (int)cdiv_h(n, C::BP), nq = (int)cdiv_h(m, C::BQ);
+    const dim3 blk(64 * C::WP * C::WQ), gt((unsigned)tri, (unsigned)batch), ga((unsigned)((int64_t)np * nq), (unsigned)batch);
+    const int vec = (uintptr_t)O % (4 * sizeof(gst)) == 0 && ldo % 4 == 0 && so % 4 == 0;
+    for (int k = 0; k < steps; ++k) {
+        const double *c = co + 3 * k;
+        const double na = top * top, nb = fabs(c[1]) * na + fabs(c[2]) * na * na;
+        const double sa = F16 ? scale16(na, 16384.0) : 1.0, sb = F16 ? scale16(nb, 16384.0) : 1.0;
+        const double next = 1.02 * step_bound(c, top);
+        const bool last = k == steps - 1;
+        const double sx1 = last ? scale : (F16 ? scale16(next, want) : 1.0);
+        const st *hi = (const st *)(ws + pl.x[k & 1]), *lo = (const st *)(ws + pl.xl[k & 1]);
+        st *hi1 = (st *)(ws + pl.x[(k & 1) ^ 1]), *lo1 = (st *)(ws + pl.xl[(k & 1) ^ 1]);
+        hipLaunchKernelGGL((k_ns_gram<E, C, TALL>), gt, blk, 0, stream, hi, D, (float)(1.0 / (sx * sx)), (float)sa, A, da);
+        SPEC_LAUNCH_CHECK();
+        hipLaunchKernelGGL((k_ns_poly<E, C>), gt, blk, 0, stream, A, da, D, (float)c[1], (float)c[2], (float)(1.0 / sa),
+                           (float)sb, B, db);
+        SPEC_LAUNCH_CHECK();
+        if (last)
+            hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, true>), ga, blk, 0, stream, hi, lo, B, db, D, np, nq,
+                               (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O, ldo, so,
+                               vec);
+        else
+            hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, false>), ga, blk, 0, stream, hi, lo, B, db, D, np, nq,
+                               (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O, ldo, so,
+                               vec);
+        SPEC_LAUNCH_CHECK();
+        top = next;
+        sx = sx1;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+size_t orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int t)
+{
+    return (size_t)ns_plan(batch, m, n, t).total;
+}
+
+// whether the iterates stay within f16's range: their bounds reach at most 2^7
+bool orthogonalize_bounded(const double *co, int steps)
+{
+    double top = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const double na = top * top;
+        if (!(na <= 16384.0 && fabs(co[3 * k + 1]) * na + fabs(co[3 * k + 2]) * na * na <= 16384.0)) return false;
+        top = 1.02 * step_bound(co + 3 * k, top);
+    }
+    return top <= 16384.0;
+}
+
+hipError_t launch_orthogonalize(hipStream_t stream, const void *G, int t, int64_t batch, int64_t m, int64_t n,
+                                int64_t ldg, int64_t sg, const double *co, int steps, double eps, double scale, void *O,
+                                int64_t ldo, int64_t so, void *ws)
+{
+    char *w = (char *)ws;
+    if (t == SPEC_BF16)
+        return m > n ? ns_run<ElBF16, ElF16, true>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w)
+                     : ns_run<ElBF16, ElF16, false>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w);
+    return m > n ? ns_run<ElF32, ElF32, true>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w)
+                 : ns_run<ElF32, ElF32, false>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w);
+}

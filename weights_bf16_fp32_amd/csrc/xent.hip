@@ -1,0 +1,553 @@
+// Softmax cross entropy of a linear head over a large vocabulary, gfx950:
+//
+//   z_tv = scale <h_t, w_v>,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target
+//   g_tv = scale dloss_t (exp(z_tv - lse_t) - [v = target_t]),  dH = G W,  dW = beta dW + G^T H
+//
+// The T x V logits are never stored.  Forward: every 128 x 128 tile of logits is
+// reduced to one (maximum, sum of exponentials) per row while it is in the
+// accumulators, and the tiles' pairs are joined per row.  Backward: a piece of
+// the vocabulary at a time, the logits are formed again and leave as the bf16 (f32)
+// gradient G of that piece, which the two gradient products read back.
+//
+// Rows without a target (outside [0, V)) are dropped before the products: the
+// rest of H is packed, so they cost nothing, and whatever they hold (NaN
+// included) reaches no output.
+//
+//   k_xent_pack      positions of the rows with a target, their rows of H, packed
+//   k_xent_wpack     a piece of W with 16-byte rows (only where W has none)
+//   k_xent_fwd       logits tile -> (max, sum) per row, the target's logit
+//   k_xent_join      lse and loss of every row
+//   k_xent_g         logits tile -> G tile
+//   k_xent_dw        dW of the piece
+//   k_xent_dh        partial dH of the piece (f32, by split)
+//   k_xent_dh_out    dH from the partials, zero rows for rows without a target
+#include <algorithm>
+
+#include "internal.h"
+#include "mm.h"
+
+namespace {
+
+inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
+
+SPEC_DEVICE int64_t load_id(const void *p, int is64, int64_t i)
+{
+    return is64 ? reinterpret_cast<const int64_t *>(p)[i] : (int64_t) reinterpret_cast<const int32_t *>(p)[i];
+}
+
+constexpr int PACK_ROWS = 32;  // rows per workgroup of k_xent_pack
+
+// 16-byte chunks of a row: a full one where both ends are aligned, else by element
+template <typename S>
+SPEC_DEVICE void copy_row(const S *__restrict__ src, S *__restrict__ dst, int64_t d, int64_t dp, bool vec, int lane,
+                          int lanes)
+{
+    constexpr int EPC = 16 / (int)sizeof(S);
+    if (vec) {
+        for (int64_t c = lane; c < dp / EPC; c += lanes)
+            reinterpret_cast<uint4 *>(dst)[c] = reinterpret_cast<const uint4 *>(src)[c];
+    } else {
+        for (int64_t c = lane; c < dp; c += lanes) dst[c] = c < d ? src[c] : (S)0;
+    }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restrict__ H, int64_t ldh, int64_t d,
+                                                   int64_t dp, int vec, const void *__restrict__ target, int is64,
+                                                   int64_t T, int64_t V, typename E::st *__restrict__ Hp,
+                                                   int *__restrict__ pos, int *__restrict__ ptgt,
+                                                   const float *__restrict__ lse, const float *__restrict__ dloss,
+                                                   float *__restrict__ plse, float *__restrict__ pdl,
+                                                   int *__restrict__ nvalid)
+{
+    __shared__ int cnt[4], where[PACK_ROWS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t t0 = (int64_t)blockIdx.x * PACK_ROWS;
+    int before = 0;  // rows with a target before this block's
+    for (int64_t t = tid; t < t0; t += 256) {
+        const int64_t y = load_id(target, is64, t);
+        before += y >= 0 && y < V;
+    }
+    for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
+    if (lane == 0) cnt[wave] = before;
+    __syncthreads();
+    before = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+    if (wave == 0) {
+        const int64_t t = t0 + lane;
+        const bool in = lane < PACK_ROWS && t < T;
+        const int64_t y = in ? load_id(target, is64, t) : -1;
+        const bool ok = y >= 0 && y < V;
+        const uint64_t m = __ballot(ok);
+        const int p = before + __popcll(m & ((1ull << lane) - 1));
+        if (lane < PACK_ROWS) where[lane] = ok ? p : -1;
+        if (in) pos[t] = ok ? p : -1;
+        if (ok) {
+            ptgt[p] = (int)y;
+            if (lse != nullptr) {
+                plse[p] = lse[t];
+                pdl[p] = dloss[t];
+            }
+        }
+        if (lane == 0 && t0 + PACK_ROWS >= T) *nvalid = before + __popcll(m);
+    }
+    __syncthreads();
+    for (int r = wave; r < PACK_ROWS; r += 4) {
+        const int p = where[r];
+        if (p >= 0) copy_row(H + (t0 + r) * ldh, Hp + (int64_t)p * dp, d, dp, vec != 0, lane, 64);
+    }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void k_xent_wpack(const typename E::st *__restrict__ W, int64_t ldw, int64_t d,
+                                                    int64_t dp, int64_t rows, typename E::st *__restrict__ Wp)
+{
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r < rows) copy_row(W + r * ldw, Wp + r * dp, d, dp, false, threadIdx.x & 63, 64);
+}
+
+// two LDS stages of both operands
+#define MM_STAGES(M)                                                                                           \
+    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]
+
+struct Cfg128 {
+    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
+};
+
+template <typename E, typename C, bool PS, bool QS>
+using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
+
+// The logits of vocabulary rows [tile] (P) and packed tokens (Q).
+template <typename M, typename E>
+SPEC_DEVICE void logits(M &mm, const typename E::st *W, int64_t ldw, int64_t vn, const typename E::st *Hp, int64_t dp,
+                        int n, int64_t d, int64_t v0, int t0, char *sp0, char *sp1, char *sq0, char *sq1, int BP,
+                        int BQ)
+{
+    constexpr int SZ = M::SZ;
+    const MmSrc P{(const char *)(W + v0 * ldw), ldw * SZ, (int)min<int64_t>(BP, vn - v0), d};
+    const MmSrc Q{(const char *)(Hp + (int64_t)t0 * dp), dp * SZ, min(BQ, n - t0), d};
+    mm.run(P, Q, 0, d, sp0, sp1, sq0, sq1);
+}
+
+// grid: tiles of [vn vocabulary rows] x [T tokens]; W's rows are vocabulary
+// entries vbase .. vbase + vn - 1.  part[t][tile0 + tp] = (max, sum exp(z - max)).
+// dk: d rounded up to 16 bytes (the padding of both operands is zero).
+template <typename E, typename C>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_fwd(const typename E::st *__restrict__ W, int64_t ldw,
+                                                                  int64_t vn, int64_t vbase,
+                                                                  const typename E::st *__restrict__ Hp, int64_t dp,
+                                                                  int64_t dk, const int *__restrict__ nvalid, int np,
+                                                                  int nq, float scale, const int *__restrict__ ptgt,
+                                                                  float *__restrict__ ztgt, float2 *__restrict__ part,
+                                                                  int64_t ldpart, int tile0)
+{
+    using M = MmOf<E, C, false, false>;
+    MM_STAGES(M);
+    __shared__ float2 red[C::WP][C::BQ];
+    int tp, tq;
+    mm_tile(blockIdx.x, np, nq, tp, tq);
+    const int n = *nvalid, t0 = tq * C::BQ;
+    if (t0 >= n) return;
+    const int64_t v0 = (int64_t)tp * C::BP;
+    M mm;
+    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, sp0, sp1, sq0, sq1, C::BP, C::BQ);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wp = wave % C::WP;
+    const int p0 = wp * (C::BP / C::WP) + 4 * (lane >> 5), q0 = (wave / C::WP) * (C::BQ / C::WQ) + (lane & 31);
+    const int lim = (int)min<int64_t>(C::BP, vn - v0);
+#pragma unroll
+    for (int b = 0; b < M::NI; ++b) {
+        const int q = q0 + 32 * b;
+        const bool in = t0 + q < n;
+        const int64_t y = in ? (int64_t)ptgt[t0 + q] - vbase - v0 : -1;  // the target's place in this tile
+        float top = -INFINITY;
+#pragma unroll
+        for (int m = 0; m < M::MI; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int p = p0 + 32 * m + 8 * (e >> 2) + (e & 3);
+                const float z = p < lim ? scale * mm.acc[m][b][e] : -INFINITY;
+                mm.acc[m][b][e] = z;
+                top = fmaxf(top, z);
+                if (p == y && p < lim) ztgt[t0 + q] = z;
+            }
+        {
+            float a = top, c = top;
+            halfswap32(a, c);
+            top = fmaxf(a, c);
+        }
+        // a tile without a finite logit sums to zero (or to NaN with NaN or +inf in it)
+        const float ref = top == -INFINITY ? 0.f : top;
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < M::MI; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s += __expf(mm.acc[m][b][e] - ref);
+        s = pair32_sum(s);
+        if (lane < 32) red[wp][q] = make_float2(top, s);
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < C::BQ; q += 64 * C::WP * C::WQ) {
+        if (t0 + q >= n) break;
+        float2 r = red[0][q];
+#pragma unroll
+        for (int w = 1; w < C::WP; ++w) {
+            const float2 o = red[w][q];
+            const float top = fmaxf(r.x, o.x), ref = top == -INFINITY ? 0.f : top;
+            r.y = r.y * __expf(r.x - ref) + o.y * __expf(o.x - ref);
+            r.x = top;
+        }
+        part[(int64_t)(t0 + q) * ldpart + tile0 + tp] = r;
+    }
+}
+
+// one wave per row: the row's lse from its tiles' (max, sum) and its loss
+__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int64_t ldpart, int ntile,
+                                                   const int *__restrict__ pos, const float *__restrict__ ztgt,
+                                                   int64_t T, float *__restrict__ loss, float *__restrict__ lse)
+{
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (t >= T) return;
+    const int p = pos[t];
+    if (p < 0) {
+        if (lane == 0) loss[t] = lse[t] = 0.f;
+        return;
+    }
+    const float2 *r = part + (int64_t)p * ldpart;
+    float top = -INFINITY, s = 0.f;
+    for (int i = lane; i < ntile; i += 64) {
+        const float2 o = r[i];
+        const float m = fmaxf(top, o.x), ref = m == -INFINITY ? 0.f : m;
+        s = s * __expf(top - ref) + o.y * __expf(o.x - ref);
+        top = m;
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+        const float ot = __shfl_xor(top, o), os = __shfl_xor(s, o);
+        const float m = fmaxf(top, ot), ref = m == -INFINITY ? 0.f : m;
+        s = s * __expf(top - ref) + os * __expf(ot - ref);
+        top = m;
+    }
+    if (lane == 0) {
+        const float l = top == -INFINITY ? NAN : top + logf(s);  // no finite logit: as 0 / 0
+        lse[t] = l;
+        loss[t] = l - ztgt[p];
+    }
+}
+
+// G[t][v - vbase], columns up to vn rounded up to 16 bytes (zero past vn)
+template <typename E, typename C>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_g(const typename E::st *__restrict__ W, int64_t ldw,
+                                                                int64_t vn, int64_t vbase,
+                                                                const typename E::st *__restrict__ Hp, int64_t dp,
+                                                                int64_t dk, const int *__restrict__ nvalid, int np,
+                                                                int nq, float scale, const int *__restrict__ ptgt,
+                                                                const float *__restrict__ plse,
+                                                                const float *__restrict__ pdl,
+                                                                typename E::st *__restrict__ G, int64_t ldg)
+{
+    using M = MmOf<E, C, false, false>;
+    MM_STAGES(M);
+    int tp, tq;
+    mm_tile(blockIdx.x, np, nq, tp, tq);
+    const int n = *nvalid, t0 = tq * C::BQ;
+    if (t0 >= n) return;
+    const int64_t v0 = (int64_t)tp * C::BP;
+    M mm;
+    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, sp0, sp1, sq0, sq1, C::BP, C::BQ);
+    const int lim = (int)min<int64_t>(C::BP, vn - v0);
+    const int lim4 = (int)min<int64_t>(C::BP, round_up(vn, M::EPC) - v0);
+    mm.each4([&](int p, int q, float (&v)[4]) {
+        if (t0 + q >= n || p >= lim4) return;
+        const int64_t y = (int64_t)ptgt[t0 + q] - vbase - v0;
+        const float l = plse[t0 + q], w = pdl[t0 + q] * scale;
+        Vec4<E> o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o.v[e] = E::round(p + e < lim ? (__expf(scale * v[e] - l) - (p + e == y ? 1.f : 0.f)) * w : 0.f);
+        *reinterpret_cast<Vec4<E> *>(G + (int64_t)(t0 + q) * ldg + v0 + p) = o;
+    });
+}
+
+// dW rows v (Q) by columns of d (P): sum over tokens of H[t][p] G[t][q]
+template <typename E, typename C>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dw(const typename E::st *__restrict__ Hp, int64_t dp,
+                                                                 const typename E::st *__restrict__ G, int64_t ldg,
+                                                                 int64_t vn, int64_t d, const int *__restrict__ nvalid,
+                                                                 int np, int nq, typename E::st *__restrict__ dW,
+                                                                 int64_t lddw, float beta, int vec)
+{
+    using M = MmOf<E, C, true, true>;
+    MM_STAGES(M);
+    int tp, tq;
+    mm_tile(blockIdx.x, np, nq, tp, tq);
+    const int64_t n = *nvalid, p0 = (int64_t)tp * C::BP, v0 = (int64_t)tq * C::BQ;
+    const MmSrc P{(const char *)(Hp + p0), dp * M::SZ, (int)min<int64_t>(C::BP, d - p0), n};
+    const MmSrc Q{(const char *)(G + v0), ldg * M::SZ, (int)min<int64_t>(C::BQ, vn - v0), n};
+    M mm;
+    mm.run(P, Q, 0, n, sp0, sp1, sq0, sq1);
+    mm.each4([&](int p, int q, float (&v)[4]) {
+        if (q >= Q.lim || p >= P.lim) return;
+        typename E::st *o = dW + (v0 + q) * lddw + p0 + p;
+        if (vec && p + 4 <= P.lim) {
+            Vec4<E> r;
+            if (beta != 0.f) r = *reinterpret_cast<const Vec4<E> *>(o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.v[e] = E::round(beta != 0.f ? v[e] + beta * E::wide(r.v[e]) : v[e]);
+            *reinterpret_cast<Vec4<E> *>(o) = r;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p + e < P.lim) o[e] = E::round(beta != 0.f ? v[e] + beta * E::wide(o[e]) : v[e]);
+        }
+    });
+}
+
+// part[split][t][p] (+)= sum over the split's share of the piece of W[v][p] G[t][v]
+template <typename E, typename C>
+__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dh(const typename E::st *__restrict__ W, int64_t ldw,
+                                                                 const typename E::st *__restrict__ G, int64_t ldg,
+                                                                 int64_t vn, int64_t per, int64_t d, int64_t T,
+                                                                 const int *__restrict__ nvalid, int np, int nq,
+                                                                 float *__restrict__ part, int64_t ldp, int first)
+{
+    using M = MmOf<E, C, true, false>;
+    MM_STAGES(M);
+    int tp, tq;
+    const int64_t tiles = (int64_t)np * nq;
+    const int split = (int)(blockIdx.x / tiles);
+    mm_tile(blockIdx.x % tiles, np, nq, tp, tq);
+    const int n = *nvalid, t0 = tq * C::BQ;
+    if (t0 >= n) return;
+    const int64_t p0 = (int64_t)tp * C::BP, kb = split * per, ke = min<int64_t>(vn, kb + per);
+    const MmSrc P{(const char *)(W + p0), ldw * M::SZ, (int)min<int64_t>(C::BP, d - p0), ke};
+    const MmSrc Q{(const char *)(G + (int64_t)t0 * ldg), ldg * M::SZ, min(C::BQ, n - t0), round_up(ke, M::EPC)};
+    M mm;
+    mm.run(P, Q, kb, ke, sp0, sp1, sq0, sq1);
+    float *out = part + ((int64_t)split * T + t0) * ldp + p0;
+    mm.each4([&](int p, int q, float (&v)[4]) {
+        if (q >= Q.lim || p >= P.lim) return;  // ldp is a multiple of 4: a group of four lies in its row
+        float4 *o = reinterpret_cast<float4 *>(out + (int64_t)q * ldp + p);
+        float4 r = make_float4(v[0], v[1], v[2], v[3]);
+        if (!first) {
+            const float4 a = *o;
+            r.x += a.x, r.y += a.y, r.z += a.z, r.w += a.w;
+        }
+        *o = r;
+    });
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ part, int64_t ldp, int splits,
+                                                     int64_t T, int64_t d, const int *__restrict__ pos,
+                                                     typename E::st *__restrict__ dH, int64_t lddh)
+{
+    const int64_t t = blockIdx.x, p = pos[t];
+    for (int64_t c = threadIdx.x; c < d; c += 256) {
+        float s = 0.f;
+        if (p >= 0)
+            for (int k = 0; k < splits; ++k) s += part[((int64_t)k * T + p) * ldp + c];
+        dH[t * lddh + c] = E::round(s);
+    }
+}
+
+// ------------------------------------------------------------------ sizes
+
+constexpr int64_t XENT_G_BYTES = (int64_t)128 << 20;  // a piece's gradient stays in the 256 MB last-level cache
+
+struct XentPlan {
+    int64_t dp;      // row of packed H and W: d rounded up to 64 elements
+    int64_t dk;      // d rounded up to 16 bytes
+    int64_t piece;   // vocabulary entries per piece
+    int splits;      // of a piece's contraction in dH
+    // byte offsets into the workspace
+    int64_t pos, ptgt, plse, pdl, nvalid, hp, wp, ztgt, part, g, total;
+};
+
+XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
+{
+    XentPlan p{};
+    const int64_t es = t == SPEC_BF16 ? 2 : 4;
+    p.dp = up_h(d, 64);
+    p.dk = up_h(d, 16 / es);
+    const int64_t Tn = std::max<int64_t>(T, 1);
+    p.piece = std::max<int64_t>(2048, XENT_G_BYTES / (es * Tn) / 256 * 256);
+    p.piece = std::min<int64_t>(p.piece, up_h(V, 256));
+    // dH has few tiles when tokens are few: split its contraction until about
+    // two workgroups per CU have work, in shares of at least 512 entries
+    const int64_t tiles = cdiv_h(Tn, 128) * cdiv_h(d, 128);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, p.piece / 512, 64}));
+    int64_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = o;
+        o += up_h(bytes, 256);
+        return at;
+    };
+    p.nvalid = take(4);
+    p.pos = take(4 * Tn);
+    p.ptgt = take(4 * Tn);
+    p.hp = take(es * Tn * p.dp);
+    p.wp = take(es * p.piece * p.dp);
+    if (grad) {
+        p.plse = take(4 * Tn);
+        p.pdl = take(4 * Tn);
+        p.g = take(es * Tn * p.piece);
+        p.part = take((int64_t)4 * p.splits * Tn * up_h(d, 4));
+    } else {
+        p.ztgt = take(4 * Tn);
+        p.part = take(8 * Tn * cdiv_h(V, 128));
+    }
+    p.total = o;
+    return p;
+}
+
+template <typename E>
+hipError_t pack(hipStream_t stream, const XentPlan &pl, const void *H, int64_t ldh, const void *target, int is64,
+                const float *lse, const float *dloss, int64_t T, int64_t V, int64_t d, char *ws)
+{
+    using st = typename E::st;
+    const int vec = (uintptr_t)H % 16 == 0 && ldh * sizeof(st) % 16 == 0 && d == pl.dp;
+    hipLaunchKernelGGL(k_xent_pack<E>, dim3((unsigned)cdiv_h(T, PACK_ROWS)), dim3(256), 0, stream, (const st *)H, ldh, d,
+                       pl.dp, vec, target, is64, T, V, (st *)(ws + pl.hp), (int *)(ws + pl.pos), (int *)(ws + pl.ptgt),
+                       lse, dloss, (float *)(ws + pl.plse), (float *)(ws + pl.pdl), (int *)(ws + pl.nvalid));
+    return hipGetLastError();
+}
+
+// W as the products can read it: itself where its rows are 16-byte aligned, else a packed piece
+template <typename E>
+bool direct_w(const void *W, int64_t ldw, int64_t d)
+{
+    const int64_t es = sizeof(typename E::st);
+    return (uintptr_t)W % 16 == 0 && ldw * es % 16 == 0 && d * es % 16 == 0;
+}
+
+template <typename E>
+hipError_t wpiece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t &ldw, int64_t d, int64_t vn,
+                  bool direct, char *ws, const typename E::st *&out)
+{
+    using st = typename E::st;
+    out = W;
+    if (direct) return hipSuccess;
+    hipLaunchKernelGGL(k_xent_wpack<E>, dim3((unsigned)cdiv_h(vn, 4)), dim3(256), 0, stream, W, ldw, d, pl.dp, vn,
+                       (st *)(ws + pl.wp));
+    out = (const st *)(ws + pl.wp);
+    ldw = pl.dp;
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t xent_fwd(hipStream_t stream, const void *H, int64_t ldh, const void *W, int64_t ldw, const void *target,
+                    int is64, int64_t T, int64_t V, int64_t d, float scale, float *loss, float *lse, char *ws)
+{
+    using st = typename E::st;
+    using C = Cfg128;
+    const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, false);
+    hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, nullptr, nullptr, T, V, d, ws);
+    if (e != hipSuccess) return e;
+    const bool direct = direct_w<E>(W, ldw, d);
+    const int64_t piece = direct ? V : pl.piece, ldpart = cdiv_h(V, C::BP);
+    for (int64_t v = 0; v < V; v += piece) {
+        const int64_t vn = std::min(piece, V - v);
+        int64_t ld = ldw;
+        const st *Wv;
+        e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
+        if (e != hipSuccess) return e;
+        const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
+        hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, Wv,
+                           ld, vn, v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq,
+                           scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
+                           (int)(v / C::BP));
+        SPEC_LAUNCH_CHECK();
+    }
+    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv_h(T, 4)), dim3(256), 0, stream, (const float2 *)(ws + pl.part),
+                       ldpart, (int)ldpart, (const int *)(ws + pl.pos), (const float *)(ws + pl.ztgt), T, loss, lse);
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void *W, int64_t ldw, const void *target,
+                     int is64, int64_t T, int64_t V, int64_t d, float scale, const float *lse, const float *dloss,
+                     void *dH, int64_t lddh, void *dW, int64_t lddw, float beta, char *ws)
+{
+    using st = typename E::st;
+    using C = Cfg128;
+    const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, true);
+    hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, lse, dloss, T, V, d, ws);
+    if (e != hipSuccess) return e;
+    const bool direct = direct_w<E>(W, ldw, d);
+    const int *nvalid = (const int *)(ws + pl.nvalid);
+    const st *Hp = (const st *)(ws + pl.hp);
+    st *G = (st *)(ws + pl.g);
+    float *part = (float *)(ws + pl.part);
+    const int64_t ldp = up_h(d, 4);
+    const int nt = 64 * C::WP * C::WQ, tq = (int)cdiv_h(T, C::BQ), dpn = (int)cdiv_h(d, C::BP);
+    const int vec = (uintptr_t)dW % (4 * sizeof(st)) == 0 && lddw % 4 == 0;
+    for (int64_t v = 0; v < V; v += pl.piece) {
+        const int64_t vn = std::min(pl.piece, V - v);
+        int64_t ld = ldw;
+        const st *Wv;
+        e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
+        if (e != hipSuccess) return e;
+        const int vp = (int)cdiv_h(vn, C::BP), vq = (int)cdiv_h(vn, C::BQ);
+        hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)vp * tq)), dim3(nt), 0, stream, Wv, ld, vn, v, Hp,
+                           pl.dp, pl.dk, nvalid, vp, tq, scale, (const int *)(ws + pl.ptgt),
+                           (const float *)(ws + pl.plse), (const float *)(ws + pl.pdl), G, pl.piece);
+        SPEC_LAUNCH_CHECK();
+        hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)dpn * vq)), dim3(nt), 0, stream, Hp, pl.dp, G,
+                           pl.piece, vn, d, nvalid, dpn, vq, (st *)dW + v * lddw, lddw, beta, vec);
+        SPEC_LAUNCH_CHECK();
+        const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
+        hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)dpn * tq * pl.splits)), dim3(nt), 0, stream, Wv,
+                           ld, G, pl.piece, vn, per, d, T, nvalid, dpn, tq, part, ldp, v == 0);
+        SPEC_LAUNCH_CHECK();
+    }
+    hipLaunchKernelGGL(k_xent_dh_out<E>, dim3((unsigned)T), dim3(256), 0, stream, part, ldp, pl.splits, T, d,
+                       (const int *)(ws + pl.pos), (st *)dH, lddh);
+    return hipGetLastError();
+}
+
+// dW <- beta dW where no token has a target to add
+template <typename E>
+__global__ __launch_bounds__(256) void k_xent_scale(typename E::st *__restrict__ dW, int64_t lddw, int64_t d, float beta)
+{
+    typename E::st *r = dW + (int64_t)blockIdx.x * lddw;
+    for (int64_t c = threadIdx.x; c < d; c += 256) r[c] = E::round(beta != 0.f ? beta * E::wide(r[c]) : 0.f);
+}
+
+}  // namespace
+
+size_t linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t d, int t)
+{
+    return (size_t)xent_plan(T, V, d, t, false).total;
+}
+
+size_t linear_xent_grad_workspace_bytes(int64_t T, int64_t V, int64_t d, int t)
+{
+    return (size_t)xent_plan(T, V, d, t, true).total;
+}
+
+hipError_t launch_linear_xent(hipStream_t stream, const void *H, const void *W, int t, int64_t T, int64_t V, int64_t d,
+                              int64_t ldh, int64_t ldw, const void *target, int is64, float scale, float *loss,
+                              float *lse, void *ws)
+{
+    if (T == 0) return hipSuccess;
+    return t == SPEC_BF16 ? xent_fwd<ElBF16>(stream, H, ldh, W, ldw, target, is64, T, V, d, scale, loss, lse, (char *)ws)
+                          : xent_fwd<ElF32>(stream, H, ldh, W, ldw, target, is64, T, V, d, scale, loss, lse, (char *)ws);
+}
+
+hipError_t launch_linear_xent_grad(hipStream_t stream, const void *H, const void *W, int t, int64_t T, int64_t V,
+                                   int64_t d, int64_t ldh, int64_t ldw, const void *target, int is64, float scale,
+                                   const float *lse, const float *dloss, void *dH, int64_t lddh, void *dW, int64_t lddw,
+                                   float beta, void *ws)
+{
+    if (T == 0) {
+        if (t == SPEC_BF16)
+            hipLaunchKernelGGL(k_xent_scale<ElBF16>, dim3((unsigned)V), dim3(256), 0, stream, (uint16_t *)dW, lddw, d, beta);
+        else
+            hipLaunchKernelGGL(k_xent_scale<ElF32>, dim3((unsigned)V), dim3(256), 0, stream, (float *)dW, lddw, d, beta);
+        return hipGetLastError();
+    }
+    return t == SPEC_BF16 ? xent_grad<ElBF16>(stream, H, ldh, W, ldw, target, is64, T, V, d, scale, lse, dloss, dH, lddh,
+                                              dW, lddw, beta, (char *)ws)
+                          : xent_grad<ElF32>(stream, H, ldh, W, ldw, target, is64, T, V, d, scale, lse, dloss, dH, lddh,
+                                             dW, lddw, beta, (char *)ws);
+}
