@@ -14,17 +14,17 @@
 // (no registers, no address arithmetic in the loop beyond the base); the
 // hardware writes a wave's 64 chunks to consecutive LDS addresses, so bank
 // conflicts are avoided by choosing which chunk a lane fetches:
-//   Kc  LDS row p = 8 chunks, chunk c in slot c ^ (p & 7): the fragment read
-//       (32 rows, one chunk each, 16 bytes per lane) meets every slot equally.
+//   Kc  LDS row p = 8 chunks, chunk c in slot c ^ ((p >> 1) & 7): a fragment read
+//       takes one chunk of 16 rows per cycle, which are the 16 slots of two rows
+//       (the 64 banks) once each; with p & 7 every second LDS cycle was a conflict.
 //   Ks  LDS row k = BP / (16 bytes) chunks, chunk c in slot c ^ f(k).  16-bit
 //       fragments are read with the transposing LDS load (per 16 lanes: four
 //       k-rows of 16 elements, each lane receives its column's four k), whose
 //       rows k & 3 go to different 64-byte groups by f = 4 (k & 3); f32
 //       fragments read 32 consecutive columns of rows k and k + 4, separated by
 //       f = 8 ((k >> 2) & 1).
-// Two LDS stages: while a stage is multiplied the next is being filled; one
-// barrier per K-step.  Rows past the end read as zero: a lane whose chunk lies
-// outside gets an offset beyond the buffer resource.
+// The LDS conflict counter reads zero for all forms.  Rows past the end read as
+// zero: a lane whose chunk lies outside gets an offset beyond the buffer resource.
 #pragma once
 
 #include <type_traits>
@@ -70,20 +70,37 @@ struct MmSrc {
     int64_t K;         // end of k: past it the operand is zero (Kc: a multiple of 16 bytes)
 };
 
+// f(0), ..., f(N - 1) with the index as a constant
+template <int I, int N, typename F>
+SPEC_DEVICE void mm_for(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        mm_for<I + 1, N>(f);
+    }
+}
+
 template <typename E, int BP, int BQ, int WP, int WQ, bool PS, bool QS>
 struct Mm {
     static constexpr int SZ = (int)sizeof(typename E::st);
     static constexpr int EPC = 16 / SZ;    // elements per chunk
-    static constexpr int BK = 128 / SZ;    // k per step
+    static constexpr int ROW = 128;        // bytes of an operand row per step
+    static constexpr int BK = ROW / SZ;    // k per step
+    static constexpr int RC = ROW / 16;    // chunks of a row
+    static constexpr int KQ = ROW / 32;    // fragments (32 bytes of k) per step
+    static constexpr int STAGES = 2;
     static constexpr int NT = 64 * WP * WQ;
     static constexpr int MI = BP / WP / 32, NI = BQ / WQ / 32;
-    static constexpr int P_BYTES = BP * 128, Q_BYTES = BQ * 128;
-    static constexpr int PL = BP * 8 / NT, QL = BQ * 8 / NT;  // chunks per thread and step
+    static constexpr int P_BYTES = BP * ROW, Q_BYTES = BQ * ROW;
+    static constexpr int PL = BP * RC / NT, QL = BQ * RC / NT;  // chunks per thread and step
     static_assert(PL >= 1 && QL >= 1 && BP % (32 * WP) == 0 && BQ % (32 * WQ) == 0, "tile");
 
     static constexpr uint32_t OUT = 0xFFFFFFF0u;
 
     f32x16_t acc[MI][NI];
+
+    // slot permutation of row p of a Kc tile
+    static SPEC_DEVICE int kc_f(int p) { return ROW == 128 ? (p >> 1) & 7 : (p >> 2) & 3; }
 
     // slot permutation of row k of a Ks tile with R columns
     template <int R>
@@ -93,59 +110,51 @@ struct Mm {
         return (SZ == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1)) & (CH - 1);
     }
 
+    // byte offsets of this thread's chunks of a K-step from the step's base; kc:
+    // the first k of its chunks (Kc: the same for all of them, the slots repeat every 16 rows)
     template <int R, bool S, int N>
-    static SPEC_DEVICE void offsets(const MmSrc &s, uint32_t (&v)[N], int (&kc)[N])
+    static SPEC_DEVICE void offsets(const MmSrc &s, uint32_t (&v)[N], int &kc)
     {
+        const int tid = threadIdx.x;
+        kc = S ? 0 : (((tid % RC) ^ kc_f(tid / RC)) * EPC);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int q = i * NT + (int)threadIdx.x;
+            const int q = i * NT + tid;
             if (S) {
                 constexpr int CH = R / EPC;
                 const int k = q / CH, c = (q % CH) ^ ks_f<R>(k);
-                kc[i] = 0;
                 v[i] = c * EPC < s.lim ? (uint32_t)(k * (int)s.ldb + c * 16) : OUT;
             } else {
-                const int row = q >> 3, c = (q & 7) ^ (row & 7);
-                kc[i] = c * EPC;
-                v[i] = row < s.lim ? (uint32_t)(row * (int)s.ldb + c * 16) : OUT;
+                const int row = q / RC;
+                v[i] = row < s.lim ? (uint32_t)(row * (int)s.ldb + kc * SZ) : OUT;
             }
         }
     }
 
-    // starts the copy of K-step [k0, k0 + BK) of one operand
+    // starts the copy of K-step [k0, k0 + BK) of one operand; what lies past its K arrives as zero
     template <bool S, int N>
-    static SPEC_DEVICE void stage(const MmSrc &s, const uint32_t (&v)[N], const int (&kc)[N], int64_t k0, char *lds)
+    static SPEC_DEVICE void stage(const MmSrc &s, const uint32_t (&v)[N], int kc, int64_t k0, char *lds)
     {
-        const int64_t K = s.K;
         char *dst = lds + ((int)threadIdx.x & ~63) * 16;  // the wave's first chunk
+        const int64_t left = s.K - k0;
+        int num;
+        uint32_t past = 0;
         if (S) {
-            const int64_t lim = (s.lim + EPC - 1) / EPC * 16;
-            const int64_t rem = (K - k0 - 1) * s.ldb + lim;
-            const int num = K > k0 && s.lim > 0 ? (int)(rem < 0x7FFFFFF0 ? rem : 0x7FFFFFF0) : 0;
-            const __amdgpu_buffer_rsrc_t rs =
-                __builtin_amdgcn_make_buffer_rsrc((void *)(s.base + k0 * s.ldb), 0, num, 0x00020000);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(dst + i * NT * 16), 16, (int)v[i], 0, 0, 0);
+            const int64_t rem = (left - 1) * s.ldb + (s.lim + EPC - 1) / EPC * 16;
+            num = left > 0 && s.lim > 0 ? (int)(rem < 0x7FFFFFF0 ? rem : 0x7FFFFFF0) : 0;
         } else {
-            const __amdgpu_buffer_rsrc_t rs =
-                __builtin_amdgcn_make_buffer_rsrc((void *)(s.base + k0 * SZ), 0, 0x7FFFFFF0, 0x00020000);
-            if (k0 + BK <= K) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(dst + i * NT * 16), 16, (int)v[i], 0, 0,
-                                                             0);
-            } else {
-                const int left = (int)max<int64_t>(K - k0, 0);
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(dst + i * NT * 16), 16,
-                                                             (int)(kc[i] < left ? v[i] : OUT), 0, 0, 0);
-            }
+            num = 0x7FFFFFF0;
+            past = kc < left ? 0u : 0x80000000u;
         }
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(s.base + (left > 0 ? k0 : 0) * (S ? s.ldb : (int64_t)SZ)), 0, num, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(dst + i * NT * 16), 16, (int)(v[i] | past), 0, 0,
+                                                     0);
     }
 
-    // the 32-row fragment at rows r0 .. r0 + 31 of kk-th quarter of the K-step
+    // the 32-row fragment at rows r0 .. r0 + 31 of the kk-th half of the K-step
     struct Frag {
         f32x4_t x;
     };
@@ -155,7 +164,7 @@ struct Mm {
         Frag f;
         const int h = lane >> 5;
         if (!S) {
-            f.x = *reinterpret_cast<const f32x4_t *>(lds + (r0 + (lane & 31)) * 128 + (((2 * kk + h) ^ (lane & 7)) << 4));
+            f.x = *reinterpret_cast<const f32x4_t *>(lds + (r0 + (lane & 31)) * ROW + (((2 * kk + h) ^ kc_f(lane & 31)) << 4));
         } else if (SZ == 2) {
             const int kq = (lane >> 2) & 3;
             const int chunk = (r0 >> 3) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
@@ -189,39 +198,49 @@ struct Mm {
         }
     }
 
-    SPEC_DEVICE void multiply(const char *sp, const char *sq, int p0, int q0, int lane)
+    struct Frags {
+        Frag a[MI], b[NI];
+    };
+    static SPEC_DEVICE void fetch(Frags &f, const char *sp, const char *sq, int p0, int q0, int kk, int lane)
     {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            Frag a[MI], b[NI];
+        for (int m = 0; m < MI; ++m) f.a[m] = frag<BP, PS>(sp, p0 + 32 * m, kk, lane);
 #pragma unroll
-            for (int m = 0; m < MI; ++m) a[m] = frag<BP, PS>(sp, p0 + 32 * m, kk, lane);
+        for (int n = 0; n < NI; ++n) f.b[n] = frag<BQ, QS>(sq, q0 + 32 * n, kk, lane);
+    }
+    // the reads before this point stay before the products after it
+    SPEC_DEVICE void multiply(const Frags &f)
+    {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = 0; n < NI; ++n) b[n] = frag<BQ, QS>(sq, q0 + 32 * n, kk, lane);
+        for (int m = 0; m < MI; ++m)
 #pragma unroll
-            for (int m = 0; m < MI; ++m)
-#pragma unroll
-                for (int n = 0; n < NI; ++n) acc[m][n] = mfma(a[m], b[n], acc[m][n]);
-        }
+            for (int n = 0; n < NI; ++n) acc[m][n] = mfma(f.a[m], f.b[n], acc[m][n]);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
-    // the LDS copies issued by this wave have landed, then those of every wave
+    // all but the latest `left` LDS copies of this wave have landed, and so have every wave's
+    template <int LEFT>
     static SPEC_DEVICE void landed()
     {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        static_assert(LEFT < 16, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(0x0F70 | LEFT);
         __syncthreads();
     }
 
-    // acc = sum over k in [kb, K); sp0 .. sq1: the two stages of both operands
-    // (separate LDS objects, so that a read of one stage need not wait for the
-    // copy into the other).
-    SPEC_DEVICE void run(const MmSrc &P, const MmSrc &Q, int64_t kb, int64_t K, char *sp0, char *sp1, char *sq0,
-                         char *sq1)
+    // The stages of both operands: separate LDS objects, so that a read of one
+    // stage need not wait for the copy into another.
+    struct Lds {
+        char *p[STAGES], *q[STAGES];
+    };
+
+    // acc = sum over k in [kb, K)
+    SPEC_DEVICE void run(const MmSrc &P, const MmSrc &Q, int64_t kb, int64_t K, const Lds &s)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         const int p0 = (wave % WP) * (BP / WP), q0 = (wave / WP) * (BQ / WQ);
         uint32_t vp[PL], vq[QL];
-        int kp[PL], kq[QL];
+        int kp, kq;
         offsets<BP, PS>(P, vp, kp);
         offsets<BQ, QS>(Q, vq, kq);
 #pragma unroll
@@ -231,25 +250,38 @@ struct Mm {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.f;
         if (kb >= K) return;
-        stage<PS>(P, vp, kp, kb, sp0);
-        stage<QS>(Q, vq, kq, kb, sq0);
-        for (int64_t k0 = kb;; k0 += 2 * BK) {
-            landed();
-            const bool one = k0 + BK < K, two = k0 + 2 * BK < K;
-            if (one) {
-                stage<PS>(P, vp, kp, k0 + BK, sp1);
-                stage<QS>(Q, vq, kq, k0 + BK, sq1);
-            }
-            multiply(sp0, sq0, p0, q0, lane);
-            if (!one) break;
-            landed();
-            if (two) {
-                stage<PS>(P, vp, kp, k0 + 2 * BK, sp0);
-                stage<QS>(Q, vq, kq, k0 + 2 * BK, sq0);
-            }
-            multiply(sp1, sq1, p0, q0, lane);
-            if (!two) break;
+        // The fragments of the next half step are read while a half is multiplied.
+        // Before the second half's products its fragments are in registers, so
+        // the stage is free: there the barrier stands, the stage's next step is
+        // requested, and the next stage's first fragments are read behind the
+        // products.  Steps past K are requested too (they arrive as zeros), so
+        // that the number of copies in flight is always the same.
+        constexpr int S = STAGES;
+        Frags f0, f1;
+        auto request = [&](int64_t k, int i) {
+            stage<PS>(P, vp, kp, k, s.p[i]);
+            stage<QS>(Q, vq, kq, k, s.q[i]);
+        };
+        mm_for<0, S>([&](auto I) { request(kb + decltype(I)::value * BK, decltype(I)::value); });
+        landed<(S - 1) * (PL + QL)>();
+        fetch(f0, s.p[0], s.q[0], p0, q0, 0, lane);
+        // S steps per turn, with no way out between them (a copy of every
+        // accumulator would be kept for it)
+        for (int64_t k0 = kb; k0 < K; k0 += S * BK) {
+            mm_for<0, S>([&](auto I) {
+                constexpr int i = decltype(I)::value, j = (i + 1) % S;
+                mm_for<1, KQ>([&](auto Q_) {
+                    constexpr int kk = decltype(Q_)::value;
+                    fetch(kk & 1 ? f1 : f0, s.p[i], s.q[i], p0, q0, kk, lane);
+                    multiply(kk & 1 ? f0 : f1);
+                });
+                landed<(S - 2) * (PL + QL)>();
+                request(k0 + (i + S) * BK, i);
+                fetch(f0, s.p[j], s.q[j], p0, q0, 0, lane);
+                multiply(f1);
+            });
         }
+        landed<0>();  // nothing is left to arrive in LDS that others may use
     }
 
     // f(p, q, v): four results p .. p + 3 of row q (offsets within the tile)
@@ -286,3 +318,23 @@ SPEC_DEVICE void mm_tile(int64_t id, int np, int nq, int &tp, int &tq)
     tq = band * G + rest % w;
     tp = rest / w;
 }
+
+// Tile shapes: 256 x 256 by eight waves (128 x 64 each, one workgroup per CU:
+// 128 KB of LDS) and 128 x 128 by four (64 x 64 each, two workgroups per CU).
+struct Tile256 {
+    static constexpr int BP = 256, BQ = 256, WP = 2, WQ = 4;
+};
+struct Tile128 {
+    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
+};
+
+template <typename E, typename C, bool PS, bool QS>
+using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
+
+// declares the LDS stages of both operands as `lds`
+#define MM_STAGES(M)                                                                                           \
+    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]; \
+    const typename M::Lds lds{{sp0, sp1}, {sq0, sq1}}
+
+// two waves per SIMD: one workgroup of Tile256, two of Tile128 per CU
+#define MM_BOUNDS(C) __launch_bounds__(64 * C::WP * C::WQ, 2)

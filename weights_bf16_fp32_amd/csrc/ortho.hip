@@ -44,16 +44,6 @@ inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
 
 constexpr int NORM_BLOCKS = 64;  // partial sums of squares per matrix
 
-#define MM_STAGES(M)                                                                                           \
-    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]
-
-struct Cfg128 {
-    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
-};
-
-template <typename E, typename C, bool PS, bool QS>
-using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
-
 // grid (NORM_BLOCKS, batch)
 template <typename G>
 __global__ __launch_bounds__(256) void k_ns_norm(const typename G::st *__restrict__ X, int64_t m, int64_t n, int64_t ld,
@@ -148,7 +138,7 @@ SPEC_DEVICE void put_sym(typename E::st *A, float *diag, const NsDims &D, int64_
 
 // grid (tiles on and below the diagonal, batch).  real: 1 / sx^2
 template <typename E, typename C, bool TALL>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_gram(const typename E::st *__restrict__ X, NsDims D,
+__global__ MM_BOUNDS(C) void k_ns_gram(const typename E::st *__restrict__ X, NsDims D,
                                                                     float real, float sa,
                                                                     typename E::st *__restrict__ A,
                                                                     float *__restrict__ diag)
@@ -163,7 +153,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_gram(const typenam
     const MmSrc P{(const char *)(x + j0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
     const MmSrc Q{(const char *)(x + i0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
-    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, 0, K, lds);
     mm.each4([&](int p, int q, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= real;
@@ -173,7 +163,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_gram(const typenam
 
 // B = b A + c A^2 with A = diag(da) + E; ea = 1 / sa
 template <typename E, typename C>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_poly(const typename E::st *__restrict__ A,
+__global__ MM_BOUNDS(C) void k_ns_poly(const typename E::st *__restrict__ A,
                                                                     const float *__restrict__ da, NsDims D, float b,
                                                                     float c, float ea, float sb,
                                                                     typename E::st *__restrict__ B,
@@ -190,7 +180,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_poly(const typenam
     const MmSrc P{(const char *)(a + j0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
     const MmSrc Q{(const char *)(a + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
-    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, 0, K, lds);
     mm.each4([&](int p, int q, float (&v)[4]) {
         const int64_t i = i0 + q, j = j0 + p;
         if (i < D.r && j < D.ap) {
@@ -210,7 +200,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_poly(const typenam
 // The next X (scaled by sx1), or O = scale X in the last step.
 // ex = 1 / sx of the current X, eb = 1 / sb.
 template <typename E, typename C, bool TALL, typename O, bool LAST>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_apply(
+__global__ MM_BOUNDS(C) void k_ns_apply(
     const typename E::st *__restrict__ hi, const typename E::st *__restrict__ lo, const typename E::st *__restrict__ B,
     const float *__restrict__ db, NsDims D, int np, int nq, float a, float ex, float eb, float sx1,
     typename E::st *__restrict__ hi1, typename E::st *__restrict__ lo1, typename O::st *__restrict__ out, int64_t ldo,
@@ -234,7 +224,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_ns_apply(
         Q = MmSrc{(const char *)(bm + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     }
     M mm;
-    mm.run(P, Q, 0, K, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, 0, K, lds);
     mm.each4([&](int p, int q, float (&v)[4]) {
         const int64_t i = i0 + q, j = j0 + p;
         if (i >= D.rows || j >= D.xp) return;
@@ -333,7 +323,7 @@ template <typename GT, typename E, bool TALL>
 hipError_t ns_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
                   const double *co, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so, char *ws)
 {
-    using C = Cfg128;
+    using C = Tile128;
     using st = typename E::st;
     using gst = typename GT::st;
     constexpr bool F16 = sizeof(st) == 2;

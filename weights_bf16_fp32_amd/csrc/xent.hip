@@ -106,34 +106,22 @@ __global__ __launch_bounds__(256) void k_xent_wpack(const typename E::st *__rest
     if (r < rows) copy_row(W + r * ldw, Wp + r * dp, d, dp, false, threadIdx.x & 63, 64);
 }
 
-// two LDS stages of both operands
-#define MM_STAGES(M)                                                                                           \
-    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]
-
-struct Cfg128 {
-    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
-};
-
-template <typename E, typename C, bool PS, bool QS>
-using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
-
 // The logits of vocabulary rows [tile] (P) and packed tokens (Q).
 template <typename M, typename E>
 SPEC_DEVICE void logits(M &mm, const typename E::st *W, int64_t ldw, int64_t vn, const typename E::st *Hp, int64_t dp,
-                        int n, int64_t d, int64_t v0, int t0, char *sp0, char *sp1, char *sq0, char *sq1, int BP,
-                        int BQ)
+                        int n, int64_t d, int64_t v0, int t0, const typename M::Lds &lds, int BP, int BQ)
 {
     constexpr int SZ = M::SZ;
     const MmSrc P{(const char *)(W + v0 * ldw), ldw * SZ, (int)min<int64_t>(BP, vn - v0), d};
     const MmSrc Q{(const char *)(Hp + (int64_t)t0 * dp), dp * SZ, min(BQ, n - t0), d};
-    mm.run(P, Q, 0, d, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, 0, d, lds);
 }
 
 // grid: tiles of [vn vocabulary rows] x [T tokens]; W's rows are vocabulary
 // entries vbase .. vbase + vn - 1.  part[t][tile0 + tp] = (max, sum exp(z - max)).
 // dk: d rounded up to 16 bytes (the padding of both operands is zero).
 template <typename E, typename C>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_fwd(const typename E::st *__restrict__ W, int64_t ldw,
+__global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, int64_t ldw,
                                                                   int64_t vn, int64_t vbase,
                                                                   const typename E::st *__restrict__ Hp, int64_t dp,
                                                                   int64_t dk, const int *__restrict__ nvalid, int np,
@@ -150,7 +138,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_fwd(const typena
     if (t0 >= n) return;
     const int64_t v0 = (int64_t)tp * C::BP;
     M mm;
-    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, sp0, sp1, sq0, sq1, C::BP, C::BQ);
+    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wp = wave % C::WP;
     const int p0 = wp * (C::BP / C::WP) + 4 * (lane >> 5), q0 = (wave / C::WP) * (C::BQ / C::WQ) + (lane & 31);
     const int lim = (int)min<int64_t>(C::BP, vn - v0);
@@ -236,7 +224,7 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 
 // G[t][v - vbase], columns up to vn rounded up to 16 bytes (zero past vn)
 template <typename E, typename C>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_g(const typename E::st *__restrict__ W, int64_t ldw,
+__global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int64_t ldw,
                                                                 int64_t vn, int64_t vbase,
                                                                 const typename E::st *__restrict__ Hp, int64_t dp,
                                                                 int64_t dk, const int *__restrict__ nvalid, int np,
@@ -253,7 +241,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_g(const typename
     if (t0 >= n) return;
     const int64_t v0 = (int64_t)tp * C::BP;
     M mm;
-    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, sp0, sp1, sq0, sq1, C::BP, C::BQ);
+    logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
     const int lim = (int)min<int64_t>(C::BP, vn - v0);
     const int lim4 = (int)min<int64_t>(C::BP, round_up(vn, M::EPC) - v0);
     mm.each4([&](int p, int q, float (&v)[4]) {
@@ -270,7 +258,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_g(const typename
 
 // dW rows v (Q) by columns of d (P): sum over tokens of H[t][p] G[t][q]
 template <typename E, typename C>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dw(const typename E::st *__restrict__ Hp, int64_t dp,
+__global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, int64_t dp,
                                                                  const typename E::st *__restrict__ G, int64_t ldg,
                                                                  int64_t vn, int64_t d, const int *__restrict__ nvalid,
                                                                  int np, int nq, typename E::st *__restrict__ dW,
@@ -284,7 +272,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dw(const typenam
     const MmSrc P{(const char *)(Hp + p0), dp * M::SZ, (int)min<int64_t>(C::BP, d - p0), n};
     const MmSrc Q{(const char *)(G + v0), ldg * M::SZ, (int)min<int64_t>(C::BQ, vn - v0), n};
     M mm;
-    mm.run(P, Q, 0, n, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, 0, n, lds);
     mm.each4([&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;
         typename E::st *o = dW + (v0 + q) * lddw + p0 + p;
@@ -304,7 +292,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dw(const typenam
 
 // part[split][t][p] (+)= sum over the split's share of the piece of W[v][p] G[t][v]
 template <typename E, typename C>
-__global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dh(const typename E::st *__restrict__ W, int64_t ldw,
+__global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int64_t ldw,
                                                                  const typename E::st *__restrict__ G, int64_t ldg,
                                                                  int64_t vn, int64_t per, int64_t d, int64_t T,
                                                                  const int *__restrict__ nvalid, int np, int nq,
@@ -322,7 +310,7 @@ __global__ __launch_bounds__(64 * C::WP * C::WQ, 2) void k_xent_dh(const typenam
     const MmSrc P{(const char *)(W + p0), ldw * M::SZ, (int)min<int64_t>(C::BP, d - p0), ke};
     const MmSrc Q{(const char *)(G + (int64_t)t0 * ldg), ldg * M::SZ, min(C::BQ, n - t0), round_up(ke, M::EPC)};
     M mm;
-    mm.run(P, Q, kb, ke, sp0, sp1, sq0, sq1);
+    mm.run(P, Q, kb, ke, lds);
     float *out = part + ((int64_t)split * T + t0) * ldp + p0;
     mm.each4([&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;  // ldp is a multiple of 4: a group of four lies in its row
@@ -434,29 +422,82 @@ hipError_t wpiece(hipStream_t stream, const XentPlan &pl, const typename E::st *
     return hipGetLastError();
 }
 
+// 256 x 256 tiles where they fill most of the CUs; 128 x 128 where there are
+// fewer (or 128 tokens leave half of a tile empty).
+inline bool big_tiles(int64_t rows, int64_t cols)
+{
+    return rows > 128 && cols > 128 && cdiv_h(rows, 256) * cdiv_h(cols, 256) >= 192;
+}
+
+template <typename E, typename C>
+hipError_t fwd_piece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t ldw, int64_t vn, int64_t v,
+                     int64_t T, float scale, int64_t ldpart, char *ws)
+{
+    const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
+    hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, W, ldw,
+                       vn, v, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq,
+                       scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
+                       (int)(v / C::BP));
+    return hipGetLastError();
+}
+
+template <typename E, typename C>
+hipError_t g_piece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t ldw, int64_t vn, int64_t v,
+                   int64_t T, float scale, char *ws)
+{
+    using st = typename E::st;
+    const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
+    hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, W, ldw, vn,
+                       v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq, scale,
+                       (const int *)(ws + pl.ptgt), (const float *)(ws + pl.plse), (const float *)(ws + pl.pdl),
+                       (st *)(ws + pl.g), pl.piece);
+    return hipGetLastError();
+}
+
+template <typename E, typename C>
+hipError_t dw_piece(hipStream_t stream, const XentPlan &pl, int64_t vn, int64_t d, typename E::st *dW, int64_t lddw,
+                    float beta, char *ws)
+{
+    using st = typename E::st;
+    const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(vn, C::BQ);
+    const int vec = (uintptr_t)dW % (4 * sizeof(st)) == 0 && lddw % 4 == 0;
+    hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream,
+                       (const st *)(ws + pl.hp), pl.dp, (const st *)(ws + pl.g), pl.piece, vn, d,
+                       (const int *)(ws + pl.nvalid), np, nq, dW, lddw, beta, vec);
+    return hipGetLastError();
+}
+
+template <typename E, typename C>
+hipError_t dh_piece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t ldw, int64_t vn, int64_t T,
+                    int64_t d, bool first, char *ws)
+{
+    const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(T, C::BQ);
+    const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
+    hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)np * nq * pl.splits)), dim3(64 * C::WP * C::WQ), 0,
+                       stream, W, ldw, (const typename E::st *)(ws + pl.g), pl.piece, vn, per, d, T,
+                       (const int *)(ws + pl.nvalid), np, nq, (float *)(ws + pl.part), up_h(d, 4), first);
+    return hipGetLastError();
+}
+
 template <typename E>
 hipError_t xent_fwd(hipStream_t stream, const void *H, int64_t ldh, const void *W, int64_t ldw, const void *target,
                     int is64, int64_t T, int64_t V, int64_t d, float scale, float *loss, float *lse, char *ws)
 {
     using st = typename E::st;
-    using C = Cfg128;
     const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, false);
     hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, nullptr, nullptr, T, V, d, ws);
     if (e != hipSuccess) return e;
-    const bool direct = direct_w<E>(W, ldw, d);
-    const int64_t piece = direct ? V : pl.piece, ldpart = cdiv_h(V, C::BP);
+    const bool direct = direct_w<E>(W, ldw, d), big = big_tiles(T, V);
+    const int64_t piece = direct ? V : pl.piece, ldpart = cdiv_h(V, big ? 256 : 128);
     for (int64_t v = 0; v < V; v += piece) {
         const int64_t vn = std::min(piece, V - v);
         int64_t ld = ldw;
         const st *Wv;
         e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
         if (e != hipSuccess) return e;
-        const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
-        hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, Wv,
-                           ld, vn, v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq,
-                           scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
-                           (int)(v / C::BP));
-        SPEC_LAUNCH_CHECK();
+        e = big ? fwd_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws)
+                : fwd_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws);
+        if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv_h(T, 4)), dim3(256), 0, stream, (const float2 *)(ws + pl.part),
                        ldpart, (int)ldpart, (const int *)(ws + pl.pos), (const float *)(ws + pl.ztgt), T, loss, lse);
@@ -469,39 +510,29 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
                      void *dH, int64_t lddh, void *dW, int64_t lddw, float beta, char *ws)
 {
     using st = typename E::st;
-    using C = Cfg128;
     const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, true);
     hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, lse, dloss, T, V, d, ws);
     if (e != hipSuccess) return e;
     const bool direct = direct_w<E>(W, ldw, d);
-    const int *nvalid = (const int *)(ws + pl.nvalid);
-    const st *Hp = (const st *)(ws + pl.hp);
-    st *G = (st *)(ws + pl.g);
-    float *part = (float *)(ws + pl.part);
-    const int64_t ldp = up_h(d, 4);
-    const int nt = 64 * C::WP * C::WQ, tq = (int)cdiv_h(T, C::BQ), dpn = (int)cdiv_h(d, C::BP);
-    const int vec = (uintptr_t)dW % (4 * sizeof(st)) == 0 && lddw % 4 == 0;
     for (int64_t v = 0; v < V; v += pl.piece) {
         const int64_t vn = std::min(pl.piece, V - v);
         int64_t ld = ldw;
         const st *Wv;
+        st *dWv = (st *)dW + v * lddw;
         e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
         if (e != hipSuccess) return e;
-        const int vp = (int)cdiv_h(vn, C::BP), vq = (int)cdiv_h(vn, C::BQ);
-        hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)vp * tq)), dim3(nt), 0, stream, Wv, ld, vn, v, Hp,
-                           pl.dp, pl.dk, nvalid, vp, tq, scale, (const int *)(ws + pl.ptgt),
-                           (const float *)(ws + pl.plse), (const float *)(ws + pl.pdl), G, pl.piece);
-        SPEC_LAUNCH_CHECK();
-        hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)dpn * vq)), dim3(nt), 0, stream, Hp, pl.dp, G,
-                           pl.piece, vn, d, nvalid, dpn, vq, (st *)dW + v * lddw, lddw, beta, vec);
-        SPEC_LAUNCH_CHECK();
-        const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
-        hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)dpn * tq * pl.splits)), dim3(nt), 0, stream, Wv,
-                           ld, G, pl.piece, vn, per, d, T, nvalid, dpn, tq, part, ldp, v == 0);
-        SPEC_LAUNCH_CHECK();
+        e = big_tiles(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
+                             : g_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ws);
+        if (e != hipSuccess) return e;
+        e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, dWv, lddw, beta, ws)
+                             : dw_piece<E, Tile128>(stream, pl, vn, d, dWv, lddw, beta, ws);
+        if (e != hipSuccess) return e;
+        e = big_tiles(T * pl.splits, d) ? dh_piece<E, Tile256>(stream, pl, Wv, ld, vn, T, d, v == 0, ws)
+                                        : dh_piece<E, Tile128>(stream, pl, Wv, ld, vn, T, d, v == 0, ws);
+        if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_xent_dh_out<E>, dim3((unsigned)T), dim3(256), 0, stream, part, ldp, pl.splits, T, d,
-                       (const int *)(ws + pl.pos), (st *)dH, lddh);
+    hipLaunchKernelGGL(k_xent_dh_out<E>, dim3((unsigned)T), dim3(256), 0, stream, (const float *)(ws + pl.part), up_h(d, 4),
+                       pl.splits, T, d, (const int *)(ws + pl.pos), (st *)dH, lddh);
     return hipGetLastError();
 }
 
