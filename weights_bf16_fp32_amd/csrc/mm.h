@@ -20,10 +20,10 @@
 //   Ks  LDS row k = BP / (16 bytes) chunks, chunk c in slot c ^ f(k).  16-bit
 //       fragments are read with the transposing LDS load (per 16 lanes: four
 //       k-rows of 16 elements, each lane receives its column's four k), whose
-//       rows k & 3 go to different 64-byte groups by f = 4 (k & 3); f32
-//       fragments read 32 consecutive columns of rows k and k + 4, separated by
-//       f = 8 ((k >> 2) & 1).
-// The LDS conflict counter reads zero for all forms.  Rows past the end read as
+//       rows k & 3 go to different 64-byte groups by f = 4 (k & 3) (narrower
+//       tiles' rows lie in different groups by themselves); f32 fragments read 32
+//       consecutive columns of rows k and k + 4, separated by f = 8 ((k >> 2) & 1).
+// The LDS conflict counter reads zero for the 16-bit forms.  Rows past the end read as
 // zero: a lane whose chunk lies outside gets an offset beyond the buffer resource.
 #pragma once
 
@@ -80,24 +80,30 @@ SPEC_DEVICE void mm_for(F &&f)
     }
 }
 
-template <typename E, int BP, int BQ, int WP, int WQ, bool PS, bool QS>
+template <typename E, typename C, bool PS, bool QS>
 struct Mm {
+    static constexpr int BP = C::BP, BQ = C::BQ, WP = C::WP, WQ = C::WQ, WK = C::WK;
     static constexpr int SZ = (int)sizeof(typename E::st);
     static constexpr int EPC = 16 / SZ;    // elements per chunk
     static constexpr int ROW = 128;        // bytes of an operand row per step
     static constexpr int BK = ROW / SZ;    // k per step
     static constexpr int RC = ROW / 16;    // chunks of a row
-    static constexpr int KQ = ROW / 32;    // fragments (32 bytes of k) per step
-    static constexpr int STAGES = 2;
-    static constexpr int NT = 64 * WP * WQ;
+    static constexpr int KW = ROW / 32 / WK;  // fragments (32 bytes of k) per step and wave
+    static constexpr int STAGES = C::STAGES;
+    static constexpr int NT = C::NT;
     static constexpr int MI = BP / WP / 32, NI = BQ / WQ / 32;
     static constexpr int P_BYTES = BP * ROW, Q_BYTES = BQ * ROW;
     static constexpr int PL = BP * RC / NT, QL = BQ * RC / NT;  // chunks per thread and step
     static_assert(PL >= 1 && QL >= 1 && BP % (32 * WP) == 0 && BQ % (32 * WQ) == 0, "tile");
+    static_assert(NT == 64 * WP * WQ * WK, "threads");
 
     static constexpr uint32_t OUT = 0xFFFFFFF0u;
 
     f32x16_t acc[MI][NI];
+
+    // a wave's first row of P and of Q in the tile
+    static SPEC_DEVICE int wave_p0(int wave) { return wave % WP * (BP / WP); }
+    static SPEC_DEVICE int wave_q0(int wave) { return wave / WP % WQ * (BQ / WQ); }
 
     // slot permutation of row p of a Kc tile
     static SPEC_DEVICE int kc_f(int p) { return ROW == 128 ? (p >> 1) & 7 : (p >> 2) & 3; }
@@ -107,7 +113,8 @@ struct Mm {
     static SPEC_DEVICE int ks_f(int k)
     {
         constexpr int CH = R / EPC;
-        return (SZ == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1)) & (CH - 1);
+        if (SZ == 2) return CH == 16 || CH == 32 ? 4 * (k & 3) : CH >= 8 ? 4 * ((k >> 1) & 1) : 0;
+        return CH >= 16 ? 8 * ((k >> 2) & 1) : 0;
     }
 
     // byte offsets of this thread's chunks of a K-step from the step's base; kc:
@@ -192,9 +199,7 @@ struct Mm {
             return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a.x),
                                                           __builtin_bit_cast(f16x8_t, b.x), c, 0, 0, 0);
         } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x[j], b.x[j], c, 0, 0, 0);
-            return c;
+            return c;  // multiply() orders the four products of a fragment itself
         }
     }
 
@@ -212,10 +217,21 @@ struct Mm {
     SPEC_DEVICE void multiply(const Frags &f)
     {
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (SZ == 4) {
+            // a lane's four k in turn, all accumulators in between
 #pragma unroll
-        for (int m = 0; m < MI; ++m)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int n = 0; n < NI; ++n) acc[m][n] = mfma(f.a[m], f.b[n], acc[m][n]);
+                for (int m = 0; m < MI; ++m)
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(f.a[m].x[j], f.b[n].x[j], acc[m][n], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int m = 0; m < MI; ++m)
+#pragma unroll
+                for (int n = 0; n < NI; ++n) acc[m][n] = mfma(f.a[m], f.b[n], acc[m][n]);
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -223,22 +239,50 @@ struct Mm {
     template <int LEFT>
     static SPEC_DEVICE void landed()
     {
-        static_assert(LEFT < 16, "vmcnt");
-        __builtin_amdgcn_s_waitcnt(0x0F70 | LEFT);
+        static_assert(LEFT < 64, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
         __syncthreads();
     }
 
     // The stages of both operands: separate LDS objects, so that a read of one
-    // stage need not wait for the copy into another.
+    // stage need not wait for the copy into another (the first STAGES are used).
     struct Lds {
-        char *p[STAGES], *q[STAGES];
+        char *p[8], *q[8];
+        float4 *red;  // WK > 1: the waves' sums of one accumulator, 16 KB
     };
+
+    // WK > 1: every wave holds the sums over its share of k of the whole tile.
+    // One accumulator at a time they are added, in order of the waves; wave w
+    // keeps rows 8 w .. 8 w + 7 of it (each lane four of them, in elements 0..3).
+    SPEC_DEVICE void join(const Lds &s)
+    {
+        static_assert(WK == 1 || (WK == 4 && WP == 1 && WQ == 1), "shares of k");
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    s.red[(wave * 4 + g) * 64 + lane] = make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1],
+                                                                    acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
+                __syncthreads();
+                float4 r = s.red[wave * 64 + lane];
+#pragma unroll
+                for (int w = 1; w < WK; ++w) {
+                    const float4 o = s.red[(w * 4 + wave) * 64 + lane];
+                    r.x += o.x, r.y += o.y, r.z += o.z, r.w += o.w;
+                }
+                acc[m][n][0] = r.x, acc[m][n][1] = r.y, acc[m][n][2] = r.z, acc[m][n][3] = r.w;
+                __syncthreads();
+            }
+    }
 
     // acc = sum over k in [kb, K)
     SPEC_DEVICE void run(const MmSrc &P, const MmSrc &Q, int64_t kb, int64_t K, const Lds &s)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int p0 = (wave % WP) * (BP / WP), q0 = (wave / WP) * (BQ / WQ);
+        const int p0 = wave_p0(wave), q0 = wave_q0(wave), kw = wave / (WP * WQ) * KW;
         uint32_t vp[PL], vq[QL];
         int kp, kq;
         offsets<BP, PS>(P, vp, kp);
@@ -249,58 +293,95 @@ struct Mm {
             for (int n = 0; n < NI; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.f;
-        if (kb >= K) return;
-        // The fragments of the next half step are read while a half is multiplied.
-        // Before the second half's products its fragments are in registers, so
-        // the stage is free: there the barrier stands, the stage's next step is
-        // requested, and the next stage's first fragments are read behind the
-        // products.  Steps past K are requested too (they arrive as zeros), so
-        // that the number of copies in flight is always the same.
-        constexpr int S = STAGES;
-        Frags f0, f1;
-        auto request = [&](int64_t k, int i) {
-            stage<PS>(P, vp, kp, k, s.p[i]);
-            stage<QS>(Q, vq, kq, k, s.q[i]);
-        };
-        mm_for<0, S>([&](auto I) { request(kb + decltype(I)::value * BK, decltype(I)::value); });
-        landed<(S - 1) * (PL + QL)>();
-        fetch(f0, s.p[0], s.q[0], p0, q0, 0, lane);
-        // S steps per turn, with no way out between them (a copy of every
-        // accumulator would be kept for it)
-        for (int64_t k0 = kb; k0 < K; k0 += S * BK) {
-            mm_for<0, S>([&](auto I) {
-                constexpr int i = decltype(I)::value, j = (i + 1) % S;
-                mm_for<1, KQ>([&](auto Q_) {
-                    constexpr int kk = decltype(Q_)::value;
-                    fetch(kk & 1 ? f1 : f0, s.p[i], s.q[i], p0, q0, kk, lane);
-                    multiply(kk & 1 ? f0 : f1);
+        if (kb < K) {
+            // The next fragments are read while the present ones are multiplied.
+            // Before the last products of a step its fragments are in registers, so
+            // the stage is free: there the barrier stands, the stage's next step is
+            // requested, and the next stage's first fragments are read behind the
+            // products.  Steps past K are requested too (they arrive as zeros), so
+            // that the number of copies in flight is always the same.
+            constexpr int S = STAGES;
+            static_assert(S * KW % 2 == 0 && S <= 8, "stages");
+            Frags f[2];
+            auto request = [&](int64_t k, int i) {
+                stage<PS>(P, vp, kp, k, s.p[i]);
+                stage<QS>(Q, vq, kq, k, s.q[i]);
+            };
+            mm_for<0, S>([&](auto I) { request(kb + decltype(I)::value * BK, decltype(I)::value); });
+            landed<(S - 1) * (PL + QL)>();
+            fetch(f[0], s.p[0], s.q[0], p0, q0, kw, lane);
+            for (int64_t k0 = kb; k0 < K; k0 += S * BK) {
+                mm_for<0, S>([&](auto I) {
+                    constexpr int i = decltype(I)::value, j = (i + 1) % S;
+                    // large tiles run the steps past K of a turn (on zeros): a way out
+                    // between steps would keep a copy of every accumulator
+                    if (MI * NI <= 4 && i > 0 && k0 + i * BK >= K) return;
+                    mm_for<0, KW>([&](auto Q_) {
+                        constexpr int kk = decltype(Q_)::value, cur = (i * KW + kk) & 1;
+                        if constexpr (kk < KW - 1) {
+                            fetch(f[cur ^ 1], s.p[i], s.q[i], p0, q0, kw + kk + 1, lane);
+                        } else {
+                            landed<(S - 2) * (PL + QL)>();
+                            request(k0 + (i + S) * BK, i);
+                            fetch(f[cur ^ 1], s.p[j], s.q[j], p0, q0, kw, lane);
+                        }
+                        multiply(f[cur]);
+                    });
                 });
-                landed<(S - 2) * (PL + QL)>();
-                request(k0 + (i + S) * BK, i);
-                fetch(f0, s.p[j], s.q[j], p0, q0, 0, lane);
-                multiply(f1);
-            });
+            }
+            landed<0>();  // nothing is left to arrive in LDS
         }
-        landed<0>();  // nothing is left to arrive in LDS that others may use
+        if constexpr (WK > 1) join(s);
     }
 
-    // f(p, q, v): four results p .. p + 3 of row q (offsets within the tile)
+    // f(p, q, v): four results p .. p + 3 of row q (offsets within the tile).
+    // A lane's results lie in one row and the lanes' rows differ, so memory would
+    // be met 16 bytes at a time; large tiles pass them through LDS (each wave its
+    // own part of the stages) and meet it in runs of a wave's whole width.
     template <typename F>
-    SPEC_DEVICE void each4(F &&f)
+    SPEC_DEVICE void each4(const Lds &s, F &&f)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int p0 = (wave % WP) * (BP / WP) + 4 * (lane >> 5), q0 = (wave / WP) * (BQ / WQ) + (lane & 31);
+        if constexpr (WK > 1) {
+            const int p0 = 8 * wave + 4 * (lane >> 5), q0 = lane & 31;
 #pragma unroll
-        for (int n = 0; n < NI; ++n)
+            for (int n = 0; n < NI; ++n)
 #pragma unroll
-            for (int m = 0; m < MI; ++m)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[m][n][4 * g + e];
-                    f(p0 + 32 * m + 8 * g, q0 + 32 * n, v);
+                for (int m = 0; m < MI; ++m) {
+                    float v[4] = {acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]};
+                    f(p0 + 32 * m, q0 + 32 * n, v);
                 }
+        } else {
+            constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
+            static_assert(32 * PC * 16 * 2 == P_BYTES && NT / 128 <= 2 * STAGES, "two waves share a stage's operand");
+            const int part = wave >> 1;  // (selected, not indexed: LDS objects have no table of addresses)
+            char *mine = s.p[0];
+            mm_for<1, NT / 128>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                if (part == i) mine = i < STAGES ? s.p[i] : s.q[i < STAGES ? 0 : i - STAGES];
+            });
+            float4 *buf = reinterpret_cast<float4 *>(mine) + (wave & 1) * 32 * PC;
+            const auto slot = [](int q, int c) { return q * PC + (c ^ (PC == 24 ? (q >> 1) & 7 : q & 15)); };
+            const int p0 = wave_p0(wave), q0 = wave_q0(wave);
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                wave_sync();
+#pragma unroll
+                for (int m = 0; m < MI; ++m)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        buf[slot(lane & 31, 8 * m + 2 * g + (lane >> 5))] =
+                            make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
+                wave_sync();
+#pragma unroll
+                for (int i = 0; i < PC / 2; ++i) {
+                    const int u = 64 * i + lane, q = u / PC, c = u % PC;
+                    const float4 r = buf[slot(q, c)];
+                    float v[4] = {r.x, r.y, r.z, r.w};
+                    f(p0 + 4 * c, q0 + 32 * n + q, v);
+                }
+            }
+        }
     }
 };
 
@@ -319,22 +400,65 @@ SPEC_DEVICE void mm_tile(int64_t id, int np, int nq, int &tp, int &tq)
     tp = rest / w;
 }
 
-// Tile shapes: 256 x 256 by eight waves (128 x 64 each, one workgroup per CU:
-// 128 KB of LDS) and 128 x 128 by four (64 x 64 each, two workgroups per CU).
+// Tile shapes.  256 x 256 by eight waves (128 x 64 each, one workgroup per CU:
+// 128 KB of LDS), 192 x 192 by six (96 x 64 each, three stages in 144 KB) and
+// 128 x 128 by four (64 x 64 each, two workgroups per CU).
+// Products with few tiles take 64 x 64 or 32 x 32: each of four waves sums a
+// quarter of every K-step over the whole tile, and the stages are deeper,
+// because a step then lasts less than a copy takes to arrive.
 struct Tile256 {
-    static constexpr int BP = 256, BQ = 256, WP = 2, WQ = 4;
+    static constexpr int BP = 256, BQ = 256, WP = 2, WQ = 4, WK = 1, STAGES = 2, NT = 512;
+};
+struct Tile192 {
+    static constexpr int BP = 192, BQ = 192, WP = 2, WQ = 3, WK = 1, STAGES = 3, NT = 384;
 };
 struct Tile128 {
-    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2;
+    static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2, WK = 1, STAGES = 2, NT = 256;
+};
+struct Tile64 {
+    static constexpr int BP = 64, BQ = 64, WP = 1, WQ = 1, WK = 4, STAGES = 4, NT = 256;
+};
+struct Tile32 {
+    static constexpr int BP = 32, BQ = 32, WP = 1, WQ = 1, WK = 4, STAGES = 8, NT = 256;
 };
 
-template <typename E, typename C, bool PS, bool QS>
-using MmOf = Mm<E, C::BP, C::BQ, C::WP, C::WQ, PS, QS>;
+// declares the LDS of a tile as `lds` (what a shape does not use is not allocated)
+#define MM_STAGES(M)                                                                                              \
+    __shared__ __attribute__((aligned(16))) char P0[M::P_BYTES], P1[M::P_BYTES], Q0[M::Q_BYTES], Q1[M::Q_BYTES];  \
+    __shared__ __attribute__((aligned(16))) char P2[M::P_BYTES], P3[M::P_BYTES], Q2[M::Q_BYTES], Q3[M::Q_BYTES];  \
+    __shared__ __attribute__((aligned(16))) char P4[M::P_BYTES], P5[M::P_BYTES], Q4[M::Q_BYTES], Q5[M::Q_BYTES];  \
+    __shared__ __attribute__((aligned(16))) char P6[M::P_BYTES], P7[M::P_BYTES], Q6[M::Q_BYTES], Q7[M::Q_BYTES];  \
+    __shared__ float4 red_[1024];                                                                                 \
+    const typename M::Lds lds{{P0, P1, P2, P3, P4, P5, P6, P7}, {Q0, Q1, Q2, Q3, Q4, Q5, Q6, Q7}, red_}
 
-// declares the LDS stages of both operands as `lds`
-#define MM_STAGES(M)                                                                                           \
-    __shared__ __attribute__((aligned(16))) char sp0[M::P_BYTES], sp1[M::P_BYTES], sq0[M::Q_BYTES], sq1[M::Q_BYTES]; \
-    const typename M::Lds lds{{sp0, sp1}, {sq0, sq1}}
+// two waves per SIMD: one workgroup of Tile256 or two of the others per CU
+#define MM_BOUNDS(C) __launch_bounds__(C::NT, 2)
 
-// two waves per SIMD: one workgroup of Tile256, two of Tile128 per CU
-#define MM_BOUNDS(C) __launch_bounds__(64 * C::WP * C::WQ, 2)
+// Calls f with the tile shape that takes the least time for the busiest CU:
+// count(edge) tiles dealt to 256 CUs, a tile's time being its area times what
+// that shape takes per result against the largest (16 bits, measured at
+// 4096^3 and, for the small ones, 512^3 and 1024^3; f32 is bound by the MFMA
+// rate in every shape and loses only what small tiles wait for their copies).
+template <typename E, typename N, typename F>
+inline hipError_t mm_pick(N &&count, F &&f)
+{
+    constexpr bool H = sizeof(typename E::st) == 2;
+    const int edge[5] = {256, 192, 128, 64, 32};
+    const double per[5] = {1.0, 1.04, H ? 1.17 : 1.0, H ? 2.1 : 1.2, H ? 6.0 : 2.0};
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < 5; ++i) {
+        const double t = (double)((count((int64_t)edge[i]) + 255) / 256) * edge[i] * edge[i] * per[i];
+        if (i == 0 || t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    switch (best) {
+    case 0: return f(Tile256{});
+    case 1: return f(Tile192{});
+    case 2: return f(Tile128{});
+    case 3: return f(Tile64{});
+    default: return f(Tile32{});
+    }
+}

@@ -42,25 +42,46 @@ namespace {
 inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
 
-constexpr int NORM_BLOCKS = 64;  // partial sums of squares per matrix
+// workgroups of the norm per matrix: about 64 elements per thread
+inline int norm_blocks(int64_t m, int64_t n) { return (int)std::min<int64_t>(512, cdiv_h(m * n, 64 * 256)); }
 
-// grid (NORM_BLOCKS, batch)
+// four consecutive elements j .. j + 3 of a row of n (zero past its end); vec:
+// the row and its neighbours are aligned to four elements
+template <typename G>
+SPEC_DEVICE void row4(const typename G::st *x, int64_t j, int64_t n, int vec, float (&v)[4])
+{
+    if (vec && j + 4 <= n) {
+        const Vec4<G> r = *reinterpret_cast<const Vec4<G> *>(x + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = G::wide(r.v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = j + e < n ? G::wide(x[j + e]) : 0.f;
+    }
+}
+
+// grid (norm_blocks, batch): a wave per row in turn; squares and sums in f64, so
+// that no G overflows
 template <typename G>
 __global__ __launch_bounds__(256) void k_ns_norm(const typename G::st *__restrict__ X, int64_t m, int64_t n, int64_t ld,
-                                                 int64_t stride, double *__restrict__ part)
+                                                 int64_t stride, int vec, double *__restrict__ part)
 {
     __shared__ double red[4];
     const typename G::st *x = X + blockIdx.y * stride;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double s = 0.0;
-    for (int64_t i = blockIdx.x; i < m; i += NORM_BLOCKS)
-        for (int64_t j = threadIdx.x; j < n; j += 256) {
-            const double v = (double)G::wide(x[i * ld + j]);
-            s += v * v;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < m; i += 4 * (int64_t)gridDim.x)
+#pragma unroll 4
+        for (int64_t j = 4 * lane; j < n; j += 256) {
+            float v[4];
+            row4<G>(x + i * ld, j, n, vec, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += (double)v[e] * (double)v[e];
         }
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    if (lane == 0) red[wave] = s;
     __syncthreads();
-    if (threadIdx.x == 0) part[(int64_t)blockIdx.y * NORM_BLOCKS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+    if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
 // X as the kernels hold it: leading part and, for f16, the rest
@@ -93,19 +114,22 @@ SPEC_DEVICE void get_x(const typename E::st *hi, const typename E::st *lo, int64
 // X = G * sx / (norm + eps), padding columns zero.  grid (rows, batch)
 template <typename G, typename E>
 __global__ __launch_bounds__(256) void k_ns_load(const typename G::st *__restrict__ X, int64_t n, int64_t ld,
-                                                 int64_t stride, const double *__restrict__ part, double eps, float sx,
+                                                 int64_t stride, int vec, const double *__restrict__ part, int nb, double eps, float sx,
                                                  typename E::st *__restrict__ hi, typename E::st *__restrict__ lo,
                                                  int64_t xp, int64_t xs)
 {
-    double s = part[(int64_t)blockIdx.y * NORM_BLOCKS + (threadIdx.x & 63)];
+    double s = 0.0;
+    for (int i = threadIdx.x & 63; i < nb; i += 64) s += part[(int64_t)blockIdx.y * nb + i];
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     const float inv = (float)((double)sx / (sqrt(s) + eps));
     const int64_t i = blockIdx.x;
     const typename G::st *x = X + blockIdx.y * stride + i * ld;
+#pragma unroll 2
     for (int64_t j = 4 * threadIdx.x; j < xp; j += 1024) {
         float v[4];
+        row4<G>(x, j, n, vec, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = j + e < n ? G::wide(x[j + e]) * inv : 0.f;
+        for (int e = 0; e < 4; ++e) v[e] *= inv;
         put_x<E>(hi, lo, blockIdx.y * xs + i * xp + j, v);
     }
 }
@@ -114,7 +138,6 @@ __global__ __launch_bounds__(256) void k_ns_load(const typename G::st *__restric
 struct NsDims {
     int64_t rows, cols, xp, xs;  // X
     int64_t r, ap, as;           // A, B
-    int nt;                      // tiles per side of A
 };
 
 // stores four entries (row i, columns j..j+3) of a symmetric matrix with zero
@@ -143,10 +166,10 @@ __global__ MM_BOUNDS(C) void k_ns_gram(const typename E::st *__restrict__ X, NsD
                                                                     typename E::st *__restrict__ A,
                                                                     float *__restrict__ diag)
 {
-    using M = MmOf<E, C, TALL, TALL>;
+    using M = Mm<E, C, TALL, TALL>;
     MM_STAGES(M);
     int ti, tj;
-    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), D.nt, ti, tj);
+    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), (int)((D.r + C::BP - 1) / C::BP), ti, tj);
     const int64_t i0 = (int64_t)ti * C::BQ, j0 = (int64_t)tj * C::BP;
     const typename E::st *x = X + blockIdx.y * D.xs;
     const int64_t step = TALL ? 1 : D.xp, K = TALL ? D.rows : round_up(D.cols, M::EPC);
@@ -154,7 +177,7 @@ __global__ MM_BOUNDS(C) void k_ns_gram(const typename E::st *__restrict__ X, NsD
     const MmSrc Q{(const char *)(x + i0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= real;
         put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i0 + q, j0 + p, ti != tj, v, sa);
@@ -169,10 +192,10 @@ __global__ MM_BOUNDS(C) void k_ns_poly(const typename E::st *__restrict__ A,
                                                                     typename E::st *__restrict__ B,
                                                                     float *__restrict__ diag)
 {
-    using M = MmOf<E, C, false, false>;
+    using M = Mm<E, C, false, false>;
     MM_STAGES(M);
     int ti, tj;
-    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), D.nt, ti, tj);
+    tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), (int)((D.r + C::BP - 1) / C::BP), ti, tj);
     const int64_t i0 = (int64_t)ti * C::BQ, j0 = (int64_t)tj * C::BP;
     const typename E::st *a = A + blockIdx.y * D.as;
     const float *d = da + blockIdx.y * D.r;
@@ -181,7 +204,7 @@ __global__ MM_BOUNDS(C) void k_ns_poly(const typename E::st *__restrict__ A,
     const MmSrc Q{(const char *)(a + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         const int64_t i = i0 + q, j = j0 + p;
         if (i < D.r && j < D.ap) {
             const float di = d[i];
@@ -206,7 +229,7 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
     typename E::st *__restrict__ hi1, typename E::st *__restrict__ lo1, typename O::st *__restrict__ out, int64_t ldo,
     int64_t os, int vec)
 {
-    using M = MmOf<E, C, !TALL, false>;
+    using M = Mm<E, C, !TALL, false>;
     MM_STAGES(M);
     int tp, tq;
     mm_tile(blockIdx.x, np, nq, tp, tq);
@@ -225,7 +248,7 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
     }
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         const int64_t i = i0 + q, j = j0 + p;
         if (i >= D.rows || j >= D.xp) return;
         float x[4];
@@ -277,7 +300,7 @@ NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int t)
         o += up_h(bytes, 256);
         return at;
     };
-    p.part = take(8 * batch * NORM_BLOCKS);
+    p.part = take(8 * batch * norm_blocks(m, n));
     p.da = take(4 * batch * D.r);
     p.db = take(4 * batch * D.r);
     p.a = take(es * batch * D.as);
@@ -323,27 +346,27 @@ template <typename GT, typename E, bool TALL>
 hipError_t ns_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
                   const double *co, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so, char *ws)
 {
-    using C = Tile128;
     using st = typename E::st;
     using gst = typename GT::st;
     constexpr bool F16 = sizeof(st) == 2;
-    NsPlan pl = ns_plan(batch, m, n, F16 ? SPEC_BF16 : SPEC_F32);
-    NsDims &D = pl.D;
-    D.nt = (int)cdiv_h(D.r, C::BP);
+    const NsPlan pl = ns_plan(batch, m, n, F16 ? SPEC_BF16 : SPEC_F32);
+    const NsDims &D = pl.D;
     double *part = (double *)(ws + pl.part);
     float *da = (float *)(ws + pl.da), *db = (float *)(ws + pl.db);
     st *A = (st *)(ws + pl.a), *B = (st *)(ws + pl.b);
     // entries of X are about 1 / sqrt(m n) at first and at most the largest singular value
     const double want = exp2(floor(0.5 * log2((double)m * (double)n)));
     double top = 1.0, sx = F16 ? scale16(1.0, want) : 1.0;
-    hipLaunchKernelGGL(k_ns_norm<GT>, dim3(NORM_BLOCKS, (unsigned)batch), dim3(256), 0, stream, (const gst *)G, m, n, ldg,
-                       sg, part);
+    const int nb = norm_blocks(m, n);
+    const int vin = (uintptr_t)G % (4 * sizeof(gst)) == 0 && ldg % 4 == 0 && sg % 4 == 0;
+    hipLaunchKernelGGL(k_ns_norm<GT>, dim3((unsigned)nb, (unsigned)batch), dim3(256), 0, stream, (const gst *)G, m, n, ldg,
+                       sg, vin, part);
     SPEC_LAUNCH_CHECK();
     hipLaunchKernelGGL((k_ns_load<GT, E>), dim3((unsigned)m, (unsigned)batch), dim3(256), 0, stream, (const gst *)G, n, ldg,
-                       sg, part, eps, (float)sx, (st *)(ws + pl.x[0]), (st *)(ws + pl.xl[0]), D.xp, D.xs);
+                       sg, vin, part, nb, eps, (float)sx, (st *)(ws + pl.x[0]), (st *)(ws + pl.xl[0]), D.xp, D.xs);
     SPEC_LAUNCH_CHECK();
-    const int tri = D.nt * (D.nt + 1) / 2, np = (int)cdiv_h(n, C::BP), nq = (int)cdiv_h(m, C::BQ);
-    const dim3 blk(64 * C::WP * C::WQ), gt((unsigned)tri, (unsigned)batch), ga((unsigned)((int64_t)np * nq), (unsigned)batch);
+    const auto tri = [&](int64_t e) { return cdiv_h(D.r, e) * (cdiv_h(D.r, e) + 1) / 2; };
+    const auto rect = [&](int64_t e) { return cdiv_h(m, e) * cdiv_h(n, e); };
     const int vec = (uintptr_t)O % (4 * sizeof(gst)) == 0 && ldo % 4 == 0 && so % 4 == 0;
     for (int k = 0; k < steps; ++k) {
         const double *c = co + 3 * k;
@@ -354,20 +377,32 @@ hipError_t ns_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, i
         const double sx1 = last ? scale : (F16 ? scale16(next, want) : 1.0);
         const st *hi = (const st *)(ws + pl.x[k & 1]), *lo = (const st *)(ws + pl.xl[k & 1]);
         st *hi1 = (st *)(ws + pl.x[(k & 1) ^ 1]), *lo1 = (st *)(ws + pl.xl[(k & 1) ^ 1]);
-        hipLaunchKernelGGL((k_ns_gram<E, C, TALL>), gt, blk, 0, stream, hi, D, (float)(1.0 / (sx * sx)), (float)sa, A, da);
-        SPEC_LAUNCH_CHECK();
-        hipLaunchKernelGGL((k_ns_poly<E, C>), gt, blk, 0, stream, A, da, D, (float)c[1], (float)c[2], (float)(1.0 / sa),
-                           (float)sb, B, db);
-        SPEC_LAUNCH_CHECK();
-        if (last)
-            hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, true>), ga, blk, 0, stream, hi, lo, B, db, D, np, nq,
-                               (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O, ldo, so,
-                               vec);
-        else
-            hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, false>), ga, blk, 0, stream, hi, lo, B, db, D, np, nq,
-                               (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O, ldo, so,
-                               vec);
-        SPEC_LAUNCH_CHECK();
+        hipError_t e = mm_pick<E>([&](int64_t w) { return tri(w) * batch; }, [&](auto shape) {
+            using C = decltype(shape);
+            const dim3 grid((unsigned)tri(C::BP), (unsigned)batch);
+            hipLaunchKernelGGL((k_ns_gram<E, C, TALL>), grid, dim3(C::NT), 0, stream, hi, D, (float)(1.0 / (sx * sx)),
+                               (float)sa, A, da);
+            SPEC_LAUNCH_CHECK();
+            hipLaunchKernelGGL((k_ns_poly<E, C>), grid, dim3(C::NT), 0, stream, A, da, D, (float)c[1], (float)c[2],
+                               (float)(1.0 / sa), (float)sb, B, db);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+        e = mm_pick<E>([&](int64_t w) { return rect(w) * batch; }, [&](auto shape) {
+            using C = decltype(shape);
+            const int np = (int)cdiv_h(n, C::BP), nq = (int)cdiv_h(m, C::BQ);
+            const dim3 grid((unsigned)((int64_t)np * nq), (unsigned)batch);
+            if (last)
+                hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, true>), grid, dim3(C::NT), 0, stream, hi, lo, B, db, D, np,
+                                   nq, (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O,
+                                   ldo, so, vec);
+            else
+                hipLaunchKernelGGL((k_ns_apply<E, C, TALL, GT, false>), grid, dim3(C::NT), 0, stream, hi, lo, B, db, D, np,
+                                   nq, (float)c[0], (float)(1.0 / sx), (float)(1.0 / sb), (float)sx1, hi1, lo1, (gst *)O,
+                                   ldo, so, vec);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
         top = next;
         sx = sx1;
     }

@@ -129,7 +129,7 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
                                                                   float *__restrict__ ztgt, float2 *__restrict__ part,
                                                                   int64_t ldpart, int tile0)
 {
-    using M = MmOf<E, C, false, false>;
+    using M = Mm<E, C, false, false>;
     MM_STAGES(M);
     __shared__ float2 red[C::WP][C::BQ];
     int tp, tq;
@@ -174,7 +174,7 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
         if (lane < 32) red[wp][q] = make_float2(top, s);
     }
     __syncthreads();
-    for (int q = threadIdx.x; q < C::BQ; q += 64 * C::WP * C::WQ) {
+    for (int q = threadIdx.x; q < C::BQ; q += C::NT) {
         if (t0 + q >= n) break;
         float2 r = red[0][q];
 #pragma unroll
@@ -233,7 +233,7 @@ __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int6
                                                                 const float *__restrict__ pdl,
                                                                 typename E::st *__restrict__ G, int64_t ldg)
 {
-    using M = MmOf<E, C, false, false>;
+    using M = Mm<E, C, false, false>;
     MM_STAGES(M);
     int tp, tq;
     mm_tile(blockIdx.x, np, nq, tp, tq);
@@ -244,7 +244,7 @@ __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int6
     logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
     const int lim = (int)min<int64_t>(C::BP, vn - v0);
     const int lim4 = (int)min<int64_t>(C::BP, round_up(vn, M::EPC) - v0);
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         if (t0 + q >= n || p >= lim4) return;
         const int64_t y = (int64_t)ptgt[t0 + q] - vbase - v0;
         const float l = plse[t0 + q], w = pdl[t0 + q] * scale;
@@ -264,7 +264,7 @@ __global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, in
                                                                  int np, int nq, typename E::st *__restrict__ dW,
                                                                  int64_t lddw, float beta, int vec)
 {
-    using M = MmOf<E, C, true, true>;
+    using M = Mm<E, C, true, true>;
     MM_STAGES(M);
     int tp, tq;
     mm_tile(blockIdx.x, np, nq, tp, tq);
@@ -273,7 +273,7 @@ __global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, in
     const MmSrc Q{(const char *)(G + v0), ldg * M::SZ, (int)min<int64_t>(C::BQ, vn - v0), n};
     M mm;
     mm.run(P, Q, 0, n, lds);
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;
         typename E::st *o = dW + (v0 + q) * lddw + p0 + p;
         if (vec && p + 4 <= P.lim) {
@@ -298,7 +298,7 @@ __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int
                                                                  const int *__restrict__ nvalid, int np, int nq,
                                                                  float *__restrict__ part, int64_t ldp, int first)
 {
-    using M = MmOf<E, C, true, false>;
+    using M = Mm<E, C, true, false>;
     MM_STAGES(M);
     int tp, tq;
     const int64_t tiles = (int64_t)np * nq;
@@ -312,7 +312,7 @@ __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int
     M mm;
     mm.run(P, Q, kb, ke, lds);
     float *out = part + ((int64_t)split * T + t0) * ldp + p0;
-    mm.each4([&](int p, int q, float (&v)[4]) {
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;  // ldp is a multiple of 4: a group of four lies in its row
         float4 *o = reinterpret_cast<float4 *>(out + (int64_t)q * ldp + p);
         float4 r = make_float4(v[0], v[1], v[2], v[3]);
@@ -434,7 +434,7 @@ hipError_t fwd_piece(hipStream_t stream, const XentPlan &pl, const typename E::s
                      int64_t T, float scale, int64_t ldpart, char *ws)
 {
     const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
-    hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, W, ldw,
+    hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W, ldw,
                        vn, v, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq,
                        scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
                        (int)(v / C::BP));
@@ -447,7 +447,7 @@ hipError_t g_piece(hipStream_t stream, const XentPlan &pl, const typename E::st 
 {
     using st = typename E::st;
     const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
-    hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream, W, ldw, vn,
+    hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W, ldw, vn,
                        v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq, scale,
                        (const int *)(ws + pl.ptgt), (const float *)(ws + pl.plse), (const float *)(ws + pl.pdl),
                        (st *)(ws + pl.g), pl.piece);
@@ -461,7 +461,7 @@ hipError_t dw_piece(hipStream_t stream, const XentPlan &pl, int64_t vn, int64_t 
     using st = typename E::st;
     const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(vn, C::BQ);
     const int vec = (uintptr_t)dW % (4 * sizeof(st)) == 0 && lddw % 4 == 0;
-    hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(64 * C::WP * C::WQ), 0, stream,
+    hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream,
                        (const st *)(ws + pl.hp), pl.dp, (const st *)(ws + pl.g), pl.piece, vn, d,
                        (const int *)(ws + pl.nvalid), np, nq, dW, lddw, beta, vec);
     return hipGetLastError();
@@ -473,7 +473,7 @@ hipError_t dh_piece(hipStream_t stream, const XentPlan &pl, const typename E::st
 {
     const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(T, C::BQ);
     const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
-    hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)np * nq * pl.splits)), dim3(64 * C::WP * C::WQ), 0,
+    hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)np * nq * pl.splits)), dim3(C::NT), 0,
                        stream, W, ldw, (const typename E::st *)(ws + pl.g), pl.piece, vn, per, d, T,
                        (const int *)(ws + pl.nvalid), np, nq, (float *)(ws + pl.part), up_h(d, 4), first);
     return hipGetLastError();
