@@ -334,6 +334,20 @@ struct Mm {
         if constexpr (WK > 1) join(s);
     }
 
+    // A wave's part of the stages: room for 32 of its rows in f32.
+    static SPEC_DEVICE float4 *own_part(const Lds &s)
+    {
+        constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
+        static_assert(32 * PC * 16 * 2 == P_BYTES && NT / 128 <= 2 * STAGES, "two waves share a stage's operand");
+        const int wave = threadIdx.x >> 6, part = wave >> 1;
+        char *mine = s.p[0];  // (selected, not indexed: LDS objects have no table of addresses)
+        mm_for<1, NT / 128>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            if (part == i) mine = i < STAGES ? s.p[i] : s.q[i < STAGES ? 0 : i - STAGES];
+        });
+        return reinterpret_cast<float4 *>(mine) + (wave & 1) * 32 * PC;
+    }
+
     // f(p, q, v): four results p .. p + 3 of row q (offsets within the tile).
     // A lane's results lie in one row and the lanes' rows differ, so memory would
     // be met 16 bytes at a time; large tiles pass them through LDS (each wave its
@@ -353,14 +367,7 @@ struct Mm {
                 }
         } else {
             constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
-            static_assert(32 * PC * 16 * 2 == P_BYTES && NT / 128 <= 2 * STAGES, "two waves share a stage's operand");
-            const int part = wave >> 1;  // (selected, not indexed: LDS objects have no table of addresses)
-            char *mine = s.p[0];
-            mm_for<1, NT / 128>([&](auto I) {
-                constexpr int i = decltype(I)::value;
-                if (part == i) mine = i < STAGES ? s.p[i] : s.q[i < STAGES ? 0 : i - STAGES];
-            });
-            float4 *buf = reinterpret_cast<float4 *>(mine) + (wave & 1) * 32 * PC;
+            float4 *buf = own_part(s);
             const auto slot = [](int q, int c) { return q * PC + (c ^ (PC == 24 ? (q >> 1) & 7 : q & 15)); };
             const int p0 = wave_p0(wave), q0 = wave_q0(wave);
 #pragma unroll
@@ -379,6 +386,54 @@ struct Mm {
                     const float4 r = buf[slot(q, c)];
                     float v[4] = {r.x, r.y, r.z, r.w};
                     f(p0 + 4 * c, q0 + 32 * n + q, v);
+                }
+            }
+        }
+    }
+
+    // f(p, q, v): the results of rows q .. q + 3 at p: the tile of the transposed
+    // product, in runs of 32 rows
+    template <typename F>
+    SPEC_DEVICE void each4_across(const Lds &s, F &&f)
+    {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int p0 = wave_p0(wave), q0 = wave_q0(wave);
+        if constexpr (WK > 1) {
+            // rows 8 wave + 4 h .. + 3 of each 32 x 32 block are in this lane's column
+            float *buf = reinterpret_cast<float *>(s.red) + wave * 8 * 32;
+#pragma unroll
+            for (int n = 0; n < NI; ++n)
+#pragma unroll
+                for (int m = 0; m < MI; ++m) {
+                    wave_sync();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) buf[(4 * (lane >> 5) + e) * 32 + (lane & 31)] = acc[m][n][e];
+                    wave_sync();
+                    const float4 r = reinterpret_cast<const float4 *>(buf)[lane];
+                    float v[4] = {r.x, r.y, r.z, r.w};
+                    f(32 * m + 8 * wave + (lane >> 3), 32 * n + 4 * (lane & 7), v);
+                }
+        } else {
+            // rows p of 32 floats; p and p + 4 are written together, so bit 0 of the
+            // row is flipped by bit 2 to put them on different banks
+            float *buf = reinterpret_cast<float *>(own_part(s));
+            const auto row = [](int p) { return (p ^ ((p >> 2) & 1)) * 32; };
+            constexpr int PR = BP / WP;
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                wave_sync();
+#pragma unroll
+                for (int m = 0; m < MI; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        buf[row(32 * m + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) + (lane & 31)] = acc[m][n][e];
+                wave_sync();
+#pragma unroll
+                for (int i = 0; i < PR / 8; ++i) {
+                    const int p = 8 * i + (lane >> 3);
+                    const float4 r = *reinterpret_cast<const float4 *>(buf + row(p) + 4 * (lane & 7));
+                    float v[4] = {r.x, r.y, r.z, r.w};
+                    f(p0 + p, q0 + 32 * n + 4 * (lane & 7), v);
                 }
             }
         }

@@ -140,23 +140,20 @@ struct NsDims {
     int64_t r, ap, as;           // A, B
 };
 
-// stores four entries (row i, columns j..j+3) of a symmetric matrix with zero
-// diagonal, mirrored for tiles below the diagonal; di receives the diagonal
+// stores four entries (row i, columns j..j+3) of a symmetric matrix, its diagonal
+// apart in diag; on: whether the entries may lie on the diagonal
 template <typename E>
-SPEC_DEVICE void put_sym(typename E::st *A, float *diag, const NsDims &D, int64_t i, int64_t j, bool below,
+SPEC_DEVICE void put_sym(typename E::st *A, float *diag, const NsDims &D, int64_t i, int64_t j, bool on,
                          const float (&v)[4], float scale)
 {
+    if (i >= D.r || j >= D.ap) return;
     Vec4<E> o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (!below && i == j + e && i < D.r) diag[i] = v[e];
-        o.v[e] = !below && i == j + e ? (typename E::st)0 : E::round(v[e] * scale);
+        if (on && i == j + e) diag[i] = v[e];
+        o.v[e] = on && i == j + e ? (typename E::st)0 : E::round(v[e] * scale);
     }
-    if (i < D.r && j < D.ap) *reinterpret_cast<Vec4<E> *>(A + i * D.ap + j) = o;
-    if (below && i < D.ap) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) A[(j + e) * D.ap + i] = o.v[e];
-    }
+    *reinterpret_cast<Vec4<E> *>(A + i * D.ap + j) = o;
 }
 
 // grid (tiles on and below the diagonal, batch).  real: 1 / sx^2
@@ -177,11 +174,13 @@ __global__ MM_BOUNDS(C) void k_ns_gram(const typename E::st *__restrict__ X, NsD
     const MmSrc Q{(const char *)(x + i0 * step), D.xp * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
+    const auto put = [&](int64_t i, int64_t j, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= real;
-        put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i0 + q, j0 + p, ti != tj, v, sa);
-    });
+        put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti == tj, v, sa);
+    };
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) { put(i0 + q, j0 + p, v); });
+    if (ti != tj) mm.each4_across(lds, [&](int p, int q, float (&v)[4]) { put(j0 + p, i0 + q, v); });
 }
 
 // B = b A + c A^2 with A = diag(da) + E; ea = 1 / sa
@@ -204,20 +203,20 @@ __global__ MM_BOUNDS(C) void k_ns_poly(const typename E::st *__restrict__ A,
     const MmSrc Q{(const char *)(a + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
-        const int64_t i = i0 + q, j = j0 + p;
-        if (i < D.r && j < D.ap) {
-            const float di = d[i];
-            const Vec4<E> x = *reinterpret_cast<const Vec4<E> *>(a + i * D.ap + j);
+    const auto put = [&](int64_t i, int64_t j, float (&v)[4]) {
+        if (i >= D.r || j >= D.ap) return;
+        const float di = d[i];
+        const Vec4<E> x = *reinterpret_cast<const Vec4<E> *>(a + i * D.ap + j);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float dj = j + e < D.r ? d[j + e] : 0.f;
-                const float aa = c * (v[e] * ea * ea);
-                v[e] = i == j + e ? b * di + (c * di * di + aa) : (b + c * (di + dj)) * (E::wide(x.v[e]) * ea) + aa;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const float dj = j + e < D.r ? d[j + e] : 0.f;
+            const float aa = c * (v[e] * ea * ea);
+            v[e] = i == j + e ? b * di + (c * di * di + aa) : (b + c * (di + dj)) * (E::wide(x.v[e]) * ea) + aa;
         }
-        put_sym<E>(B + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti != tj, v, sb);
-    });
+        put_sym<E>(B + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti == tj, v, sb);
+    };
+    mm.each4(lds, [&](int p, int q, float (&v)[4]) { put(i0 + q, j0 + p, v); });
+    if (ti != tj) mm.each4_across(lds, [&](int p, int q, float (&v)[4]) { put(j0 + p, i0 + q, v); });
 }
 
 // The next X (scaled by sx1), or O = scale X in the last step.

@@ -11,7 +11,9 @@
 //
 // Rows without a target (outside [0, V)) are dropped before the products: the
 // rest of H is packed, so they cost nothing, and whatever they hold (NaN
-// included) reaches no output.
+// included) reaches no output.  The number of rows left is known on the device
+// only: grids are sized for all of them, and the workgroups of the first tiles
+// (counted with the number left, so that they spread over the XCDs) do the work.
 //
 //   k_xent_pack      positions of the rows with a target, their rows of H, packed
 //   k_xent_wpack     a piece of W with 16-byte rows (only where W has none)
@@ -125,17 +127,18 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
                                                                   int64_t vn, int64_t vbase,
                                                                   const typename E::st *__restrict__ Hp, int64_t dp,
                                                                   int64_t dk, const int *__restrict__ nvalid, int np,
-                                                                  int nq, float scale, const int *__restrict__ ptgt,
+                                                                  float scale, const int *__restrict__ ptgt,
                                                                   float *__restrict__ ztgt, float2 *__restrict__ part,
                                                                   int64_t ldpart, int tile0)
 {
     using M = Mm<E, C, false, false>;
     MM_STAGES(M);
     __shared__ float2 red[C::WP][C::BQ];
+    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ;
     int tp, tq;
+    if (blockIdx.x >= (unsigned)(np * nq)) return;
     mm_tile(blockIdx.x, np, nq, tp, tq);
-    const int n = *nvalid, t0 = tq * C::BQ;
-    if (t0 >= n) return;
+    const int t0 = tq * C::BQ;
     const int64_t v0 = (int64_t)tp * C::BP;
     M mm;
     logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
@@ -146,18 +149,31 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
     for (int b = 0; b < M::NI; ++b) {
         const int q = q0 + 32 * b;
         const bool in = t0 + q < n;
-        const int64_t y = in ? (int64_t)ptgt[t0 + q] - vbase - v0 : -1;  // the target's place in this tile
+#pragma unroll
+        for (int m = 0; m < M::MI; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mm.acc[m][b][e] *= scale;
+        if (lim < C::BP) {  // the vocabulary ends in this tile
+#pragma unroll
+            for (int m = 0; m < M::MI; ++m)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (p0 + 32 * m + 8 * (e >> 2) + (e & 3) >= lim) mm.acc[m][b][e] = -INFINITY;
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int m = 0; m < M::MI; ++m)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int p = p0 + 32 * m + 8 * (e >> 2) + (e & 3);
-                const float z = p < lim ? scale * mm.acc[m][b][e] : -INFINITY;
-                mm.acc[m][b][e] = z;
-                top = fmaxf(top, z);
-                if (p == y && p < lim) ztgt[t0 + q] = z;
-            }
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, mm.acc[m][b][e]);
+        // few tiles hold a target of one of their rows
+        const int64_t y = in ? (int64_t)ptgt[t0 + q] - vbase - v0 - p0 : -1;  // its place from this lane's first
+        if (__any(y >= 0 && y < C::BP / C::WP)) {
+#pragma unroll
+            for (int m = 0; m < M::MI; ++m)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (y == 32 * m + 8 * (e >> 2) + (e & 3)) ztgt[t0 + q] = mm.acc[m][b][e];
+        }
         {
             float a = top, c = top;
             halfswap32(a, c);
@@ -228,17 +244,18 @@ __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int6
                                                                 int64_t vn, int64_t vbase,
                                                                 const typename E::st *__restrict__ Hp, int64_t dp,
                                                                 int64_t dk, const int *__restrict__ nvalid, int np,
-                                                                int nq, float scale, const int *__restrict__ ptgt,
+                                                                float scale, const int *__restrict__ ptgt,
                                                                 const float *__restrict__ plse,
                                                                 const float *__restrict__ pdl,
                                                                 typename E::st *__restrict__ G, int64_t ldg)
 {
     using M = Mm<E, C, false, false>;
     MM_STAGES(M);
+    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ;
     int tp, tq;
+    if (blockIdx.x >= (unsigned)(np * nq)) return;
     mm_tile(blockIdx.x, np, nq, tp, tq);
-    const int n = *nvalid, t0 = tq * C::BQ;
-    if (t0 >= n) return;
+    const int t0 = tq * C::BQ;
     const int64_t v0 = (int64_t)tp * C::BP;
     M mm;
     logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
@@ -295,17 +312,17 @@ template <typename E, typename C>
 __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int64_t ldw,
                                                                  const typename E::st *__restrict__ G, int64_t ldg,
                                                                  int64_t vn, int64_t per, int64_t d, int64_t T,
-                                                                 const int *__restrict__ nvalid, int np, int nq,
+                                                                 const int *__restrict__ nvalid, int np, int splits,
                                                                  float *__restrict__ part, int64_t ldp, int first)
 {
     using M = Mm<E, C, true, false>;
     MM_STAGES(M);
+    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ, tiles = np * nq;
     int tp, tq;
-    const int64_t tiles = (int64_t)np * nq;
-    const int split = (int)(blockIdx.x / tiles);
+    if (blockIdx.x >= (unsigned)(tiles * splits)) return;
+    const int split = (int)blockIdx.x / tiles;
     mm_tile(blockIdx.x % tiles, np, nq, tp, tq);
-    const int n = *nvalid, t0 = tq * C::BQ;
-    if (t0 >= n) return;
+    const int t0 = tq * C::BQ;
     const int64_t p0 = (int64_t)tp * C::BP, kb = split * per, ke = min<int64_t>(vn, kb + per);
     const MmSrc P{(const char *)(W + p0), ldw * M::SZ, (int)min<int64_t>(C::BP, d - p0), ke};
     const MmSrc Q{(const char *)(G + (int64_t)t0 * ldg), ldg * M::SZ, min(C::BQ, n - t0), round_up(ke, M::EPC)};
@@ -340,7 +357,9 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
 
 // ------------------------------------------------------------------ sizes
 
-constexpr int64_t XENT_G_BYTES = (int64_t)128 << 20;  // a piece's gradient stays in the 256 MB last-level cache
+// Bytes of a piece's gradient G.  Larger pieces add into the f32 partial dH less
+// often (100 MB read and written per piece at 6144 x 4096).
+constexpr int64_t XENT_G_BYTES = (int64_t)256 << 20;
 
 struct XentPlan {
     int64_t dp;      // row of packed H and W: d rounded up to 64 elements
@@ -435,7 +454,7 @@ hipError_t fwd_piece(hipStream_t stream, const XentPlan &pl, const typename E::s
 {
     const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
     hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W, ldw,
-                       vn, v, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq,
+                       vn, v, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np,
                        scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
                        (int)(v / C::BP));
     return hipGetLastError();
@@ -448,7 +467,7 @@ hipError_t g_piece(hipStream_t stream, const XentPlan &pl, const typename E::st 
     using st = typename E::st;
     const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
     hipLaunchKernelGGL((k_xent_g<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W, ldw, vn,
-                       v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, nq, scale,
+                       v, (const st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np, scale,
                        (const int *)(ws + pl.ptgt), (const float *)(ws + pl.plse), (const float *)(ws + pl.pdl),
                        (st *)(ws + pl.g), pl.piece);
     return hipGetLastError();
@@ -475,7 +494,7 @@ hipError_t dh_piece(hipStream_t stream, const XentPlan &pl, const typename E::st
     const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
     hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)np * nq * pl.splits)), dim3(C::NT), 0,
                        stream, W, ldw, (const typename E::st *)(ws + pl.g), pl.piece, vn, per, d, T,
-                       (const int *)(ws + pl.nvalid), np, nq, (float *)(ws + pl.part), up_h(d, 4), first);
+                       (const int *)(ws + pl.nvalid), np, pl.splits, (float *)(ws + pl.part), up_h(d, 4), first);
     return hipGetLastError();
 }
 
