@@ -547,7 +547,7 @@ int spec_timing_read(int kernel, double *total_ms, int64_t *launches);
 /* Embedding lookup:  Y[i] = scale * E[ids[i]]  (computed in f32, rounded once).
  * E: [V][lde], Y: [n][ldy], both of type t = SPEC_BF16 or SPEC_F32 (else
  * SPEC_EUNSUPPORTED), d values per row; Y must not overlap E.
- * Requires 1 <= V < 2^31, 1 <= d <= 2^20, 0 <= n < 2^31, lde, ldy >= d; else SPEC_EINVAL. */
+ * Requires 1 <= V < 2^31 - 1, 1 <= d <= 2^20, 0 <= n < 2^31, lde, ldy >= d; else SPEC_EINVAL. */
 int spec_embed(void *stream, const void *E, int t, int64_t V, int64_t d, int64_t lde, const void *ids, int idt,
                int64_t n, double scale, void *Y, int64_t ldy);
 
@@ -574,8 +574,9 @@ int spec_embed_grad(void *stream, const void *dY, int yt, int64_t n, int64_t V, 
  * A row whose logits hold NaN or +inf has loss and lse NaN.
  * ws: device workspace of spec_linear_xent_workspace(T, V, d, t) bytes (256-byte
  * aligned): packed H, one (max, sum) pair per row and 128 logits.
- * Requires 1 <= V < 2^31, 1 <= d <= 2^20, 0 <= T <= 2^22, ldh, ldw >= d and
- * <= 2^20 + 64; else SPEC_EINVAL.  16-byte aligned rows of W are read in place,
+ * Requires 1 <= V < 2^31 - 1, 1 <= d <= 2^20, 0 <= T <= 2^22, ldh, ldw >= d and
+ * <= 2^20 + 64 (else SPEC_EINVAL), and fewer than 2^30 tiles of 128 x 128 logits
+ * (else SPEC_EUNSUPPORTED).  16-byte aligned rows of W are read in place,
  * others are copied a piece at a time. */
 int spec_linear_xent_workspace(int64_t T, int64_t V, int64_t d, int t, size_t *bytes);
 

@@ -64,7 +64,11 @@ int check_xent_sizes(int64_t T, int64_t V, int64_t d, int t)
 {
     if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
     if (T > ((int64_t)1 << 22)) return SPEC_EINVAL;
-    return check_rows(T, V, d);
+    const int st = check_rows(T, V, d);
+    if (st != SPEC_OK) return st;
+    // tiles of 128 x 128 logits are counted in 31 bits
+    if ((T + 127) / 128 * ((V + 127) / 128) >= ((int64_t)1 << 30)) return SPEC_EUNSUPPORTED;
+    return SPEC_OK;
 }
 
 int check_ortho_sizes(int64_t batch, int64_t m, int64_t n, int t)

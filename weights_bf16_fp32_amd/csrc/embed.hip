@@ -15,10 +15,10 @@
 // in a neighbour's share, to be joined by a second pass.
 //
 //   k_embed      lookup
-//   k_sort_hist  digits per share of the positions
-//   k_sort_scan  first place of every (digit, share)
+//   k_eg_start   zero rows; beside them, up to 16384 positions sorted by one workgroup
+//   k_sort_hist  more positions: digits per share of the positions,
+//   k_sort_scan  first place of every (digit, share),
 //   k_sort_move  positions to their places
-//   k_eg_fill    zero rows
 //   k_eg_sum     sums over sorted positions
 //   k_eg_join    sums of rows that cross shares
 #include <algorithm>
@@ -161,18 +161,130 @@ __global__ __launch_bounds__(256) void k_sort_move(const int *__restrict__ keys,
     }
 }
 
+// ------------------------------------------------------------------ one workgroup's sort
+
+constexpr int ONE_MAX = 16384;  // positions
+constexpr int ONE_BITS = 9;     // of the key per pass
+constexpr int ONE_ROUNDS = ONE_MAX / 1024;
+
+struct OneLds {
+    int cnt[16][1 << ONE_BITS];
+    int buf[ONE_MAX];
+    int wsum[8];
+};
+
+// The positions in order of their keys, by 1024 threads: keys and positions stay
+// in registers (wave w holds the places w 64 R .. in rounds of 64) and change
+// places through LDS once per pass.
+SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n, int passes, int *okeys, int *oidx)
+{
+    constexpr int ND = 1 << ONE_BITS;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int R = (n + 1023) / 1024;
+    int key[ONE_ROUNDS], idx[ONE_ROUNDS], at[ONE_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ONE_ROUNDS; ++r) {
+        const int i = (wave * R + r) * 64 + lane;
+        idx[r] = i;
+        key[r] = r < R && i < n ? first_key(ids, is64, i, V) : 0;
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * ONE_BITS;
+        for (int i = tid; i < 16 * ND; i += 1024) s.cnt[i / ND][i % ND] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ONE_ROUNDS; ++r) {
+            if (r >= R) break;
+            const bool in = (wave * R + r) * 64 + lane < n;
+            const int dg = (key[r] >> shift) & (ND - 1);
+            uint64_t same = __ballot(in);  // lanes with this lane's digit
+#pragma unroll
+            for (int k = 0; k < ONE_BITS; ++k) {
+                const uint64_t m = __ballot((dg >> k) & 1);
+                same &= (dg >> k) & 1 ? m : ~m;
+            }
+            const int before = __popcll(same & ((1ull << lane) - 1));
+            at[r] = in ? s.cnt[wave][dg] + before : 0;
+            wave_sync();
+            if (in && before == 0) s.cnt[wave][dg] += __popcll(same);
+            wave_sync();
+        }
+        __syncthreads();
+        // places: digits in order, and of one digit the waves in order
+        int total = 0;
+        if (tid < ND)
+            for (int w = 0; w < 16; ++w) {
+                const int x = s.cnt[w][tid];
+                s.cnt[w][tid] = total;
+                total += x;
+            }
+        int inc = total;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 63 && wave < 8) s.wsum[wave] = inc;
+        __syncthreads();
+        if (tid < ND) {
+            int base = inc - total;
+            for (int w = 0; w < wave; ++w) base += s.wsum[w];
+            for (int w = 0; w < 16; ++w) s.cnt[w][tid] += base;
+        }
+        __syncthreads();
+        const bool last = pass == passes - 1;
+#pragma unroll
+        for (int r = 0; r < ONE_ROUNDS; ++r) {
+            if (r >= R || (wave * R + r) * 64 + lane >= n) continue;
+            at[r] += s.cnt[wave][(key[r] >> shift) & (ND - 1)];
+            if (last) {
+                okeys[at[r]] = key[r];
+                oidx[at[r]] = idx[r];
+            } else {
+                s.buf[at[r]] = key[r];
+            }
+        }
+        if (last) return;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ONE_ROUNDS; ++r) {
+            const int i = (wave * R + r) * 64 + lane;
+            if (r < R && i < n) key[r] = s.buf[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ONE_ROUNDS; ++r)
+            if (r < R && (wave * R + r) * 64 + lane < n) s.buf[at[r]] = idx[r];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ONE_ROUNDS; ++r) {
+            const int i = (wave * R + r) * 64 + lane;
+            if (r < R && i < n) idx[r] = s.buf[i];
+        }
+    }
+}
+
 // ------------------------------------------------------------------ sums
 
 constexpr int EG_SHARE = 32;  // sorted positions per workgroup
+constexpr int EG_AHEAD = 8;   // rows in flight per thread
 
+// Workgroup 0 sorts (sort != 0); the others write zeros over dE's rows, which
+// take as long as their bytes: the sort runs beside them.
 template <typename O, int VEC>
-__global__ __launch_bounds__(256) void k_eg_fill(typename O::st *__restrict__ dE, int64_t V, int64_t d, int64_t ldd)
+__global__ __launch_bounds__(1024) void k_eg_start(const void *__restrict__ ids, int is64, int64_t V, int n, int passes,
+                                                   int sort, int *__restrict__ okeys, int *__restrict__ oidx,
+                                                   typename O::st *__restrict__ dE, int64_t d, int64_t ldd)
 {
-    const int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (v >= V) return;
+    __shared__ OneLds lds;
+    if (sort && blockIdx.x == 0) {
+        sort_one(lds, ids, is64, V, n, passes, okeys, oidx);
+        return;
+    }
+    const int64_t first = (int64_t)(blockIdx.x - sort) * 16 + (threadIdx.x >> 6), step = 16 * (int64_t)(gridDim.x - sort);
     const Pack<typename O::st, VEC> z{};
-    for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64)
-        *reinterpret_cast<Pack<typename O::st, VEC> *>(dE + v * ldd + c) = z;
+    for (int64_t v = first; v < V; v += step)
+        for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64)
+            *reinterpret_cast<Pack<typename O::st, VEC> *>(dE + v * ldd + c) = z;
 }
 
 template <typename O, int VEC>
@@ -186,39 +298,64 @@ SPEC_DEVICE void eg_put(typename O::st *row, int64_t c, const float (&s)[VEC], f
 }
 
 // grid (shares, column blocks of 256 VEC).  head[share] / tail[share]: the sum
-// of the share's first / last row where it began before / goes on after
+// of the share's first / last row where it began before / goes on after.
+// Positions are taken EG_AHEAD at a time, their rows requested together.
 template <typename E, typename O, int VEC>
 __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict__ dY, int64_t d, int64_t ldy,
                                                 const int *__restrict__ keys, const int *__restrict__ idx, int64_t n,
                                                 int64_t V, float scale, int add, typename O::st *__restrict__ dE,
                                                 int64_t ldd, float *__restrict__ head, float *__restrict__ tail)
 {
+    using P = Pack<typename E::st, VEC>;
     const int64_t b = (int64_t)blockIdx.x * EG_SHARE, e = min<int64_t>(n, b + EG_SHARE);
     const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
-    if (c >= d) return;
+    if (c >= d || keys[b] >= V) return;
     float s[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[k] = 0.f;
     bool open = b > 0 && keys[b - 1] == keys[b];  // the row began before this share
-    int64_t i = b;
-    while (i < e) {
-        const int key = keys[i];
-        if (key >= V) return;
+    const auto leave = [&](float *p) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) s[k] = 0.f;
-        for (; i < e && keys[i] == key; ++i) {
-            const Pack<typename E::st, VEC> x =
-                *reinterpret_cast<const Pack<typename E::st, VEC> *>(dY + (int64_t)idx[i] * ldy + c);
+        for (int k = 0; k < VEC; ++k) p[(int64_t)blockIdx.x * d + c + k] = s[k];
+    };
+    int cur = keys[b];
+    for (int64_t i0 = b; i0 < e; i0 += EG_AHEAD) {
+        P x[EG_AHEAD];
+        int key[EG_AHEAD];
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) s[k] += E::wide(x.v[k]);
+        for (int j = 0; j < EG_AHEAD; ++j) {
+            const int64_t i = min<int64_t>(i0 + j, e - 1);
+            key[j] = i0 + j < e ? keys[i] : (int)V;
+            // (positions without a token have the last keys; their rows are not read)
+            x[j] = key[j] < V ? *reinterpret_cast<const P *>(dY + (int64_t)idx[i] * ldy + c) : P{};
         }
-        const bool goes_on = i == e && e < n && keys[e] == key;
-        if (open || goes_on) {
-            float *p = (open ? head : tail) + (int64_t)blockIdx.x * d + c;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) p[k] = s[k];
-        } else {
-            eg_put<O, VEC>(dE + key * ldd, c, s, scale, add);
+        for (int j = 0; j < EG_AHEAD; ++j) {
+            if (key[j] != cur) {
+                if (cur < V) {
+                    if (open)
+                        leave(head);
+                    else if (i0 + j < e || e == n || keys[e] != cur)
+                        eg_put<O, VEC>(dE + cur * ldd, c, s, scale, add);
+                    else
+                        leave(tail);
+                }
+                open = false;
+                cur = key[j];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) s[k] += E::wide(x[j].v[k]);
         }
-        open = false;
+    }
+    if (cur < V) {
+        if (open)
+            leave(head);
+        else if (e == n || keys[e] != cur)
+            eg_put<O, VEC>(dE + cur * ldd, c, s, scale, add);
+        else
+            leave(tail);
     }
 }
 
@@ -234,18 +371,27 @@ __global__ __launch_bounds__(256) void k_eg_join(int64_t d, const int *__restric
     const int key = keys[e - 1];
     if (key >= V || keys[e] != key) return;
     if (keys[b] == key && b > 0 && keys[b - 1] == key) return;  // began earlier
+    // the shares it goes through: those whose first position still has its key
+    int64_t lo = blockIdx.x + 1, hi = (n - 1) / EG_SHARE;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (keys[mid * EG_SHARE] == key)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
     float s[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) s[k] = tail[(int64_t)blockIdx.x * d + c + k];
-    for (int64_t f = e; f < n && keys[f] == key; f += EG_SHARE) {
-        const float *p = head + f / EG_SHARE * d + c;
+#pragma unroll 8
+    for (int64_t f = blockIdx.x + 1; f <= lo; ++f)
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) s[k] += p[k];
-    }
+        for (int k = 0; k < VEC; ++k) s[k] += head[f * d + c + k];
     eg_put<O, VEC>(dE + key * ldd, c, s, scale, add);
 }
 
 struct EgPlan {
+    bool one;  // one workgroup sorts
     int nshare, passes, bits;
     int64_t key[2], idx[2], hist, head, tail, total;
 };
@@ -255,7 +401,8 @@ EgPlan eg_plan(int64_t n, int64_t V, int64_t d)
     EgPlan p{};
     int kb = 1;  // bits of the largest key, V
     while ((V >> kb) != 0) ++kb;
-    p.passes = (int)cdiv_h(kb, DIGIT_MAX);
+    p.one = n <= ONE_MAX;
+    p.passes = (int)cdiv_h(kb, p.one ? ONE_BITS : DIGIT_MAX);
     p.bits = (int)cdiv_h(kb, p.passes);
     const int64_t nn = std::max<int64_t>(n, 1);
     p.nshare = (int)cdiv_h(nn, SORT_SHARE);
@@ -282,13 +429,18 @@ hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int6
 {
     const EgPlan p = eg_plan(n, V, d);
     typename O::st *out = (typename O::st *)dE;
-    if (!add) {
-        hipLaunchKernelGGL((k_eg_fill<O, VEC>), dim3((unsigned)cdiv_h(V, 4)), dim3(256), 0, stream, out, V, d, ldd);
+    const int sort = p.one && n > 0;
+    const int fill = add ? 0 : (int)std::min<int64_t>(cdiv_h(V, 16), 2048);
+    const int last = p.one ? 0 : (p.passes + 1) & 1;
+    int *okeys = (int *)(ws + p.key[last]), *oidx = (int *)(ws + p.idx[last]);
+    if (sort + fill > 0) {
+        hipLaunchKernelGGL((k_eg_start<O, VEC>), dim3((unsigned)(sort + fill)), dim3(1024), 0, stream, ids, is64, V, (int)n,
+                           p.passes, sort, okeys, oidx, out, d, ldd);
         SPEC_LAUNCH_CHECK();
     }
     if (n == 0) return hipSuccess;
     int *hist = (int *)(ws + p.hist);
-    for (int k = 0; k < p.passes; ++k) {
+    for (int k = 0; k < p.passes && !p.one; ++k) {
         const int *keys = k == 0 ? nullptr : (const int *)(ws + p.key[(k + 1) & 1]);
         const int *idx = k == 0 ? nullptr : (const int *)(ws + p.idx[(k + 1) & 1]);
         hipLaunchKernelGGL(k_sort_hist, dim3((unsigned)p.nshare), dim3(256), 0, stream, keys, ids, is64, V, n, k * p.bits,
@@ -300,7 +452,7 @@ hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int6
                            k * p.bits, p.bits, p.nshare, hist, (int *)(ws + p.key[k & 1]), (int *)(ws + p.idx[k & 1]));
         SPEC_LAUNCH_CHECK();
     }
-    const int *keys = (const int *)(ws + p.key[(p.passes + 1) & 1]), *idx = (const int *)(ws + p.idx[(p.passes + 1) & 1]);
+    const int *keys = okeys, *idx = oidx;
     const dim3 grid((unsigned)cdiv_h(n, EG_SHARE), (unsigned)cdiv_h(d, 256 * VEC));
     float *head = (float *)(ws + p.head), *tail = (float *)(ws + p.tail);
     hipLaunchKernelGGL((k_eg_sum<E, O, VEC>), grid, dim3(256), 0, stream, (const typename E::st *)dY, d, ldy, keys, idx, n,
@@ -344,15 +496,17 @@ hipError_t launch_embed_grad(hipStream_t stream, const void *dY, int yt, int64_t
 {
     const int64_t ys = yt == SPEC_BF16 ? 2 : 4, es = et == SPEC_BF16 ? 2 : 4;
     char *w = (char *)ws;
-    // four elements per thread where both sides allow it
-    const bool vec = d % 4 == 0 && ldy % 4 == 0 && ldd % 4 == 0 && (uintptr_t)dY % (4 * ys) == 0 &&
-                     (uintptr_t)dE % (4 * es) == 0;
+    // eight or four elements per thread where both sides are aligned to them
+    const auto can = [&](int64_t k) {
+        return d % k == 0 && ldy % k == 0 && ldd % k == 0 && (uintptr_t)dY % (k * ys) == 0 && (uintptr_t)dE % (k * es) == 0;
+    };
     if (yt == SPEC_BF16 && et == SPEC_BF16)
-        return vec ? eg_run<ElBF16, ElBF16, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
-                   : eg_run<ElBF16, ElBF16, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+        return can(8)   ? eg_run<ElBF16, ElBF16, 8>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+               : can(4) ? eg_run<ElBF16, ElBF16, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+                        : eg_run<ElBF16, ElBF16, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
     if (yt == SPEC_BF16)
-        return vec ? eg_run<ElBF16, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
-                   : eg_run<ElBF16, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
-    return vec ? eg_run<ElF32, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
-               : eg_run<ElF32, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+        return can(4) ? eg_run<ElBF16, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+                      : eg_run<ElBF16, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
+    return can(4) ? eg_run<ElF32, ElF32, 4>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w)
+                  : eg_run<ElF32, ElF32, 1>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, w);
 }

@@ -21,8 +21,8 @@
 //   k_xent_join      lse and loss of every row
 //   k_xent_g         logits tile -> G tile
 //   k_xent_dw        dW of the piece
-//   k_xent_dh        partial dH of the piece (f32, by split)
-//   k_xent_dh_out    dH from the partials, zero rows for rows without a target
+//   k_xent_dh        dH of the piece, added to the sums so far (f32)
+//   k_xent_dh_out    dH from the sums, zero rows for rows without a target
 #include <algorithm>
 
 #include "internal.h"
@@ -38,19 +38,27 @@ SPEC_DEVICE int64_t load_id(const void *p, int is64, int64_t i)
     return is64 ? reinterpret_cast<const int64_t *>(p)[i] : (int64_t) reinterpret_cast<const int32_t *>(p)[i];
 }
 
-constexpr int PACK_ROWS = 32;  // rows per workgroup of k_xent_pack
+constexpr int PACK_ROWS = 8;  // rows per workgroup of k_xent_pack
 
-// 16-byte chunks of a row: a full one where both ends are aligned, else by element
+// a row of d elements to one of dp, zero past d: 16 bytes at a time where both
+// ends are aligned, else by element
 template <typename S>
-SPEC_DEVICE void copy_row(const S *__restrict__ src, S *__restrict__ dst, int64_t d, int64_t dp, bool vec, int lane,
-                          int lanes)
+SPEC_DEVICE void copy_row(const S *__restrict__ src, S *__restrict__ dst, int64_t d, int64_t dp, bool vec, int lane)
 {
     constexpr int EPC = 16 / (int)sizeof(S);
     if (vec) {
-        for (int64_t c = lane; c < dp / EPC; c += lanes)
-            reinterpret_cast<uint4 *>(dst)[c] = reinterpret_cast<const uint4 *>(src)[c];
+        const uint4 *s = reinterpret_cast<const uint4 *>(src);
+        uint4 *o = reinterpret_cast<uint4 *>(dst);
+        const int64_t n = d / EPC;
+        int64_t c = lane;
+        for (; c + 192 < n; c += 256) {  // four in flight per lane
+            const uint4 a = s[c], b = s[c + 64], e = s[c + 128], f = s[c + 192];
+            o[c] = a, o[c + 64] = b, o[c + 128] = e, o[c + 192] = f;
+        }
+        for (; c < dp / EPC; c += 64) o[c] = c < n ? s[c] : make_uint4(0, 0, 0, 0);
     } else {
-        for (int64_t c = lane; c < dp; c += lanes) dst[c] = c < d ? src[c] : (S)0;
+#pragma unroll 8
+        for (int64_t c = lane; c < dp; c += 64) dst[c] = c < d ? src[c] : (S)0;
     }
 }
 
@@ -58,7 +66,7 @@ template <typename E>
 __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restrict__ H, int64_t ldh, int64_t d,
                                                    int64_t dp, int vec, const void *__restrict__ target, int is64,
                                                    int64_t T, int64_t V, typename E::st *__restrict__ Hp,
-                                                   int *__restrict__ pos, int *__restrict__ ptgt,
+                                                   int *__restrict__ pos, int *__restrict__ row, int *__restrict__ ptgt,
                                                    const float *__restrict__ lse, const float *__restrict__ dloss,
                                                    float *__restrict__ plse, float *__restrict__ pdl,
                                                    int *__restrict__ nvalid)
@@ -86,6 +94,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restr
         if (in) pos[t] = ok ? p : -1;
         if (ok) {
             ptgt[p] = (int)y;
+            row[p] = (int)t;
             if (lse != nullptr) {
                 plse[p] = lse[t];
                 pdl[p] = dloss[t];
@@ -96,7 +105,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restr
     __syncthreads();
     for (int r = wave; r < PACK_ROWS; r += 4) {
         const int p = where[r];
-        if (p >= 0) copy_row(H + (t0 + r) * ldh, Hp + (int64_t)p * dp, d, dp, vec != 0, lane, 64);
+        if (p >= 0) copy_row(H + (t0 + r) * ldh, Hp + (int64_t)p * dp, d, dp, vec != 0, lane);
     }
 }
 
@@ -105,7 +114,7 @@ __global__ __launch_bounds__(256) void k_xent_wpack(const typename E::st *__rest
                                                     int64_t dp, int64_t rows, typename E::st *__restrict__ Wp)
 {
     const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r < rows) copy_row(W + r * ldw, Wp + r * dp, d, dp, false, threadIdx.x & 63, 64);
+    if (r < rows) copy_row(W + r * ldw, Wp + r * dp, d, dp, false, threadIdx.x & 63);
 }
 
 // The logits of vocabulary rows [tile] (P) and packed tokens (Q).
@@ -307,28 +316,57 @@ __global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, in
     });
 }
 
-// part[split][t][p] (+)= sum over the split's share of the piece of W[v][p] G[t][v]
+// How the tiles of dH are dealt out.  Rounds of `slots` workgroups (those the
+// chip runs at once) take whole tiles; the tiles of a last round that leaves
+// half of it or more idle are split along the vocabulary, as many ways as fill it.
+struct DhPlan {
+    int whole;   // tiles taken whole
+    int ways;    // shares of each of the others
+    int units;   // workgroups with work
+};
+SPEC_DEVICE DhPlan dh_plan(int tiles, int slots, int most)
+{
+    const int left = tiles % slots;
+    const int ways = left > 0 ? max(1, min(most, slots / left)) : 1;
+    const int whole = ways > 1 ? tiles - left : tiles;
+    return {whole, ways, whole + (tiles - whole) * ways};
+}
+
+// part[t][p] (+)= sum over v of W[v][p] G[t][v] over the piece; the shares after
+// the first of a split tile have a tile of their own in `extra`
 template <typename E, typename C>
 __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int64_t ldw,
-                                                                 const typename E::st *__restrict__ G, int64_t ldg,
-                                                                 int64_t vn, int64_t per, int64_t d, int64_t T,
-                                                                 const int *__restrict__ nvalid, int np, int splits,
-                                                                 float *__restrict__ part, int64_t ldp, int first)
+                                       const typename E::st *__restrict__ G, int64_t ldg, int64_t vn, int64_t d,
+                                       const int *__restrict__ nvalid, int np, int slots, int most,
+                                       float *__restrict__ part, int64_t ldp, float *__restrict__ extra, int first)
 {
     using M = Mm<E, C, true, false>;
     MM_STAGES(M);
-    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ, tiles = np * nq;
+    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ, u = blockIdx.x;
+    const DhPlan pl = dh_plan(np * nq, slots, most);
+    if (u >= pl.units) return;
+    int id = u, share = 0;
+    int64_t kb = 0, ke = vn;
+    if (u >= pl.whole && pl.ways > 1) {
+        id = pl.whole + (u - pl.whole) / pl.ways;
+        share = (u - pl.whole) % pl.ways;
+        const int64_t per = round_up((vn + pl.ways - 1) / pl.ways, 64);
+        kb = share * per;
+        ke = min<int64_t>(vn, kb + per);
+    }
     int tp, tq;
-    if (blockIdx.x >= (unsigned)(tiles * splits)) return;
-    const int split = (int)blockIdx.x / tiles;
-    mm_tile(blockIdx.x % tiles, np, nq, tp, tq);
+    mm_tile(id, np, nq, tp, tq);
     const int t0 = tq * C::BQ;
-    const int64_t p0 = (int64_t)tp * C::BP, kb = split * per, ke = min<int64_t>(vn, kb + per);
+    const int64_t p0 = (int64_t)tp * C::BP;
     const MmSrc P{(const char *)(W + p0), ldw * M::SZ, (int)min<int64_t>(C::BP, d - p0), ke};
     const MmSrc Q{(const char *)(G + (int64_t)t0 * ldg), ldg * M::SZ, min(C::BQ, n - t0), round_up(ke, M::EPC)};
     M mm;
     mm.run(P, Q, kb, ke, lds);
-    float *out = part + ((int64_t)split * T + t0) * ldp + p0;
+    float *out = part + (int64_t)t0 * ldp + p0;
+    if (share > 0) {
+        out = extra + (int64_t)(u - pl.whole) * C::BP * C::BQ;
+        ldp = C::BP;
+    }
     mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;  // ldp is a multiple of 4: a group of four lies in its row
         float4 *o = reinterpret_cast<float4 *>(out + (int64_t)q * ldp + p);
@@ -341,17 +379,55 @@ __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int
     });
 }
 
-template <typename E>
-__global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ part, int64_t ldp, int splits,
-                                                     int64_t T, int64_t d, const int *__restrict__ pos,
-                                                     typename E::st *__restrict__ dH, int64_t lddh)
+constexpr int OUT_ROWS = 16;  // rows of a tile per workgroup of k_xent_dh_out
+
+// grid: tiles x (BQ / OUT_ROWS) workgroups that round the sums of their rows,
+// then cdiv(T, 4) that write the rows without a target
+template <typename E, typename C>
+__global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ part, int64_t ldp,
+                                                     const float *__restrict__ extra, const int *__restrict__ nvalid,
+                                                     int np, int nqmax, int slots, int most, int64_t T, int64_t d,
+                                                     const int *__restrict__ pos, const int *__restrict__ row,
+                                                     typename E::st *__restrict__ dH, int64_t lddh, int vec)
 {
-    const int64_t t = blockIdx.x, p = pos[t];
-    for (int64_t c = threadIdx.x; c < d; c += 256) {
-        float s = 0.f;
-        if (p >= 0)
-            for (int k = 0; k < splits; ++k) s += part[((int64_t)k * T + p) * ldp + c];
-        dH[t * lddh + c] = E::round(s);
+    constexpr int G = C::BQ / OUT_ROWS;
+    const int lane = threadIdx.x & 63;
+    const int64_t tileblocks = (int64_t)np * nqmax * G;
+    if (blockIdx.x >= tileblocks) {
+        const int64_t t = ((int64_t)blockIdx.x - tileblocks) * 4 + (threadIdx.x >> 6);
+        if (t < T && pos[t] < 0)
+            for (int64_t c = lane; c < d; c += 64) dH[t * lddh + c] = (typename E::st)0;
+        return;
+    }
+    const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ;
+    const DhPlan pl = dh_plan(np * nq, slots, most);
+    const int id = (int)(blockIdx.x / G), r0 = (int)(blockIdx.x % G) * OUT_ROWS;
+    if (id >= np * nq) return;
+    int tp, tq;
+    mm_tile(id, np, nq, tp, tq);
+    const int64_t p0 = (int64_t)tp * C::BP;
+    const int shares = id >= pl.whole ? pl.ways : 1;
+    const float *ex = extra + (int64_t)(id - pl.whole) * pl.ways * C::BP * C::BQ;
+    for (int i = threadIdx.x; i < OUT_ROWS * (C::BP / 4); i += 256) {
+        const int q = r0 + i / (C::BP / 4), p = 4 * (i % (C::BP / 4)), t = tq * C::BQ + q;
+        if (t >= n || p0 + p >= d) continue;
+        float4 s = *reinterpret_cast<const float4 *>(part + (int64_t)t * ldp + p0 + p);
+        for (int k = 1; k < shares; ++k) {
+            const float4 a = *reinterpret_cast<const float4 *>(ex + ((int64_t)k * C::BQ + q) * C::BP + p);
+            s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
+        }
+        typename E::st *o = dH + (int64_t)row[t] * lddh + p0 + p;
+        const float v[4] = {s.x, s.y, s.z, s.w};
+        if (vec && p0 + p + 4 <= d) {
+            Vec4<E> x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.v[e] = E::round(v[e]);
+            *reinterpret_cast<Vec4<E> *>(o) = x;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p0 + p + e < d) o[e] = E::round(v[e]);
+        }
     }
 }
 
@@ -365,9 +441,11 @@ struct XentPlan {
     int64_t dp;      // row of packed H and W: d rounded up to 64 elements
     int64_t dk;      // d rounded up to 16 bytes
     int64_t piece;   // vocabulary entries per piece
-    int splits;      // of a piece's contraction in dH
+    int most;        // shares of a tile of dH at most: 512 vocabulary entries each
+    bool big;        // dH in 256 x 256 tiles
+    int slots;       // and how many of its workgroups run at once
     // byte offsets into the workspace
-    int64_t pos, ptgt, plse, pdl, nvalid, hp, wp, ztgt, part, g, total;
+    int64_t pos, row, ptgt, plse, pdl, nvalid, hp, wp, ztgt, part, extra, g, total;
 };
 
 XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
@@ -379,10 +457,9 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
     const int64_t Tn = std::max<int64_t>(T, 1);
     p.piece = std::max<int64_t>(2048, XENT_G_BYTES / (es * Tn) / 256 * 256);
     p.piece = std::min<int64_t>(p.piece, up_h(V, 256));
-    // dH has few tiles when tokens are few: split its contraction until about
-    // two workgroups per CU have work, in shares of at least 512 entries
-    const int64_t tiles = cdiv_h(Tn, 128) * cdiv_h(d, 128);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, p.piece / 512, 64}));
+    p.most = (int)std::max<int64_t>(1, std::min<int64_t>(p.piece / 512, 64));
+    p.big = cdiv_h(T, 256) * cdiv_h(d, 256) >= 128;  // fewer are split, and smaller ones split finer
+    p.slots = p.big ? 256 : 512;
     int64_t o = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = o;
@@ -391,6 +468,7 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
     };
     p.nvalid = take(4);
     p.pos = take(4 * Tn);
+    p.row = take(4 * Tn);
     p.ptgt = take(4 * Tn);
     p.hp = take(es * Tn * p.dp);
     p.wp = take(es * p.piece * p.dp);
@@ -398,7 +476,8 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
         p.plse = take(4 * Tn);
         p.pdl = take(4 * Tn);
         p.g = take(es * Tn * p.piece);
-        p.part = take((int64_t)4 * p.splits * Tn * up_h(d, 4));
+        p.part = take((int64_t)4 * Tn * up_h(d, 4));
+        p.extra = take((int64_t)4 * 256 * 256 * 256);
     } else {
         p.ztgt = take(4 * Tn);
         p.part = take(8 * Tn * cdiv_h(V, 128));
@@ -412,9 +491,9 @@ hipError_t pack(hipStream_t stream, const XentPlan &pl, const void *H, int64_t l
                 const float *lse, const float *dloss, int64_t T, int64_t V, int64_t d, char *ws)
 {
     using st = typename E::st;
-    const int vec = (uintptr_t)H % 16 == 0 && ldh * sizeof(st) % 16 == 0 && d == pl.dp;
+    const int vec = (uintptr_t)H % 16 == 0 && ldh * sizeof(st) % 16 == 0 && d * sizeof(st) % 16 == 0;
     hipLaunchKernelGGL(k_xent_pack<E>, dim3((unsigned)cdiv_h(T, PACK_ROWS)), dim3(256), 0, stream, (const st *)H, ldh, d,
-                       pl.dp, vec, target, is64, T, V, (st *)(ws + pl.hp), (int *)(ws + pl.pos), (int *)(ws + pl.ptgt),
+                       pl.dp, vec, target, is64, T, V, (st *)(ws + pl.hp), (int *)(ws + pl.pos), (int *)(ws + pl.row), (int *)(ws + pl.ptgt),
                        lse, dloss, (float *)(ws + pl.plse), (float *)(ws + pl.pdl), (int *)(ws + pl.nvalid));
     return hipGetLastError();
 }
@@ -491,10 +570,24 @@ hipError_t dh_piece(hipStream_t stream, const XentPlan &pl, const typename E::st
                     int64_t d, bool first, char *ws)
 {
     const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(T, C::BQ);
-    const int64_t per = up_h(cdiv_h(vn, pl.splits), 64);
-    hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)((int64_t)np * nq * pl.splits)), dim3(C::NT), 0,
-                       stream, W, ldw, (const typename E::st *)(ws + pl.g), pl.piece, vn, per, d, T,
-                       (const int *)(ws + pl.nvalid), np, pl.splits, (float *)(ws + pl.part), up_h(d, 4), first);
+    // whole tiles of every round, then at most one round of shares
+    const int64_t grid = (int64_t)np * nq + pl.slots;
+    hipLaunchKernelGGL((k_xent_dh<E, C>), dim3((unsigned)grid), dim3(C::NT), 0, stream, W, ldw,
+                       (const typename E::st *)(ws + pl.g), pl.piece, vn, d, (const int *)(ws + pl.nvalid), np, pl.slots,
+                       pl.most, (float *)(ws + pl.part), up_h(d, 4), (float *)(ws + pl.extra), first);
+    return hipGetLastError();
+}
+
+template <typename E, typename C>
+hipError_t dh_out(hipStream_t stream, const XentPlan &pl, int64_t T, int64_t d, void *dH, int64_t lddh, char *ws)
+{
+    using st = typename E::st;
+    const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(T, C::BQ);
+    const int64_t grid = (int64_t)np * nq * (C::BQ / OUT_ROWS) + cdiv_h(T, 4);
+    const int vec = (uintptr_t)dH % (4 * sizeof(st)) == 0 && lddh % 4 == 0;
+    hipLaunchKernelGGL((k_xent_dh_out<E, C>), dim3((unsigned)grid), dim3(256), 0, stream, (const float *)(ws + pl.part),
+                       up_h(d, 4), (const float *)(ws + pl.extra), (const int *)(ws + pl.nvalid), np, nq, pl.slots,
+                       pl.most, T, d, (const int *)(ws + pl.pos), (const int *)(ws + pl.row), (st *)dH, lddh, vec);
     return hipGetLastError();
 }
 
@@ -546,13 +639,11 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
         e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, dWv, lddw, beta, ws)
                              : dw_piece<E, Tile128>(stream, pl, vn, d, dWv, lddw, beta, ws);
         if (e != hipSuccess) return e;
-        e = big_tiles(T * pl.splits, d) ? dh_piece<E, Tile256>(stream, pl, Wv, ld, vn, T, d, v == 0, ws)
-                                        : dh_piece<E, Tile128>(stream, pl, Wv, ld, vn, T, d, v == 0, ws);
+        e = pl.big ? dh_piece<E, Tile256>(stream, pl, Wv, ld, vn, T, d, v == 0, ws)
+                   : dh_piece<E, Tile128>(stream, pl, Wv, ld, vn, T, d, v == 0, ws);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_xent_dh_out<E>, dim3((unsigned)T), dim3(256), 0, stream, (const float *)(ws + pl.part), up_h(d, 4),
-                       pl.splits, T, d, (const int *)(ws + pl.pos), (st *)dH, lddh);
-    return hipGetLastError();
+    return pl.big ? dh_out<E, Tile256>(stream, pl, T, d, dH, lddh, ws) : dh_out<E, Tile128>(stream, pl, T, d, dH, lddh, ws);
 }
 
 // dW <- beta dW where no token has a target to add
