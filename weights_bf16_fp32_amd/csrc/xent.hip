@@ -177,11 +177,18 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
         // few tiles hold a target of one of their rows
         const int64_t y = in ? (int64_t)ptgt[t0 + q] - vbase - v0 - p0 : -1;  // its place from this lane's first
         if (__any(y >= 0 && y < C::BP / C::WP)) {
+            const int at = (int)max<int64_t>(-1, min<int64_t>(y, C::BP));
+            float z = 0.f;
+            bool mine = false;
 #pragma unroll
             for (int m = 0; m < M::MI; ++m)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (y == 32 * m + 8 * (e >> 2) + (e & 3)) ztgt[t0 + q] = mm.acc[m][b][e];
+                for (int e = 0; e < 16; ++e) {
+                    const bool here = at == 32 * m + 8 * (e >> 2) + (e & 3);
+                    z = here ? mm.acc[m][b][e] : z;
+                    mine |= here;
+                }
+            if (mine) ztgt[t0 + q] = z;
         }
         {
             float a = top, c = top;
