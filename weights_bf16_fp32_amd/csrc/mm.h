@@ -348,25 +348,34 @@ struct Mm {
         return reinterpret_cast<float4 *>(mine) + (wave & 1) * 32 * PC;
     }
 
-    // f(p, q, v): four results p .. p + 3 of row q (offsets within the tile).
-    // A lane's results lie in one row and the lanes' rows differ, so memory would
-    // be met 16 bytes at a time; large tiles pass them through LDS (each wave its
-    // own part of the stages) and meet it in runs of a wave's whole width.
-    template <typename F>
-    SPEC_DEVICE void each4(const Lds &s, F &&f)
+    // put(p, q, v, get(p, q)): four results p .. p + 3 of row q (offsets within the
+    // tile), with what get() read for them.  A lane's results lie in one row and
+    // the lanes' rows differ, so memory would be met 16 bytes at a time; large
+    // tiles pass them through LDS (each wave its own part of the stages) and meet
+    // it in runs of a wave's whole width.  The reads of eight groups are issued
+    // together, before the first of their stores.
+    template <typename G, typename F>
+    SPEC_DEVICE void each4(const Lds &s, G &&get, F &&put)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         if constexpr (WK > 1) {
             const int p0 = 8 * wave + 4 * (lane >> 5), q0 = lane & 31;
+            decltype(get(0, 0)) old[MI][NI];
+#pragma unroll
+            for (int n = 0; n < NI; ++n)
+#pragma unroll
+                for (int m = 0; m < MI; ++m) old[m][n] = get(p0 + 32 * m, q0 + 32 * n);
 #pragma unroll
             for (int n = 0; n < NI; ++n)
 #pragma unroll
                 for (int m = 0; m < MI; ++m) {
                     float v[4] = {acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]};
-                    f(p0 + 32 * m, q0 + 32 * n, v);
+                    put(p0 + 32 * m, q0 + 32 * n, v, old[m][n]);
                 }
         } else {
             constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
+            constexpr int AT = PC / 2 % 8 == 0 ? 8 : 6;
+            static_assert(PC / 2 % AT == 0, "groups at a time");
             float4 *buf = own_part(s);
             const auto slot = [](int q, int c) { return q * PC + (c ^ (PC == 24 ? (q >> 1) & 7 : q & 15)); };
             const int p0 = wave_p0(wave), q0 = wave_q0(wave);
@@ -381,20 +390,36 @@ struct Mm {
                             make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
                 wave_sync();
 #pragma unroll
-                for (int i = 0; i < PC / 2; ++i) {
-                    const int u = 64 * i + lane, q = u / PC, c = u % PC;
-                    const float4 r = buf[slot(q, c)];
-                    float v[4] = {r.x, r.y, r.z, r.w};
-                    f(p0 + 4 * c, q0 + 32 * n + q, v);
+                for (int i0 = 0; i0 < PC / 2; i0 += AT) {
+                    decltype(get(0, 0)) old[AT];
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) {
+                        const int u = 64 * (i0 + i) + lane;
+                        old[i] = get(p0 + 4 * (u % PC), q0 + 32 * n + u / PC);
+                    }
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) {
+                        const int u = 64 * (i0 + i) + lane, q = u / PC, c = u % PC;
+                        const float4 r = buf[slot(q, c)];
+                        float v[4] = {r.x, r.y, r.z, r.w};
+                        put(p0 + 4 * c, q0 + 32 * n + q, v, old[i]);
+                    }
                 }
             }
         }
     }
-
-    // f(p, q, v): the results of rows q .. q + 3 at p: the tile of the transposed
-    // product, in runs of 32 rows
+    struct Nothing {
+    };
     template <typename F>
-    SPEC_DEVICE void each4_across(const Lds &s, F &&f)
+    SPEC_DEVICE void each4(const Lds &s, F &&put)
+    {
+        each4(s, [](int, int) { return Nothing{}; }, [&](int p, int q, float (&v)[4], const Nothing &) { put(p, q, v); });
+    }
+
+    // put(p, q, v, get(p, q)): the results of rows q .. q + 3 at p: the tile of the
+    // transposed product, in runs of 32 rows
+    template <typename G, typename F>
+    SPEC_DEVICE void each4_across(const Lds &s, G &&get, F &&put)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         const int p0 = wave_p0(wave), q0 = wave_q0(wave);
@@ -405,13 +430,15 @@ struct Mm {
             for (int n = 0; n < NI; ++n)
 #pragma unroll
                 for (int m = 0; m < MI; ++m) {
+                    const int p = 32 * m + 8 * wave + (lane >> 3), q = 32 * n + 4 * (lane & 7);
+                    const auto old = get(p, q);
                     wave_sync();
 #pragma unroll
                     for (int e = 0; e < 4; ++e) buf[(4 * (lane >> 5) + e) * 32 + (lane & 31)] = acc[m][n][e];
                     wave_sync();
                     const float4 r = reinterpret_cast<const float4 *>(buf)[lane];
                     float v[4] = {r.x, r.y, r.z, r.w};
-                    f(32 * m + 8 * wave + (lane >> 3), 32 * n + 4 * (lane & 7), v);
+                    put(p, q, v, old);
                 }
         } else {
             // rows p of 32 floats; p and p + 4 are written together, so bit 0 of the
@@ -428,12 +455,20 @@ struct Mm {
                     for (int e = 0; e < 16; ++e)
                         buf[row(32 * m + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) + (lane & 31)] = acc[m][n][e];
                 wave_sync();
+                constexpr int AT = PR / 8 % 8 == 0 ? 8 : 6;
+                static_assert(PR / 8 % AT == 0, "groups at a time");
 #pragma unroll
-                for (int i = 0; i < PR / 8; ++i) {
-                    const int p = 8 * i + (lane >> 3);
-                    const float4 r = *reinterpret_cast<const float4 *>(buf + row(p) + 4 * (lane & 7));
-                    float v[4] = {r.x, r.y, r.z, r.w};
-                    f(p0 + p, q0 + 32 * n + 4 * (lane & 7), v);
+                for (int i0 = 0; i0 < PR / 8; i0 += AT) {
+                    decltype(get(0, 0)) old[AT];
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) old[i] = get(p0 + 8 * (i0 + i) + (lane >> 3), q0 + 32 * n + 4 * (lane & 7));
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) {
+                        const int p = 8 * (i0 + i) + (lane >> 3);
+                        const float4 r = *reinterpret_cast<const float4 *>(buf + row(p) + 4 * (lane & 7));
+                        float v[4] = {r.x, r.y, r.z, r.w};
+                        put(p0 + p, q0 + 32 * n + 4 * (lane & 7), v, old[i]);
+                    }
                 }
             }
         }
@@ -456,7 +491,7 @@ SPEC_DEVICE void mm_tile(int64_t id, int np, int nq, int &tp, int &tq)
 }
 
 // Tile shapes.  256 x 256 by eight waves (128 x 64 each, one workgroup per CU:
-// 128 KB of LDS), 192 x 192 by six (96 x 64 each, three stages in 144 KB) and
+// 128 KB of LDS), 192 x 192 by four (96 x 96 each, three stages in 144 KB) and
 // 128 x 128 by four (64 x 64 each, two workgroups per CU).
 // Products with few tiles take 64 x 64 or 32 x 32: each of four waves sums a
 // quarter of every K-step over the whole tile, and the stages are deeper,
@@ -465,7 +500,7 @@ struct Tile256 {
     static constexpr int BP = 256, BQ = 256, WP = 2, WQ = 4, WK = 1, STAGES = 2, NT = 512;
 };
 struct Tile192 {
-    static constexpr int BP = 192, BQ = 192, WP = 2, WQ = 3, WK = 1, STAGES = 3, NT = 384;
+    static constexpr int BP = 192, BQ = 192, WP = 2, WQ = 2, WK = 1, STAGES = 3, NT = 256;
 };
 struct Tile128 {
     static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2, WK = 1, STAGES = 2, NT = 256;
@@ -499,7 +534,7 @@ inline hipError_t mm_pick(N &&count, F &&f)
 {
     constexpr bool H = sizeof(typename E::st) == 2;
     const int edge[5] = {256, 192, 128, 64, 32};
-    const double per[5] = {1.0, 1.04, H ? 1.17 : 1.0, H ? 2.1 : 1.2, H ? 6.0 : 2.0};
+    const double per[5] = {1.0, 1.1, H ? 1.28 : 1.03, H ? 2.1 : 1.14, H ? 6.0 : 1.53};
     int best = 0;
     double least = 0.0;
     for (int i = 0; i < 5; ++i) {

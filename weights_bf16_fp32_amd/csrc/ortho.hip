@@ -98,19 +98,6 @@ SPEC_DEVICE void put_x(typename E::st *hi, typename E::st *lo, int64_t at, const
     if (sizeof(typename E::st) == 2) *reinterpret_cast<Vec4<E> *>(lo + at) = l;
 }
 
-template <typename E>
-SPEC_DEVICE void get_x(const typename E::st *hi, const typename E::st *lo, int64_t at, float (&v)[4])
-{
-    const Vec4<E> h = *reinterpret_cast<const Vec4<E> *>(hi + at);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = E::wide(h.v[e]);
-    if (sizeof(typename E::st) == 2) {
-        const Vec4<E> l = *reinterpret_cast<const Vec4<E> *>(lo + at);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += E::wide(l.v[e]);
-    }
-}
-
 // X = G * sx / (norm + eps), padding columns zero.  grid (rows, batch)
 template <typename G, typename E>
 __global__ __launch_bounds__(256) void k_ns_load(const typename G::st *__restrict__ X, int64_t n, int64_t ld,
@@ -146,14 +133,13 @@ template <typename E>
 SPEC_DEVICE void put_sym(typename E::st *A, float *diag, const NsDims &D, int64_t i, int64_t j, bool on,
                          const float (&v)[4], float scale)
 {
-    if (i >= D.r || j >= D.ap) return;
     Vec4<E> o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (on && i == j + e) diag[i] = v[e];
+        if (on && i == j + e && i < D.ap) diag[i] = v[e];  // (zero from r on)
         o.v[e] = on && i == j + e ? (typename E::st)0 : E::round(v[e] * scale);
     }
-    *reinterpret_cast<Vec4<E> *>(A + i * D.ap + j) = o;
+    if (i < D.r && j < D.ap) *reinterpret_cast<Vec4<E> *>(A + i * D.ap + j) = o;
 }
 
 // grid (tiles on and below the diagonal, batch).  real: 1 / sx^2
@@ -177,10 +163,11 @@ __global__ MM_BOUNDS(C) void k_ns_gram(const typename E::st *__restrict__ X, NsD
     const auto put = [&](int64_t i, int64_t j, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= real;
-        put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti == tj, v, sa);
+        put_sym<E>(A + blockIdx.y * D.as, diag + blockIdx.y * D.ap, D, i, j, ti == tj, v, sa);
     };
     mm.each4(lds, [&](int p, int q, float (&v)[4]) { put(i0 + q, j0 + p, v); });
-    if (ti != tj) mm.each4_across(lds, [&](int p, int q, float (&v)[4]) { put(j0 + p, i0 + q, v); });
+    if (ti != tj)
+        mm.each4_across(lds, [](int, int) { return 0; }, [&](int p, int q, float (&v)[4], int) { put(j0 + p, i0 + q, v); });
 }
 
 // B = b A + c A^2 with A = diag(da) + E; ea = 1 / sa
@@ -197,26 +184,40 @@ __global__ MM_BOUNDS(C) void k_ns_poly(const typename E::st *__restrict__ A,
     tri_tile_blocked(xcd_remap(blockIdx.x, gridDim.x), (int)((D.r + C::BP - 1) / C::BP), ti, tj);
     const int64_t i0 = (int64_t)ti * C::BQ, j0 = (int64_t)tj * C::BP;
     const typename E::st *a = A + blockIdx.y * D.as;
-    const float *d = da + blockIdx.y * D.r;
+    const float *d = da + blockIdx.y * D.ap;
     const int64_t K = round_up(D.r, M::EPC);
     const MmSrc P{(const char *)(a + j0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BP, D.r - j0), K};
     const MmSrc Q{(const char *)(a + i0 * D.ap), D.ap * M::SZ, (int)min<int64_t>(C::BQ, D.r - i0), K};
     M mm;
     mm.run(P, Q, 0, K, lds);
-    const auto put = [&](int64_t i, int64_t j, float (&v)[4]) {
-        if (i >= D.r || j >= D.ap) return;
-        const float di = d[i];
-        const Vec4<E> x = *reinterpret_cast<const Vec4<E> *>(a + i * D.ap + j);
+    struct Old {
+        Vec4<E> x;
+        float di;
+        float4 dj;
+    };
+    const auto get = [&](int64_t i, int64_t j) {
+        Old o{};
+        if (i < D.r && j < D.ap) {
+            o.x = *reinterpret_cast<const Vec4<E> *>(a + i * D.ap + j);
+            o.di = d[i];
+            o.dj = *reinterpret_cast<const float4 *>(d + j);
+        }
+        return o;
+    };
+    const auto put = [&](int64_t i, int64_t j, float (&v)[4], const Old &o) {
+        const float dj[4] = {o.dj.x, o.dj.y, o.dj.z, o.dj.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float dj = j + e < D.r ? d[j + e] : 0.f;
             const float aa = c * (v[e] * ea * ea);
-            v[e] = i == j + e ? b * di + (c * di * di + aa) : (b + c * (di + dj)) * (E::wide(x.v[e]) * ea) + aa;
+            v[e] = i == j + e ? b * o.di + (c * o.di * o.di + aa) : (b + c * (o.di + dj[e])) * (E::wide(o.x.v[e]) * ea) + aa;
         }
-        put_sym<E>(B + blockIdx.y * D.as, diag + blockIdx.y * D.r, D, i, j, ti == tj, v, sb);
+        put_sym<E>(B + blockIdx.y * D.as, diag + blockIdx.y * D.ap, D, i, j, ti == tj, v, sb);
     };
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) { put(i0 + q, j0 + p, v); });
-    if (ti != tj) mm.each4_across(lds, [&](int p, int q, float (&v)[4]) { put(j0 + p, i0 + q, v); });
+    mm.each4(lds, [&](int p, int q) { return get(i0 + q, j0 + p); },
+             [&](int p, int q, float (&v)[4], const Old &o) { put(i0 + q, j0 + p, v, o); });
+    if (ti != tj)
+        mm.each4_across(lds, [&](int p, int q) { return get(j0 + p, i0 + q); },
+                        [&](int p, int q, float (&v)[4], const Old &o) { put(j0 + p, i0 + q, v, o); });
 }
 
 // The next X (scaled by sx1), or O = scale X in the last step.
@@ -235,7 +236,7 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
     const int64_t j0 = (int64_t)tp * C::BP, i0 = (int64_t)tq * C::BQ;
     const int64_t xb = blockIdx.y * D.xs;
     const typename E::st *bm = B + blockIdx.y * D.as;
-    const float *d = db + blockIdx.y * D.r;
+    const float *d = db + blockIdx.y * D.ap;
     const int64_t K = round_up(D.r, M::EPC);
     MmSrc P, Q;
     if (TALL) {  // rows of B (symmetric) against rows of X
@@ -247,16 +248,28 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
     }
     M mm;
     mm.run(P, Q, 0, K, lds);
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
+    struct Old {
+        Vec4<E> h, l;
+        float4 d;
+    };
+    const auto get = [&](int p, int q) {
+        const int64_t i = i0 + q, j = j0 + p, at = xb + i * D.xp + j;
+        Old o{};
+        if (i < D.rows && j < D.xp) {
+            o.h = *reinterpret_cast<const Vec4<E> *>(hi + at);
+            if (M::SZ == 2) o.l = *reinterpret_cast<const Vec4<E> *>(lo + at);
+            o.d = TALL ? *reinterpret_cast<const float4 *>(d + j) : make_float4(d[i], d[i], d[i], d[i]);
+        }
+        return o;
+    };
+    mm.each4(lds, get, [&](int p, int q, float (&v)[4], const Old &o) {
         const int64_t i = i0 + q, j = j0 + p;
         if (i >= D.rows || j >= D.xp) return;
-        float x[4];
-        get_x<E>(hi, lo, xb + i * D.xp + j, x);
-        const float di = TALL ? 0.f : d[i];
+        const float dd[4] = {o.d.x, o.d.y, o.d.z, o.d.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float f = a + (TALL ? (j + e < D.cols ? d[j + e] : 0.f) : di);
-            v[e] = (f * x[e] + eb * v[e]) * ex * sx1;
+            const float x = E::wide(o.h.v[e]) + (M::SZ == 2 ? E::wide(o.l.v[e]) : 0.f);
+            v[e] = ((a + dd[e]) * x + eb * v[e]) * ex * sx1;
         }
         if (!LAST) {
             put_x<E>(hi1, lo1, xb + i * D.xp + j, v);
@@ -300,8 +313,8 @@ NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int t)
         return at;
     };
     p.part = take(8 * batch * norm_blocks(m, n));
-    p.da = take(4 * batch * D.r);
-    p.db = take(4 * batch * D.r);
+    p.da = take(4 * batch * D.ap);
+    p.db = take(4 * batch * D.ap);
     p.a = take(es * batch * D.as);
     p.b = take(es * batch * D.as);
     for (int i = 0; i < 2; ++i) {

@@ -277,10 +277,16 @@ __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int6
     logits<M, E>(mm, W, ldw, vn, Hp, dp, n, dk, v0, t0, lds, C::BP, C::BQ);
     const int lim = (int)min<int64_t>(C::BP, vn - v0);
     const int lim4 = (int)min<int64_t>(C::BP, round_up(vn, M::EPC) - v0);
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
+    struct Row {
+        int y;
+        float lse, w;
+    };
+    mm.each4(lds, [&](int p, int q) {
+        return t0 + q < n ? Row{ptgt[t0 + q], plse[t0 + q], pdl[t0 + q]} : Row{};
+    }, [&](int p, int q, float (&v)[4], const Row &r) {
         if (t0 + q >= n || p >= lim4) return;
-        const int64_t y = (int64_t)ptgt[t0 + q] - vbase - v0;
-        const float l = plse[t0 + q], w = pdl[t0 + q] * scale;
+        const int64_t y = r.y - vbase - v0;
+        const float l = r.lse, w = r.w * scale;
         Vec4<E> o;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -374,15 +380,12 @@ __global__ MM_BOUNDS(C) void k_xent_dh(const typename E::st *__restrict__ W, int
         out = extra + (int64_t)(u - pl.whole) * C::BP * C::BQ;
         ldp = C::BP;
     }
-    mm.each4(lds, [&](int p, int q, float (&v)[4]) {
-        if (q >= Q.lim || p >= P.lim) return;  // ldp is a multiple of 4: a group of four lies in its row
-        float4 *o = reinterpret_cast<float4 *>(out + (int64_t)q * ldp + p);
-        float4 r = make_float4(v[0], v[1], v[2], v[3]);
-        if (!first) {
-            const float4 a = *o;
-            r.x += a.x, r.y += a.y, r.z += a.z, r.w += a.w;
-        }
-        *o = r;
+    // (ldp is a multiple of 4: a group of four lies in its row)
+    const auto at = [&](int p, int q) { return reinterpret_cast<float4 *>(out + (int64_t)q * ldp + p); };
+    mm.each4(lds, [&](int p, int q) {
+        return first || q >= Q.lim || p >= P.lim ? make_float4(0.f, 0.f, 0.f, 0.f) : *at(p, q);
+    }, [&](int p, int q, float (&v)[4], const float4 &a) {
+        if (q < Q.lim && p < P.lim) *at(p, q) = make_float4(v[0] + a.x, v[1] + a.y, v[2] + a.z, v[3] + a.w);
     });
 }
 
