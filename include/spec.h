@@ -616,8 +616,8 @@ int spec_linear_xent_grad(void *stream, const void *H, const void *W, int t, int
  * (256-byte aligned).
  * Requires 1 <= m, n <= 65536 with min(m, n) <= 32768, 1 <= batch <= 65535, ldg, ldo >= n,
  * sg >= m*ldg and so >= m*ldo when batch > 1, 1 <= steps <= 32, eps >= 0,
- * finite coefficients and scale, and (SPEC_BF16) coefficients that keep every s in
- * [0, 1] below 2^7; else SPEC_EINVAL. */
+ * finite coefficients and scale, and (SPEC_BF16) coefficients whose steps keep
+ * every s in [0, 1] below 11 and |b| s^2 + |c| s^4 below 2^14; else SPEC_EINVAL. */
 int spec_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int t, size_t *bytes);
 
 int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,

@@ -26,11 +26,20 @@
 // A and B are symmetric: only tiles on and below the diagonal are computed, and
 // each is written to both places.
 //
+// Small bf16 matrices (shorter side up to 256) are bound by the number of
+// dependent launches, not by their products, and take one launch per step: a
+// workgroup computes 32 rows of the next X from the whole present one by
+//   E_i = offdiag(X_i X^T),  R_i = E_i X,  Z_i = A_i A = d_i E_i + R_i X^T + diag,
+//   X_i <- (a + b d_i + c z_ii) X_i + b R_i + c offdiag(Z_i) X
+// which multiplies more (four products of 32 rows, no symmetry) but never
+// waits for another workgroup's A or B.
+//
 //   k_ns_norm   partial sums of squares (f64)
 //   k_ns_load   X_0
 //   k_ns_gram   A and its diagonal
 //   k_ns_poly   B and its diagonal
 //   k_ns_apply  the next X, or O
+//   k_chain_load, k_chain_step   the same for small matrices
 #include <algorithm>
 #include <math.h>
 
@@ -289,6 +298,205 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
     });
 }
 
+// ------------------------------------------------------------------ small matrices
+
+// X (r x s, r <= s, whatever G's orientation) is kept row-major in `hi`, `lo`
+// (rp rows of pitch sp, padding zero) and, its leading part, transposed in `tr`
+// (sp rows of pitch rp): every product then reads both operands along k.
+struct ChainDims {
+    int r, s, rp, sp;  // rp, sp: rounded up to 64
+};
+constexpr int CHAIN_R = 256, CHAIN_S = 1024;
+constexpr int CHAIN_WORK = 1 << 17;  // r s at most (see chain_fits)
+
+// The shorter side bounds the blocks a wave holds; the product r s the time of a
+// step, which at 256 x 512 is what the three launches of the other path take.
+inline bool chain_fits(int64_t m, int64_t n)
+{
+    const int64_t r = std::min(m, n), s = std::max(m, n);
+    return r <= CHAIN_R && s <= CHAIN_S && r * s <= CHAIN_WORK;
+}
+
+using h8 = f16x8_t;
+SPEC_DEVICE uint16_t f16_bits(float x) { return ElF16::round(x); }
+
+// 32 x 32 block sum_k P[p][k] Q[q][k]: P in memory (pitch ldp), Q in LDS (pitch
+// ldq); k a multiple of 64
+SPEC_DEVICE f32x16_t chain_product(const uint16_t *__restrict__ P, int ldp, const uint16_t *Q, int ldq, int K, int lane)
+{
+    f32x16_t acc;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    const uint16_t *p = P + (lane & 31) * ldp + 8 * (lane >> 5), *q = Q + (lane & 31) * ldq + 8 * (lane >> 5);
+#pragma unroll 4
+    for (int k = 0; k < K; k += 64) {
+        h8 a[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const h8 *>(p + k + 16 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j], *reinterpret_cast<const h8 *>(q + k + 16 * j), acc, 0, 0, 0);
+    }
+    return acc;
+}
+
+// grid (rp / 32, batch), 512 threads: X = G sx / (norm + eps).  Every workgroup
+// sums all squares itself (at most 256 KB from the L2).
+__global__ __launch_bounds__(512) void k_chain_load(const uint16_t *__restrict__ G, int m, int n, int64_t ldg, int64_t sg,
+                                                    ChainDims D, double eps, float sx, uint16_t *__restrict__ hi,
+                                                    uint16_t *__restrict__ lo, uint16_t *__restrict__ tr)
+{
+    __shared__ double red[8];
+    const uint16_t *g = G + blockIdx.y * sg;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    double s = 0.0;
+    for (int i = wave; i < m; i += 8)
+#pragma unroll 4
+        for (int j = lane; j < n; j += 64) {
+            const double v = (double)bf16_to_f32(g[i * ldg + j]);
+            s += v * v;
+        }
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) red[wave] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < 8; ++w) s += red[w];
+    const float inv = (float)((double)sx / (sqrt(s) + eps));
+    const int i0 = blockIdx.x * 32;
+    const int64_t base = (int64_t)blockIdx.y * D.rp * D.sp;
+    const bool tall = m > n;
+    for (int u = tid; u < 32 * D.sp; u += 512) {
+        // along G's rows: columns of X for a wide G, rows of X for a tall one
+        const int q = tall ? u & 31 : u / D.sp, c = tall ? u >> 5 : u % D.sp, i = i0 + q;
+        const float v = i < D.r && c < D.s ? bf16_to_f32(tall ? g[c * ldg + i] : g[i * ldg + c]) * inv : 0.f;
+        const uint16_t h = f16_bits(v);
+        hi[base + (int64_t)i * D.sp + c] = h;
+        lo[base + (int64_t)i * D.sp + c] = f16_bits(v - ElF16::wide(h));
+        tr[base + (int64_t)c * D.rp + i] = h;
+    }
+}
+
+struct ChainStep {
+    float a, b, c;      // the step's polynomial
+    float sx, sx1;      // scales of X and of the next one (or of O)
+    float sa, sr, sz;   // of E, R and Z
+};
+
+// grid (rp / 32, batch), 512 threads; CB: blocks of 32 columns per wave
+template <int CB, bool LAST>
+__global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
+                                                    const uint16_t *__restrict__ tr, ChainDims D, ChainStep t,
+                                                    uint16_t *__restrict__ hi1, uint16_t *__restrict__ lo1,
+                                                    uint16_t *__restrict__ tr1, uint16_t *__restrict__ out, int64_t ldo,
+                                                    int64_t so, int tall)
+{
+    constexpr int PX = CB * 256 + 8;  // LDS pitches: 16 bytes past a multiple of 256, so that 16 rows meet 16 slots
+    constexpr int PE = CHAIN_R + 8;
+    __shared__ __attribute__((aligned(16))) uint16_t Q[32 * PX], Ez[32 * PE];  // Q: X_i, then R_i
+    __shared__ float dd[32], zz[32];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, q = lane & 31;
+    const int i0 = blockIdx.x * 32;
+    const int64_t base = (int64_t)blockIdx.y * D.rp * D.sp;
+    hi += base, lo += base, tr += base;
+    for (int u = tid; u < 32 * (D.sp / 8); u += 512) {
+        const int r = u / (D.sp / 8), c = u % (D.sp / 8);
+        *reinterpret_cast<uint4 *>(&Q[r * PX + 8 * c]) = *reinterpret_cast<const uint4 *>(hi + (int64_t)(i0 + r) * D.sp + 8 * c);
+    }
+    __syncthreads();
+    const float ex = 1.f / t.sx;
+    const int jb = wave;  // this wave's block of 32 rows j, and its blocks wave, wave + 8, .. of 32 columns
+    const bool rows = jb * 32 < D.rp, own = jb == (int)blockIdx.x;
+    const auto four = [&](uint16_t *o, const f32x16_t &v, int g, float scale) {
+        Vec4<ElF16> x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x.v[e] = f16_bits(v[4 * g + e] * scale);
+        *reinterpret_cast<Vec4<ElF16> *>(o + 8 * g + 4 * h) = x;
+    };
+    f32x16_t E;
+    if (rows) {
+        E = chain_product(hi + (int64_t)jb * 32 * D.sp, D.sp, Q, PX, D.sp, lane);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            E[e] *= ex * ex;
+            if (own && 8 * (e >> 2) + 4 * h + (e & 3) == q) {
+                dd[q] = E[e];
+                E[e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) four(&Ez[q * PE + jb * 32], E, g, t.sa);
+    }
+    __syncthreads();  // Q has been read, E and its diagonal are written
+    f32x16_t R[CB];
+#pragma unroll
+    for (int k = 0; k < CB; ++k) {
+        const int c0 = (wave + 8 * k) * 32;
+        if (c0 < D.sp) {
+            R[k] = chain_product(tr + (int64_t)c0 * D.rp, D.rp, Ez, PE, D.rp, lane);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) R[k][e] *= ex / t.sa;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) four(&Q[q * PX + c0], R[k], g, t.sr);
+        }
+    }
+    __syncthreads();
+    if (rows) {
+        const f32x16_t Z = chain_product(hi + (int64_t)jb * 32 * D.sp, D.sp, Q, PX, D.sp, lane);
+        const float d = dd[q];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float z = Z[e] * (ex / t.sr);
+            if (own && 8 * (e >> 2) + 4 * h + (e & 3) == q) {
+                zz[q] = d * d + z;
+                z = 0.f;
+            } else {
+                z += d * E[e];
+            }
+            E[e] = z;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) four(&Ez[q * PE + jb * 32], E, g, t.sz);
+    }
+    __syncthreads();
+    const float f = t.a + t.b * dd[q] + t.c * zz[q];
+    const int i = i0 + q;
+#pragma unroll
+    for (int k = 0; k < CB; ++k) {
+        const int c0 = (wave + 8 * k) * 32;
+        if (c0 >= D.sp) continue;
+        const f32x16_t W = chain_product(tr + (int64_t)c0 * D.rp, D.rp, Ez, PE, D.rp, lane);
+        Vec4<ElF16> xh[4], xl[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t at = (int64_t)i * D.sp + c0 + 8 * g + 4 * h;
+            xh[g] = *reinterpret_cast<const Vec4<ElF16> *>(hi + at);
+            xl[g] = *reinterpret_cast<const Vec4<ElF16> *>(lo + at);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = c0 + 8 * g + 4 * h;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = (ElF16::wide(xh[g].v[e]) + ElF16::wide(xl[g].v[e])) * ex;
+                v[e] = (f * x + t.b * R[k][4 * g + e] + t.c * (W[4 * g + e] * (ex / t.sz))) * t.sx1;
+            }
+            if (LAST) {
+                if (i < D.r) {
+                    uint16_t *o = out + blockIdx.y * so;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < D.s) o[tall ? (c + e) * ldo + i : i * ldo + c + e] = ElBF16::round(v[e]);
+                }
+            } else {
+                put_x<ElF16>(hi1 + base, lo1 + base, (int64_t)i * D.sp + c, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tr1[base + (int64_t)(c + e) * D.rp + i] = f16_bits(v[e]);
+            }
+        }
+    }
+}
+
 struct NsPlan {
     NsDims D;
     int64_t part, da, db, a, b, x[2], xl[2], total;
@@ -325,6 +533,28 @@ NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int t)
     return p;
 }
 
+struct ChainPlan {
+    ChainDims D;
+    int64_t hi[2], lo[2], tr[2], total;
+};
+
+ChainPlan chain_plan(int64_t batch, int64_t m, int64_t n)
+{
+    ChainPlan p{};
+    p.D.r = (int)std::min(m, n);
+    p.D.s = (int)std::max(m, n);
+    p.D.rp = (int)up_h(p.D.r, 64);
+    p.D.sp = (int)up_h(p.D.s, 64);
+    const int64_t bytes = up_h(2 * batch * p.D.rp * p.D.sp, 256);
+    for (int i = 0; i < 2; ++i) {
+        p.hi[i] = (3 * i) * bytes;
+        p.lo[i] = (3 * i + 1) * bytes;
+        p.tr[i] = (3 * i + 2) * bytes;
+    }
+    p.total = 6 * bytes;
+    return p;
+}
+
 // largest |s (a + b s^2 + c s^4)| over 0 <= s <= top: at the end or at a root
 // of a + 3 b u + 5 c u^2, u = s^2
 double step_bound(const double *co, double top)
@@ -352,6 +582,44 @@ double step_bound(const double *co, double top)
 double scale16(double bound, double most)
 {
     return std::min(most, exp2(floor(14.0 - log2(std::max(bound, 1e-300)))));
+}
+
+hipError_t chain_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, int64_t n, int64_t ldg, int64_t sg,
+                     const double *co, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so, char *ws)
+{
+    const ChainPlan p = chain_plan(batch, m, n);
+    const ChainDims D = p.D;
+    const auto at = [&](int64_t o) { return (uint16_t *)(ws + o); };
+    const double want = exp2(floor(0.5 * log2((double)m * (double)n)));
+    double top = 1.0, sx = scale16(1.0, want);
+    const dim3 grid((unsigned)(D.rp / 32), (unsigned)batch);
+    hipLaunchKernelGGL(k_chain_load, grid, dim3(512), 0, stream, (const uint16_t *)G, (int)m, (int)n, ldg, sg, D, eps,
+                       (float)sx, at(p.hi[0]), at(p.lo[0]), at(p.tr[0]));
+    SPEC_LAUNCH_CHECK();
+    const int cb = (int)cdiv_h(D.sp, 256);
+    for (int k = 0; k < steps; ++k) {
+        const double *c = co + 3 * k;
+        const double na = top * top, next = 1.02 * step_bound(c, top);
+        const bool last = k == steps - 1;
+        const ChainStep t{(float)c[0], (float)c[1], (float)c[2], (float)sx, (float)(last ? scale : scale16(next, want)),
+                          (float)scale16(na, 16384.0), (float)scale16(2.0 * na * top, 16384.0),
+                          (float)scale16(na * na, 16384.0)};
+        const int a = k & 1, b = a ^ 1;
+#define CHAIN_STEP(CB, LAST)                                                                                           \
+    hipLaunchKernelGGL((k_chain_step<CB, LAST>), grid, dim3(512), 0, stream, at(p.hi[a]), at(p.lo[a]), at(p.tr[a]), D, t, \
+                       at(p.hi[b]), at(p.lo[b]), at(p.tr[b]), (uint16_t *)O, ldo, so, m > n)
+        if (cb == 1 && last) CHAIN_STEP(1, true);
+        else if (cb == 1) CHAIN_STEP(1, false);
+        else if (cb == 2 && last) CHAIN_STEP(2, true);
+        else if (cb == 2) CHAIN_STEP(2, false);
+        else if (last) CHAIN_STEP(4, true);
+        else CHAIN_STEP(4, false);
+#undef CHAIN_STEP
+        SPEC_LAUNCH_CHECK();
+        top = next;
+        sx = t.sx1;
+    }
+    return hipSuccess;
 }
 
 template <typename GT, typename E, bool TALL>
@@ -425,16 +693,20 @@ hipError_t ns_run(hipStream_t stream, const void *G, int64_t batch, int64_t m, i
 
 size_t orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int t)
 {
+    if (t == SPEC_BF16 && chain_fits(m, n)) return (size_t)chain_plan(batch, m, n).total;
     return (size_t)ns_plan(batch, m, n, t).total;
 }
 
-// whether the iterates stay within f16's range: their bounds reach at most 2^7
+// whether f16 holds the iterates and the products in between
 bool orthogonalize_bounded(const double *co, int steps)
 {
     double top = 1.0;
     for (int k = 0; k < steps; ++k) {
         const double na = top * top;
-        if (!(na <= 16384.0 && fabs(co[3 * k + 1]) * na + fabs(co[3 * k + 2]) * na * na <= 16384.0)) return false;
+        // A, b A + c A^2, A^2 and (A - D) X within f16's range at scale one
+        if (!(na * na <= 16384.0 && 2.0 * na * top <= 16384.0 &&
+              fabs(co[3 * k + 1]) * na + fabs(co[3 * k + 2]) * na * na <= 16384.0))
+            return false;
         top = 1.02 * step_bound(co + 3 * k, top);
     }
     return top <= 16384.0;
@@ -445,6 +717,8 @@ hipError_t launch_orthogonalize(hipStream_t stream, const void *G, int t, int64_
                                 int64_t ldo, int64_t so, void *ws)
 {
     char *w = (char *)ws;
+    if (t == SPEC_BF16 && chain_fits(m, n))
+        return chain_run(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w);
     if (t == SPEC_BF16)
         return m > n ? ns_run<ElBF16, ElF16, true>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w)
                      : ns_run<ElBF16, ElF16, false>(stream, G, batch, m, n, ldg, sg, co, steps, eps, scale, O, ldo, so, w);
