@@ -300,9 +300,13 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
 
 // ------------------------------------------------------------------ small matrices
 
-// X (r x s, r <= s, whatever G's orientation) is kept row-major in `hi`, `lo`
-// (rp rows of pitch sp, padding zero) and, its leading part, transposed in `tr`
-// (sp rows of pitch rp): every product then reads both operands along k.
+// X (r x s, r <= s, whatever G's orientation; padded with zeros to rp x sp) is kept
+// in `hi` and `lo`, its leading part also transposed (sp x rp) in `tr`: every
+// product then reads both operands along k.  All of them, and the operands in
+// LDS, lie in the order of the MFMA's fragments: blocks of 32 rows, in them groups
+// of 16 k, in them 64 runs of 8 (the row, then the half of the group), so that a
+// wave's fragment is 1 KB in a run.  (Row-major, a fragment met 32 cache lines for
+// 32 bytes each, and reading X took 10 of a step's 17 us.)
 struct ChainDims {
     int r, s, rp, sp;  // rp, sp: rounded up to 64
 };
@@ -320,59 +324,128 @@ inline bool chain_fits(int64_t m, int64_t n)
 using h8 = f16x8_t;
 SPEC_DEVICE uint16_t f16_bits(float x) { return ElF16::round(x); }
 
-// 32 x 32 block sum_k P[p][k] Q[q][k]: P in memory (pitch ldp), Q in LDS (pitch
-// ldq); k a multiple of 64
-SPEC_DEVICE f32x16_t chain_product(const uint16_t *__restrict__ P, int ldp, const uint16_t *Q, int ldq, int K, int lane)
+// place of element (row, k) of a matrix with K columns
+SPEC_DEVICE int chain_at(int row, int k, int K)
 {
-    f32x16_t acc;
+    return (row >> 5) * 32 * K + (k >> 4) * 512 + ((row & 31) + 32 * ((k >> 3) & 1)) * 8 + (k & 7);
+}
+
+// a block of 32 rows of a product's operand in memory
+struct ChainRows {
+    const uint16_t *p;
+    SPEC_DEVICE ChainRows(const uint16_t *block, int, int lane) : p(block + lane * 8) {}
+    SPEC_DEVICE h8 at(int k) const { return *reinterpret_cast<const h8 *>(p + k * 32); }
+};
+// the same in registers, for K up to 256: read once, used by two products
+struct ChainHeld {
+    h8 a[16];
+    SPEC_DEVICE ChainHeld(const uint16_t *block, int K, int lane)
+    {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    const uint16_t *p = P + (lane & 31) * ldp + 8 * (lane >> 5), *q = Q + (lane & 31) * ldq + 8 * (lane >> 5);
-#pragma unroll 4
-    for (int k = 0; k < K; k += 64) {
-        h8 a[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const h8 *>(p + k + 16 * j);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j], *reinterpret_cast<const h8 *>(q + k + 16 * j), acc, 0, 0, 0);
+        for (int j = 0; j < 16; ++j) a[j] = 16 * j < K ? *reinterpret_cast<const h8 *>(block + j * 512 + lane * 8) : h8{};
     }
-    return acc;
+};
+
+SPEC_DEVICE f32x16_t chain_zero()
+{
+    f32x16_t z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.f;
+    return z;
+}
+
+// 32 x 32 block sum_k P[p][k] Q[q][k] with Q's rows in LDS; the sums of even and
+// odd groups of 16 apart, so that a product need not wait for the one before
+SPEC_DEVICE f32x16_t chain_product(const ChainRows &P, const uint16_t *Q, int K, int lane)
+{
+    f32x16_t s0 = chain_zero(), s1 = chain_zero();
+    const h8 *q = reinterpret_cast<const h8 *>(Q) + lane;
+#pragma unroll 2
+    for (int k = 0; k < K; k += 64) {
+        h8 a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = P.at(k + 16 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = q[(k / 16 + j) * 64];
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            s0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j], b[j], s0, 0, 0, 0);
+            s1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j + 1], b[j + 1], s1, 0, 0, 0);
+        }
+    }
+    return s0 + s1;
+}
+SPEC_DEVICE f32x16_t chain_product(const ChainHeld &P, const uint16_t *Q, int K, int lane)
+{
+    f32x16_t s0 = chain_zero(), s1 = chain_zero();
+    const h8 *q = reinterpret_cast<const h8 *>(Q) + lane;
+#pragma unroll
+    for (int j0 = 0; j0 < 16; j0 += 4)
+        if (16 * j0 < K) {
+            h8 b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = q[(j0 + j) * 64];
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                s0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(P.a[j0 + j], b[j], s0, 0, 0, 0);
+                s1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(P.a[j0 + j + 1], b[j + 1], s1, 0, 0, 0);
+            }
+        }
+    return s0 + s1;
 }
 
 // grid (rp / 32, batch), 512 threads: X = G sx / (norm + eps).  Every workgroup
 // sums all squares itself (at most 256 KB from the L2).
 __global__ __launch_bounds__(512) void k_chain_load(const uint16_t *__restrict__ G, int m, int n, int64_t ldg, int64_t sg,
-                                                    ChainDims D, double eps, float sx, uint16_t *__restrict__ hi,
+                                                    int vec, ChainDims D, double eps, float sx, uint16_t *__restrict__ hi,
                                                     uint16_t *__restrict__ lo, uint16_t *__restrict__ tr)
 {
     __shared__ double red[8];
     const uint16_t *g = G + blockIdx.y * sg;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     double s = 0.0;
-    for (int i = wave; i < m; i += 8)
-#pragma unroll 4
-        for (int j = lane; j < n; j += 64) {
-            const double v = (double)bf16_to_f32(g[i * ldg + j]);
-            s += v * v;
+    // a wave per row, eight rows requested together
+    for (int i = wave; i < m; i += 64)
+        for (int j = 4 * lane; j < n; j += 256) {
+            float v[8][4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int ik = i + 8 * k;
+                row4<ElBF16>(g + min(ik, m - 1) * ldg, ik < m ? j : n, n, vec, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += (double)v[k][e] * (double)v[k][e];
         }
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if (lane == 0) red[wave] = s;
     __syncthreads();
     s = 0.0;
-    for (int w = 0; w < 8; ++w) s += red[w];
+    for (int k = 0; k < 8; ++k) s += red[k];
     const float inv = (float)((double)sx / (sqrt(s) + eps));
     const int i0 = blockIdx.x * 32;
     const int64_t base = (int64_t)blockIdx.y * D.rp * D.sp;
     const bool tall = m > n;
-    for (int u = tid; u < 32 * D.sp; u += 512) {
-        // along G's rows: columns of X for a wide G, rows of X for a tall one
-        const int q = tall ? u & 31 : u / D.sp, c = tall ? u >> 5 : u % D.sp, i = i0 + q;
-        const float v = i < D.r && c < D.s ? bf16_to_f32(tall ? g[c * ldg + i] : g[i * ldg + c]) * inv : 0.f;
-        const uint16_t h = f16_bits(v);
-        hi[base + (int64_t)i * D.sp + c] = h;
-        lo[base + (int64_t)i * D.sp + c] = f16_bits(v - ElF16::wide(h));
-        tr[base + (int64_t)c * D.rp + i] = h;
+    // along G's rows: columns of X for a wide G, rows of X for a tall one
+    const int q0 = tall ? lane & 31 : wave * 4, c0 = tall ? wave * 2 + (lane >> 5) : lane;
+    const int qk = tall ? 0 : 1, ck = tall ? 16 : 0;
+    for (int cb = 0; cb < D.sp; cb += 128) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + q0 + (k & 3) * qk, c = cb + c0 + (k & 3) * ck + 64 * (k >> 2);
+            v[k] = i < D.r && c < D.s ? bf16_to_f32(tall ? g[c * ldg + i] : g[i * ldg + c]) * inv : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + q0 + (k & 3) * qk, c = cb + c0 + (k & 3) * ck + 64 * (k >> 2);
+            if (c >= D.sp) continue;
+            const uint16_t h = f16_bits(v[k]);
+            hi[base + chain_at(i, c, D.sp)] = h;
+            lo[base + chain_at(i, c, D.sp)] = f16_bits(v[k] - ElF16::wide(h));
+            tr[base + chain_at(c, i, D.rp)] = h;
+        }
     }
 }
 
@@ -384,37 +457,64 @@ struct ChainStep {
 
 // grid (rp / 32, batch), 512 threads; CB: blocks of 32 columns per wave
 template <int CB, bool LAST>
-__global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
+__global__ __launch_bounds__(512, 2) void k_chain_step(const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
                                                     const uint16_t *__restrict__ tr, ChainDims D, ChainStep t,
                                                     uint16_t *__restrict__ hi1, uint16_t *__restrict__ lo1,
                                                     uint16_t *__restrict__ tr1, uint16_t *__restrict__ out, int64_t ldo,
                                                     int64_t so, int tall)
 {
-    constexpr int PX = CB * 256 + 8;  // LDS pitches: 16 bytes past a multiple of 256, so that 16 rows meet 16 slots
-    constexpr int PE = CHAIN_R + 8;
-    __shared__ __attribute__((aligned(16))) uint16_t Q[32 * PX], Ez[32 * PE];  // Q: X_i, then R_i
+    __shared__ __attribute__((aligned(16))) uint16_t Q[32 * CB * 256], Ez[32 * CHAIN_R];  // Q: X_i, then R_i
     __shared__ float dd[32], zz[32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, q = lane & 31;
     const int i0 = blockIdx.x * 32;
     const int64_t base = (int64_t)blockIdx.y * D.rp * D.sp;
     hi += base, lo += base, tr += base;
-    for (int u = tid; u < 32 * (D.sp / 8); u += 512) {
-        const int r = u / (D.sp / 8), c = u % (D.sp / 8);
-        *reinterpret_cast<uint4 *>(&Q[r * PX + 8 * c]) = *reinterpret_cast<const uint4 *>(hi + (int64_t)(i0 + r) * D.sp + 8 * c);
-    }
-    __syncthreads();
-    const float ex = 1.f / t.sx;
+    const uint16_t *own_hi = hi + i0 * D.sp, *own_lo = lo + i0 * D.sp;  // this workgroup's rows
+    // X_i to LDS first, then everything that the first products take
+    uint4 mine[CB * 2];
+#pragma unroll
+    for (int k = 0; k < CB * 2; ++k)
+        if (tid + 512 * k < 4 * D.sp) mine[k] = reinterpret_cast<const uint4 *>(own_hi)[tid + 512 * k];
     const int jb = wave;  // this wave's block of 32 rows j, and its blocks wave, wave + 8, .. of 32 columns
     const bool rows = jb * 32 < D.rp, own = jb == (int)blockIdx.x;
-    const auto four = [&](uint16_t *o, const f32x16_t &v, int g, float scale) {
-        Vec4<ElF16> x;
+    // one block of columns per wave: its operands and its X stay in registers,
+    // all requested before the first product
+    using Rows = typename std::conditional<CB == 1, ChainHeld, ChainRows>::type;
+    const bool held = wave * 32 < D.sp;
+    const Rows Pj(hi + (rows ? jb : 0) * 32 * D.sp, D.sp, lane);
+    const Rows Pc(tr + (held ? wave : 0) * 32 * D.rp, D.rp, lane);
+    // place of the four elements of row q at column c0 + 8 g + 4 h in a block
+    const auto place = [&](int c0, int g) { return (c0 / 16 + (g >> 1)) * 512 + (q + 32 * (g & 1)) * 8 + 4 * h; };
+    Vec4<ElF16> xh[4], xl[4];
+    const auto fetch_x = [&](int c0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x.v[e] = f16_bits(v[4 * g + e] * scale);
-        *reinterpret_cast<Vec4<ElF16> *>(o + 8 * g + 4 * h) = x;
+        for (int g = 0; g < 4; ++g) {
+            xh[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_hi + place(c0, g));
+            xl[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_lo + place(c0, g));
+        }
+    };
+    if (CB == 1 && held) fetch_x(wave * 32);
+    const auto columns = [&](int k) {
+        if constexpr (CB == 1) return Pc;
+        else return ChainRows(tr + (wave + 8 * k) * 32 * D.rp, D.rp, lane);
+    };
+#pragma unroll
+    for (int k = 0; k < CB * 2; ++k)
+        if (tid + 512 * k < 4 * D.sp) reinterpret_cast<uint4 *>(Q)[tid + 512 * k] = mine[k];
+    __syncthreads();
+    const float ex = 1.f / t.sx;
+    const auto four = [&](uint16_t *o, int c0, const f32x16_t &v, float scale) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            Vec4<ElF16> x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.v[e] = f16_bits(v[4 * g + e] * scale);
+            *reinterpret_cast<Vec4<ElF16> *>(o + place(c0, g)) = x;
+        }
     };
     f32x16_t E;
     if (rows) {
-        E = chain_product(hi + (int64_t)jb * 32 * D.sp, D.sp, Q, PX, D.sp, lane);
+        E = chain_product(Pj, Q, D.sp, lane);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             E[e] *= ex * ex;
@@ -423,8 +523,7 @@ __global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__
                 E[e] = 0.f;
             }
         }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) four(&Ez[q * PE + jb * 32], E, g, t.sa);
+        four(Ez, jb * 32, E, t.sa);
     }
     __syncthreads();  // Q has been read, E and its diagonal are written
     f32x16_t R[CB];
@@ -432,16 +531,15 @@ __global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__
     for (int k = 0; k < CB; ++k) {
         const int c0 = (wave + 8 * k) * 32;
         if (c0 < D.sp) {
-            R[k] = chain_product(tr + (int64_t)c0 * D.rp, D.rp, Ez, PE, D.rp, lane);
+            R[k] = chain_product(columns(k), Ez, D.rp, lane);
 #pragma unroll
             for (int e = 0; e < 16; ++e) R[k][e] *= ex / t.sa;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) four(&Q[q * PX + c0], R[k], g, t.sr);
+            four(Q, c0, R[k], t.sr);
         }
     }
     __syncthreads();
     if (rows) {
-        const f32x16_t Z = chain_product(hi + (int64_t)jb * 32 * D.sp, D.sp, Q, PX, D.sp, lane);
+        const f32x16_t Z = chain_product(Pj, Q, D.sp, lane);
         const float d = dd[q];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -454,8 +552,7 @@ __global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__
             }
             E[e] = z;
         }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) four(&Ez[q * PE + jb * 32], E, g, t.sz);
+        four(Ez, jb * 32, E, t.sz);
     }
     __syncthreads();
     const float f = t.a + t.b * dd[q] + t.c * zz[q];
@@ -464,14 +561,8 @@ __global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__
     for (int k = 0; k < CB; ++k) {
         const int c0 = (wave + 8 * k) * 32;
         if (c0 >= D.sp) continue;
-        const f32x16_t W = chain_product(tr + (int64_t)c0 * D.rp, D.rp, Ez, PE, D.rp, lane);
-        Vec4<ElF16> xh[4], xl[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int64_t at = (int64_t)i * D.sp + c0 + 8 * g + 4 * h;
-            xh[g] = *reinterpret_cast<const Vec4<ElF16> *>(hi + at);
-            xl[g] = *reinterpret_cast<const Vec4<ElF16> *>(lo + at);
-        }
+        const f32x16_t W = chain_product(columns(k), Ez, D.rp, lane);
+        if (CB > 1) fetch_x(c0);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int c = c0 + 8 * g + 4 * h;
@@ -489,9 +580,9 @@ __global__ __launch_bounds__(512) void k_chain_step(const uint16_t *__restrict__
                         if (c + e < D.s) o[tall ? (c + e) * ldo + i : i * ldo + c + e] = ElBF16::round(v[e]);
                 }
             } else {
-                put_x<ElF16>(hi1 + base, lo1 + base, (int64_t)i * D.sp + c, v);
+                put_x<ElF16>(hi1 + base, lo1 + base, i0 * D.sp + place(c0, g), v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tr1[base + (int64_t)(c + e) * D.rp + i] = f16_bits(v[e]);
+                for (int e = 0; e < 4; ++e) tr1[base + chain_at(c + e, i, D.rp)] = f16_bits(v[e]);
             }
         }
     }
@@ -593,7 +684,8 @@ hipError_t chain_run(hipStream_t stream, const void *G, int64_t batch, int64_t m
     const double want = exp2(floor(0.5 * log2((double)m * (double)n)));
     double top = 1.0, sx = scale16(1.0, want);
     const dim3 grid((unsigned)(D.rp / 32), (unsigned)batch);
-    hipLaunchKernelGGL(k_chain_load, grid, dim3(512), 0, stream, (const uint16_t *)G, (int)m, (int)n, ldg, sg, D, eps,
+    const int vec = n % 4 == 0 && (uintptr_t)G % 8 == 0 && ldg % 4 == 0 && sg % 4 == 0;
+    hipLaunchKernelGGL(k_chain_load, grid, dim3(512), 0, stream, (const uint16_t *)G, (int)m, (int)n, ldg, sg, vec, D, eps,
                        (float)sx, at(p.hi[0]), at(p.lo[0]), at(p.tr[0]));
     SPEC_LAUNCH_CHECK();
     const int cb = (int)cdiv_h(D.sp, 256);
