@@ -338,7 +338,7 @@ struct Mm {
     static SPEC_DEVICE float4 *own_part(const Lds &s)
     {
         constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
-        static_assert(32 * PC * 16 * 2 == P_BYTES && NT / 128 <= 2 * STAGES, "two waves share a stage's operand");
+        static_assert(32 * PC * 16 * 2 <= P_BYTES && NT / 128 <= 2 * STAGES, "two waves share a stage's operand");
         const int wave = threadIdx.x >> 6, part = wave >> 1;
         char *mine = s.p[0];  // (selected, not indexed: LDS objects have no table of addresses)
         mm_for<1, NT / 128>([&](auto I) {
@@ -374,10 +374,10 @@ struct Mm {
                 }
         } else {
             constexpr int PC = BP / WP / 4;  // groups of four in a wave's row
-            constexpr int AT = PC / 2 % 8 == 0 ? 8 : 6;
+            constexpr int AT = PC / 2 % 8 == 0 ? 8 : PC / 2 % 6 == 0 ? 6 : 4;
             static_assert(PC / 2 % AT == 0, "groups at a time");
             float4 *buf = own_part(s);
-            const auto slot = [](int q, int c) { return q * PC + (c ^ (PC == 24 ? (q >> 1) & 7 : q & 15)); };
+            const auto slot = [](int q, int c) { return q * PC + (c ^ (PC == 24 ? (q >> 1) & 7 : PC == 8 ? q & 7 : q & 15)); };
             const int p0 = wave_p0(wave), q0 = wave_q0(wave);
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
@@ -504,6 +504,11 @@ struct Tile192 {
 };
 struct Tile128 {
     static constexpr int BP = 128, BQ = 128, WP = 2, WQ = 2, WK = 1, STAGES = 2, NT = 256;
+};
+// few rows of Q (one decode step's tokens) against many of P: bound by reading P,
+// so narrow, with four stages (two workgroups keep 120 KB per CU in flight)
+struct TileRow {
+    static constexpr int BP = 128, BQ = 32, WP = 4, WQ = 1, WK = 1, STAGES = 4, NT = 256;
 };
 struct Tile64 {
     static constexpr int BP = 64, BQ = 64, WP = 1, WQ = 1, WK = 4, STAGES = 4, NT = 256;

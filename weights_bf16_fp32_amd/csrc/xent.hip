@@ -537,6 +537,9 @@ inline bool big_tiles(int64_t rows, int64_t cols)
     return rows > 128 && cols > 128 && cdiv_h(rows, 256) * cdiv_h(cols, 256) >= 192;
 }
 
+// the logits of up to this many tokens take the tile for few rows
+constexpr int64_t FEW_TOKENS = 64;
+
 template <typename E, typename C>
 hipError_t fwd_piece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t ldw, int64_t vn, int64_t v,
                      int64_t T, float scale, int64_t ldpart, char *ws)
@@ -617,8 +620,9 @@ hipError_t xent_fwd(hipStream_t stream, const void *H, int64_t ldh, const void *
         const st *Wv;
         e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
         if (e != hipSuccess) return e;
-        e = big ? fwd_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws)
-                : fwd_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws);
+        e = T <= FEW_TOKENS ? fwd_piece<E, TileRow>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws)
+            : big           ? fwd_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws)
+                            : fwd_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ldpart, ws);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv_h(T, 4)), dim3(256), 0, stream, (const float2 *)(ws + pl.part),
@@ -643,8 +647,9 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
         st *dWv = (st *)dW + v * lddw;
         e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
         if (e != hipSuccess) return e;
-        e = big_tiles(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
-                             : g_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ws);
+        e = T <= FEW_TOKENS      ? g_piece<E, TileRow>(stream, pl, Wv, ld, vn, v, T, scale, ws)
+            : big_tiles(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
+                                 : g_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ws);
         if (e != hipSuccess) return e;
         e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, dWv, lddw, beta, ws)
                              : dw_piece<E, Tile128>(stream, pl, vn, d, dWv, lddw, beta, ws);
