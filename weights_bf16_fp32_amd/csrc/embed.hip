@@ -15,11 +15,12 @@
 // in a neighbour's share, to be joined by a second pass.
 //
 //   k_embed      lookup
-//   k_eg_start   zero rows; beside them, up to 16384 positions sorted by one workgroup
+//   k_eg_start   up to 16384 positions sorted by one workgroup; beside it, zeros
+//                over the first rows of dE
 //   k_sort_hist  more positions: digits per share of the positions,
 //   k_sort_scan  first place of every (digit, share),
 //   k_sort_move  positions to their places
-//   k_eg_sum     sums over sorted positions
+//   k_eg_sum     sums over sorted positions; beside them, zeros in the other rows
 //   k_eg_join    sums of rows that cross shares
 #include <algorithm>
 
@@ -42,7 +43,21 @@ struct __attribute__((aligned(VEC * sizeof(S)))) Pack {
     S v[VEC];
 };
 
-// grid (column blocks, rows / RPB): a wave per row
+// zeros that nothing reads back soon: past the caches (LINES), whose room the
+// partial sums keep, where rows are whole cache lines; parts of lines meet in the L2
+template <typename S, int VEC, bool LINES>
+SPEC_DEVICE void put_zero(S *p)
+{
+    if constexpr (LINES) {
+        static_assert(VEC * sizeof(S) == 16, "16 bytes");
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(p));
+    } else {
+        *reinterpret_cast<Pack<S, VEC> *>(p) = Pack<S, VEC>{};
+    }
+}
+
+// a wave per row
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_embed(const typename E::st *__restrict__ tab, int64_t V, int64_t d, int64_t lde,
                                                const void *__restrict__ ids, int is64, int64_t n, float scale,
@@ -165,7 +180,6 @@ __global__ __launch_bounds__(256) void k_sort_move(const int *__restrict__ keys,
 
 constexpr int ONE_MAX = 16384;  // positions
 constexpr int ONE_BITS = 9;     // of the key per pass
-constexpr int ONE_ROUNDS = ONE_MAX / 1024;
 
 struct OneLds {
     int cnt[16][1 << ONE_BITS];
@@ -176,14 +190,15 @@ struct OneLds {
 // The positions in order of their keys, by 1024 threads: keys and positions stay
 // in registers (wave w holds the places w 64 R .. in rounds of 64) and change
 // places through LDS once per pass.
-SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n, int passes, int *okeys, int *oidx)
+template <int ROUNDS>
+SPEC_DEVICE void sort_rounds(OneLds &s, const void *ids, int is64, int64_t V, int n, int passes, int *okeys, int *oidx)
 {
     constexpr int ND = 1 << ONE_BITS;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int R = (n + 1023) / 1024;
-    int key[ONE_ROUNDS], idx[ONE_ROUNDS], at[ONE_ROUNDS];
+    int key[ROUNDS], idx[ROUNDS], at[ROUNDS];
 #pragma unroll
-    for (int r = 0; r < ONE_ROUNDS; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
         const int i = (wave * R + r) * 64 + lane;
         idx[r] = i;
         key[r] = r < R && i < n ? first_key(ids, is64, i, V) : 0;
@@ -193,9 +208,8 @@ SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n
         for (int i = tid; i < 16 * ND; i += 1024) s.cnt[i / ND][i % ND] = 0;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ONE_ROUNDS; ++r) {
-            if (r >= R) break;
-            const bool in = (wave * R + r) * 64 + lane < n;
+        for (int r = 0; r < ROUNDS; ++r) {
+            const bool in = r < R && (wave * R + r) * 64 + lane < n;
             const int dg = (key[r] >> shift) & (ND - 1);
             uint64_t same = __ballot(in);  // lanes with this lane's digit
 #pragma unroll
@@ -231,36 +245,46 @@ SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n
             for (int w = 0; w < 16; ++w) s.cnt[w][tid] += base;
         }
         __syncthreads();
-        const bool last = pass == passes - 1;
 #pragma unroll
-        for (int r = 0; r < ONE_ROUNDS; ++r) {
+        for (int r = 0; r < ROUNDS; ++r) {
             if (r >= R || (wave * R + r) * 64 + lane >= n) continue;
             at[r] += s.cnt[wave][(key[r] >> shift) & (ND - 1)];
-            if (last) {
-                okeys[at[r]] = key[r];
-                oidx[at[r]] = idx[r];
-            } else {
-                s.buf[at[r]] = key[r];
-            }
+            s.buf[at[r]] = key[r];
         }
-        if (last) return;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ONE_ROUNDS; ++r) {
+        for (int r = 0; r < ROUNDS; ++r) {
             const int i = (wave * R + r) * 64 + lane;
             if (r < R && i < n) key[r] = s.buf[i];
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ONE_ROUNDS; ++r)
+        for (int r = 0; r < ROUNDS; ++r)
             if (r < R && (wave * R + r) * 64 + lane < n) s.buf[at[r]] = idx[r];
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ONE_ROUNDS; ++r) {
+        for (int r = 0; r < ROUNDS; ++r) {
             const int i = (wave * R + r) * 64 + lane;
             if (r < R && i < n) idx[r] = s.buf[i];
         }
     }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = (wave * R + r) * 64 + lane;
+        if (r < R && i < n) {
+            okeys[i] = key[r];
+            oidx[i] = idx[r];
+        }
+    }
+}
+
+// (the rounds are a constant, so that the arrays are registers)
+SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n, int passes, int *okeys, int *oidx)
+{
+    if (n <= 2048) sort_rounds<2>(s, ids, is64, V, n, passes, okeys, oidx);
+    else if (n <= 4096) sort_rounds<4>(s, ids, is64, V, n, passes, okeys, oidx);
+    else if (n <= 8192) sort_rounds<8>(s, ids, is64, V, n, passes, okeys, oidx);
+    else sort_rounds<ONE_MAX / 1024>(s, ids, is64, V, n, passes, okeys, oidx);
 }
 
 // ------------------------------------------------------------------ sums
@@ -268,12 +292,12 @@ SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n
 constexpr int EG_SHARE = 32;  // sorted positions per workgroup
 constexpr int EG_AHEAD = 8;   // rows in flight per thread
 
-// Workgroup 0 sorts (sort != 0); the others write zeros over dE's rows, which
-// take as long as their bytes: the sort runs beside them.
-template <typename O, int VEC>
+// Workgroup 0 sorts (sort != 0); the others write zeros over dE's rows below
+// `rows`, about as many as are written while it does.
+template <typename O, int VEC, bool LINES>
 __global__ __launch_bounds__(1024) void k_eg_start(const void *__restrict__ ids, int is64, int64_t V, int n, int passes,
                                                    int sort, int *__restrict__ okeys, int *__restrict__ oidx,
-                                                   typename O::st *__restrict__ dE, int64_t d, int64_t ldd)
+                                                   typename O::st *__restrict__ dE, int64_t rows, int64_t d, int64_t ldd)
 {
     __shared__ OneLds lds;
     if (sort && blockIdx.x == 0) {
@@ -281,10 +305,9 @@ __global__ __launch_bounds__(1024) void k_eg_start(const void *__restrict__ ids,
         return;
     }
     const int64_t first = (int64_t)(blockIdx.x - sort) * 16 + (threadIdx.x >> 6), step = 16 * (int64_t)(gridDim.x - sort);
-    const Pack<typename O::st, VEC> z{};
-    for (int64_t v = first; v < V; v += step)
+    for (int64_t v = first; v < rows; v += step)
         for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64)
-            *reinterpret_cast<Pack<typename O::st, VEC> *>(dE + v * ldd + c) = z;
+            put_zero<typename O::st, VEC, LINES>(dE + v * ldd + c);
 }
 
 template <typename O, int VEC>
@@ -297,18 +320,48 @@ SPEC_DEVICE void eg_put(typename O::st *row, int64_t c, const float (&s)[VEC], f
     *reinterpret_cast<Pack<typename O::st, VEC> *>(row + c) = x;
 }
 
-// grid (shares, column blocks of 256 VEC).  head[share] / tail[share]: the sum
+// Zeros in the rows v0 .. v0 + 63 that no position names: each lane looks one of
+// them up in the sorted keys.
+template <typename O, int VEC, bool LINES>
+SPEC_DEVICE void eg_gaps(const int *__restrict__ keys, int64_t n, int64_t V, int64_t v0, typename O::st *__restrict__ dE,
+                         int64_t d, int64_t ldd)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t v = v0 + lane;
+    int64_t lo = 0, hi = n;  // first position with a key of v or more
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (keys[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    const uint64_t absent = __ballot(v < V && (lo == n || keys[lo] != v));
+    for (int r = wave * 16; r < wave * 16 + 16; ++r)
+        if ((absent >> r) & 1)
+            for (int64_t c = VEC * lane; c < d; c += VEC * 64)
+                put_zero<typename O::st, VEC, LINES>(dE + (v0 + r) * ldd + c);
+}
+
+// The first shares x cols workgroups (cols: column blocks of 256 VEC) add; the
+// others write the zero rows from row0 on.  head[share] / tail[share]: the sum
 // of the share's first / last row where it began before / goes on after.
 // Positions are taken EG_AHEAD at a time, their rows requested together.
-template <typename E, typename O, int VEC>
+template <typename E, typename O, int VEC, bool LINES>
 __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict__ dY, int64_t d, int64_t ldy,
                                                 const int *__restrict__ keys, const int *__restrict__ idx, int64_t n,
                                                 int64_t V, float scale, int add, typename O::st *__restrict__ dE,
-                                                int64_t ldd, float *__restrict__ head, float *__restrict__ tail)
+                                                int64_t ldd, float *__restrict__ head, float *__restrict__ tail,
+                                                int64_t sums, int cols, int64_t row0)
 {
+    if (blockIdx.x >= sums) {
+        eg_gaps<O, VEC, LINES>(keys, n, V, row0 + ((int64_t)blockIdx.x - sums) * 64, dE, d, ldd);
+        return;
+    }
+    const int64_t share = blockIdx.x / cols;
     using P = Pack<typename E::st, VEC>;
-    const int64_t b = (int64_t)blockIdx.x * EG_SHARE, e = min<int64_t>(n, b + EG_SHARE);
-    const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
+    const int64_t b = share * EG_SHARE, e = min<int64_t>(n, b + EG_SHARE);
+    const int64_t c = VEC * ((int64_t)(blockIdx.x % cols) * 256 + threadIdx.x);
     if (c >= d || keys[b] >= V) return;
     float s[VEC];
 #pragma unroll
@@ -316,7 +369,7 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
     bool open = b > 0 && keys[b - 1] == keys[b];  // the row began before this share
     const auto leave = [&](float *p) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) p[(int64_t)blockIdx.x * d + c + k] = s[k];
+        for (int k = 0; k < VEC; ++k) p[share * d + c + k] = s[k];
     };
     int cur = keys[b];
     for (int64_t i0 = b; i0 < e; i0 += EG_AHEAD) {
@@ -423,19 +476,24 @@ EgPlan eg_plan(int64_t n, int64_t V, int64_t d)
     return p;
 }
 
-template <typename E, typename O, int VEC>
-hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
-                  int is64, float scale, int add, void *dE, int64_t ldd, char *ws)
+template <typename E, typename O, int VEC, bool LINES>
+hipError_t eg_launch(hipStream_t stream, const void *dY, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
+                     int is64, float scale, int add, void *dE, int64_t ldd, char *ws)
 {
     const EgPlan p = eg_plan(n, V, d);
     typename O::st *out = (typename O::st *)dE;
     const int sort = p.one && n > 0;
-    const int fill = add ? 0 : (int)std::min<int64_t>(cdiv_h(V, 16), 2048);
+    // rows written beside the sort: what 6 TB/s write while it takes its 10 us (2048
+    // positions) to 55 us (16384); all of them where there is nothing to sort, none
+    // where more positions are sorted by kernels of their own
+    const int64_t es = sizeof(typename O::st);
+    const int64_t early = add ? 0 : (n == 0 ? V : !p.one ? 0 : std::min<int64_t>(V, (n * 18000 + (32 << 20)) / (d * es) / 64 * 64));
+    const int fill = (int)std::min<int64_t>(cdiv_h(early, 16), 2048);
     const int last = p.one ? 0 : (p.passes + 1) & 1;
     int *okeys = (int *)(ws + p.key[last]), *oidx = (int *)(ws + p.idx[last]);
     if (sort + fill > 0) {
-        hipLaunchKernelGGL((k_eg_start<O, VEC>), dim3((unsigned)(sort + fill)), dim3(1024), 0, stream, ids, is64, V, (int)n,
-                           p.passes, sort, okeys, oidx, out, d, ldd);
+        hipLaunchKernelGGL((k_eg_start<O, VEC, LINES>), dim3((unsigned)(sort + fill)), dim3(1024), 0, stream, ids, is64, V, (int)n,
+                           p.passes, sort, okeys, oidx, out, early, d, ldd);
         SPEC_LAUNCH_CHECK();
     }
     if (n == 0) return hipSuccess;
@@ -453,13 +511,27 @@ hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int6
         SPEC_LAUNCH_CHECK();
     }
     const int *keys = okeys, *idx = oidx;
-    const dim3 grid((unsigned)cdiv_h(n, EG_SHARE), (unsigned)cdiv_h(d, 256 * VEC));
+    const int64_t shares = cdiv_h(n, EG_SHARE), cols = cdiv_h(d, 256 * VEC);
+    const int64_t gaps = add ? 0 : cdiv_h(V - early, 64);
     float *head = (float *)(ws + p.head), *tail = (float *)(ws + p.tail);
-    hipLaunchKernelGGL((k_eg_sum<E, O, VEC>), grid, dim3(256), 0, stream, (const typename E::st *)dY, d, ldy, keys, idx, n,
-                       V, scale, add, out, ldd, head, tail);
+    hipLaunchKernelGGL((k_eg_sum<E, O, VEC, LINES>), dim3((unsigned)(shares * cols + gaps)), dim3(256), 0, stream,
+                       (const typename E::st *)dY, d, ldy, keys, idx, n, V, scale, add, out, ldd, head, tail, shares * cols,
+                       (int)cols, early);
     SPEC_LAUNCH_CHECK();
-    hipLaunchKernelGGL((k_eg_join<O, VEC>), grid, dim3(256), 0, stream, d, keys, n, V, scale, add, out, ldd, head, tail);
+    hipLaunchKernelGGL((k_eg_join<O, VEC>), dim3((unsigned)shares, (unsigned)cols), dim3(256), 0, stream, d, keys, n, V,
+                       scale, add, out, ldd, head, tail);
     return hipGetLastError();
+}
+
+template <typename E, typename O, int VEC>
+hipError_t eg_run(hipStream_t stream, const void *dY, int64_t n, int64_t V, int64_t d, int64_t ldy, const void *ids,
+                  int is64, float scale, int add, void *dE, int64_t ldd, char *ws)
+{
+    constexpr int64_t es = sizeof(typename O::st);
+    if constexpr (VEC * es == 16)
+        if ((uintptr_t)dE % 128 == 0 && ldd * es % 128 == 0 && d * es % 128 == 0)
+            return eg_launch<E, O, VEC, true>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, ws);
+    return eg_launch<E, O, VEC, false>(stream, dY, n, V, d, ldy, ids, is64, scale, add, dE, ldd, ws);
 }
 
 template <typename E>

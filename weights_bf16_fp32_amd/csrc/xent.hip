@@ -142,7 +142,6 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
 {
     using M = Mm<E, C, false, false>;
     MM_STAGES(M);
-    __shared__ float2 red[C::WP][C::BQ];
     const int n = *nvalid, nq = (n + C::BQ - 1) / C::BQ;
     int tp, tq;
     if (blockIdx.x >= (unsigned)(np * nq)) return;
@@ -154,6 +153,8 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wp = wave % C::WP;
     const int p0 = wp * (C::BP / C::WP) + 4 * (lane >> 5), q0 = (wave / C::WP) * (C::BQ / C::WQ) + (lane & 31);
     const int lim = (int)min<int64_t>(C::BP, vn - v0);
+    float2 *red = reinterpret_cast<float2 *>(lds.p[0]);  // [wp][q] of the waves along the vocabulary
+    static_assert(C::WP * C::BQ * sizeof(float2) <= M::P_BYTES, "room");
 #pragma unroll
     for (int b = 0; b < M::NI; ++b) {
         const int q = q0 + 32 * b;
@@ -203,15 +204,15 @@ __global__ MM_BOUNDS(C) void k_xent_fwd(const typename E::st *__restrict__ W, in
 #pragma unroll
             for (int e = 0; e < 16; ++e) s += __expf(mm.acc[m][b][e] - ref);
         s = pair32_sum(s);
-        if (lane < 32) red[wp][q] = make_float2(top, s);
+        if (lane < 32) red[wp * C::BQ + q] = make_float2(top, s);
     }
     __syncthreads();
     for (int q = threadIdx.x; q < C::BQ; q += C::NT) {
         if (t0 + q >= n) break;
-        float2 r = red[0][q];
+        float2 r = red[q];
 #pragma unroll
         for (int w = 1; w < C::WP; ++w) {
-            const float2 o = red[w][q];
+            const float2 o = red[w * C::BQ + q];
             const float top = fmaxf(r.x, o.x), ref = top == -INFINITY ? 0.f : top;
             r.y = r.y * __expf(r.x - ref) + o.y * __expf(o.x - ref);
             r.x = top;
