@@ -255,6 +255,16 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
     }
 }
 
+// The factor that G is held without: the mantissa, in [1, 2), of the first row's
+// weight.  With equal weights (the mean) the other factor is a power of two, and
+// the entries near -1 of G, the targets hardly predicted, are exact in bf16; with
+// the weights in it they would all be off by the same rounding of 1 / rows (0.2 %).
+SPEC_DEVICE float grad_unit(const float *__restrict__ pdl, int n, float scale)
+{
+    const float w = n > 0 ? fabsf(pdl[0] * scale) : 0.f;
+    return w > 0x1p-126f && w < INFINITY ? __uint_as_float((__float_as_uint(w) & 0x7fffffu) | 0x3f800000u) : 1.f;
+}
+
 // G[t][v - vbase], columns up to vn rounded up to 16 bytes (zero past vn)
 template <typename E, typename C>
 __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int64_t ldw,
@@ -282,12 +292,13 @@ __global__ MM_BOUNDS(C) void k_xent_g(const typename E::st *__restrict__ W, int6
         int y;
         float lse, w;
     };
+    const float unit = grad_unit(pdl, n, scale);
     mm.each4(lds, [&](int p, int q) {
-        return t0 + q < n ? Row{ptgt[t0 + q], plse[t0 + q], pdl[t0 + q]} : Row{};
+        return t0 + q < n ? Row{ptgt[t0 + q], plse[t0 + q], pdl[t0 + q] * scale / unit} : Row{};
     }, [&](int p, int q, float (&v)[4], const Row &r) {
         if (t0 + q >= n || p >= lim4) return;
         const int64_t y = r.y - vbase - v0;
-        const float l = r.lse, w = r.w * scale;
+        const float l = r.lse, w = r.w;
         Vec4<E> o;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -301,7 +312,8 @@ template <typename E, typename C>
 __global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, int64_t dp,
                                                                  const typename E::st *__restrict__ G, int64_t ldg,
                                                                  int64_t vn, int64_t d, const int *__restrict__ nvalid,
-                                                                 int np, int nq, typename E::st *__restrict__ dW,
+                                                                 int np, int nq, const float *__restrict__ pdl,
+                                                                 float scale, typename E::st *__restrict__ dW,
                                                                  int64_t lddw, float beta, int vec)
 {
     using M = Mm<E, C, true, true>;
@@ -313,8 +325,11 @@ __global__ MM_BOUNDS(C) void k_xent_dw(const typename E::st *__restrict__ Hp, in
     const MmSrc Q{(const char *)(G + v0), ldg * M::SZ, (int)min<int64_t>(C::BQ, vn - v0), n};
     M mm;
     mm.run(P, Q, 0, n, lds);
+    const float unit = grad_unit(pdl, (int)n, scale);
     mm.each4(lds, [&](int p, int q, float (&v)[4]) {
         if (q >= Q.lim || p >= P.lim) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= unit;
         typename E::st *o = dW + (v0 + q) * lddw + p0 + p;
         if (vec && p + 4 <= P.lim) {
             Vec4<E> r;
@@ -399,6 +414,7 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
                                                      const float *__restrict__ extra, const int *__restrict__ nvalid,
                                                      int np, int nqmax, int slots, int most, int64_t T, int64_t d,
                                                      const int *__restrict__ pos, const int *__restrict__ row,
+                                                     const float *__restrict__ pdl, float scale,
                                                      typename E::st *__restrict__ dH, int64_t lddh, int vec)
 {
     constexpr int G = C::BQ / OUT_ROWS;
@@ -418,6 +434,7 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
     mm_tile(id, np, nq, tp, tq);
     const int64_t p0 = (int64_t)tp * C::BP;
     const int shares = id >= pl.whole ? pl.ways : 1;
+    const float unit = grad_unit(pdl, n, scale);
     const float *ex = extra + (int64_t)(id - pl.whole) * pl.ways * C::BP * C::BQ;
     for (int i = threadIdx.x; i < OUT_ROWS * (C::BP / 4); i += 256) {
         const int q = r0 + i / (C::BP / 4), p = 4 * (i % (C::BP / 4)), t = tq * C::BQ + q;
@@ -428,7 +445,7 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
             s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
         }
         typename E::st *o = dH + (int64_t)row[t] * lddh + p0 + p;
-        const float v[4] = {s.x, s.y, s.z, s.w};
+        const float v[4] = {s.x * unit, s.y * unit, s.z * unit, s.w * unit};
         if (vec && p0 + p + 4 <= d) {
             Vec4<E> x;
 #pragma unroll
@@ -567,15 +584,15 @@ hipError_t g_piece(hipStream_t stream, const XentPlan &pl, const typename E::st 
 }
 
 template <typename E, typename C>
-hipError_t dw_piece(hipStream_t stream, const XentPlan &pl, int64_t vn, int64_t d, typename E::st *dW, int64_t lddw,
-                    float beta, char *ws)
+hipError_t dw_piece(hipStream_t stream, const XentPlan &pl, int64_t vn, int64_t d, float scale, typename E::st *dW,
+                    int64_t lddw, float beta, char *ws)
 {
     using st = typename E::st;
     const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(vn, C::BQ);
     const int vec = (uintptr_t)dW % (4 * sizeof(st)) == 0 && lddw % 4 == 0;
     hipLaunchKernelGGL((k_xent_dw<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream,
                        (const st *)(ws + pl.hp), pl.dp, (const st *)(ws + pl.g), pl.piece, vn, d,
-                       (const int *)(ws + pl.nvalid), np, nq, dW, lddw, beta, vec);
+                       (const int *)(ws + pl.nvalid), np, nq, (const float *)(ws + pl.pdl), scale, dW, lddw, beta, vec);
     return hipGetLastError();
 }
 
@@ -593,7 +610,8 @@ hipError_t dh_piece(hipStream_t stream, const XentPlan &pl, const typename E::st
 }
 
 template <typename E, typename C>
-hipError_t dh_out(hipStream_t stream, const XentPlan &pl, int64_t T, int64_t d, void *dH, int64_t lddh, char *ws)
+hipError_t dh_out(hipStream_t stream, const XentPlan &pl, int64_t T, int64_t d, float scale, void *dH, int64_t lddh,
+                  char *ws)
 {
     using st = typename E::st;
     const int np = (int)cdiv_h(d, C::BP), nq = (int)cdiv_h(T, C::BQ);
@@ -601,7 +619,8 @@ hipError_t dh_out(hipStream_t stream, const XentPlan &pl, int64_t T, int64_t d, 
     const int vec = (uintptr_t)dH % (4 * sizeof(st)) == 0 && lddh % 4 == 0;
     hipLaunchKernelGGL((k_xent_dh_out<E, C>), dim3((unsigned)grid), dim3(256), 0, stream, (const float *)(ws + pl.part),
                        up_h(d, 4), (const float *)(ws + pl.extra), (const int *)(ws + pl.nvalid), np, nq, pl.slots,
-                       pl.most, T, d, (const int *)(ws + pl.pos), (const int *)(ws + pl.row), (st *)dH, lddh, vec);
+                       pl.most, T, d, (const int *)(ws + pl.pos), (const int *)(ws + pl.row), (const float *)(ws + pl.pdl), scale, (st *)dH,
+                       lddh, vec);
     return hipGetLastError();
 }
 
@@ -652,14 +671,15 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
             : big_tiles(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
                                  : g_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ws);
         if (e != hipSuccess) return e;
-        e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, dWv, lddw, beta, ws)
-                             : dw_piece<E, Tile128>(stream, pl, vn, d, dWv, lddw, beta, ws);
+        e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, scale, dWv, lddw, beta, ws)
+                             : dw_piece<E, Tile128>(stream, pl, vn, d, scale, dWv, lddw, beta, ws);
         if (e != hipSuccess) return e;
         e = pl.big ? dh_piece<E, Tile256>(stream, pl, Wv, ld, vn, T, d, v == 0, ws)
                    : dh_piece<E, Tile128>(stream, pl, Wv, ld, vn, T, d, v == 0, ws);
         if (e != hipSuccess) return e;
     }
-    return pl.big ? dh_out<E, Tile256>(stream, pl, T, d, dH, lddh, ws) : dh_out<E, Tile128>(stream, pl, T, d, dH, lddh, ws);
+    return pl.big ? dh_out<E, Tile256>(stream, pl, T, d, scale, dH, lddh, ws)
+                  : dh_out<E, Tile128>(stream, pl, T, d, scale, dH, lddh, ws);
 }
 
 // dW <- beta dW where no token has a target to add
