@@ -52,7 +52,7 @@ inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
 
 // workgroups of the norm per matrix: about 64 elements per thread
-inline int norm_blocks(int64_t m, int64_t n) { return (int)std::min<int64_t>(512, cdiv_h(m * n, 64 * 256)); }
+inline int norm_blocks(int64_t m, int64_t n) { return (int)std::min<int64_t>(1024, cdiv_h(m * n, 64 * 256)); }
 
 // four consecutive elements j .. j + 3 of a row of n (zero past its end); vec:
 // the row and its neighbours are aligned to four elements
@@ -80,12 +80,14 @@ __global__ __launch_bounds__(256) void k_ns_norm(const typename G::st *__restric
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double s = 0.0;
     for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < m; i += 4 * (int64_t)gridDim.x)
-#pragma unroll 4
-        for (int64_t j = 4 * lane; j < n; j += 256) {
-            float v[4];
-            row4<G>(x + i * ld, j, n, vec, v);
+        for (int64_t j0 = 4 * lane; j0 < n; j0 += 8 * 256) {
+            float v[8][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s += (double)v[e] * (double)v[e];
+            for (int k = 0; k < 8; ++k) row4<G>(x + i * ld, min(j0 + k * 256, n), n, vec, v[k]);  // requested together
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += (double)v[k][e] * (double)v[k][e];
         }
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if (lane == 0) red[wave] = s;
@@ -120,7 +122,6 @@ __global__ __launch_bounds__(256) void k_ns_load(const typename G::st *__restric
     const float inv = (float)((double)sx / (sqrt(s) + eps));
     const int64_t i = blockIdx.x;
     const typename G::st *x = X + blockIdx.y * stride + i * ld;
-#pragma unroll 2
     for (int64_t j = 4 * threadIdx.x; j < xp; j += 1024) {
         float v[4];
         row4<G>(x, j, n, vec, v);
