@@ -38,7 +38,9 @@ SPEC_DEVICE int64_t load_id(const void *p, int is64, int64_t i)
     return is64 ? reinterpret_cast<const int64_t *>(p)[i] : (int64_t) reinterpret_cast<const int32_t *>(p)[i];
 }
 
-constexpr int PACK_ROWS = 8;  // rows per workgroup of k_xent_pack
+// rows per workgroup of k_xent_pack: few, so that the copies fill the chip; more
+// where many workgroups would each count the targets before theirs
+inline int pack_rows(int64_t T) { return T <= 65536 ? 8 : 64; }
 
 // a row of d elements to one of dp, zero past d: 16 bytes at a time where both
 // ends are aligned, else by element
@@ -69,11 +71,11 @@ __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restr
                                                    int *__restrict__ pos, int *__restrict__ row, int *__restrict__ ptgt,
                                                    const float *__restrict__ lse, const float *__restrict__ dloss,
                                                    float *__restrict__ plse, float *__restrict__ pdl,
-                                                   int *__restrict__ nvalid)
+                                                   int *__restrict__ nvalid, int rows)
 {
-    __shared__ int cnt[4], where[PACK_ROWS];
+    __shared__ int cnt[4], where[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t t0 = (int64_t)blockIdx.x * PACK_ROWS;
+    const int64_t t0 = (int64_t)blockIdx.x * rows;
     int before = 0;  // rows with a target before this block's
     for (int64_t t = tid; t < t0; t += 256) {
         const int64_t y = load_id(target, is64, t);
@@ -85,12 +87,12 @@ __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restr
     before = cnt[0] + cnt[1] + cnt[2] + cnt[3];
     if (wave == 0) {
         const int64_t t = t0 + lane;
-        const bool in = lane < PACK_ROWS && t < T;
+        const bool in = lane < rows && t < T;
         const int64_t y = in ? load_id(target, is64, t) : -1;
         const bool ok = y >= 0 && y < V;
         const uint64_t m = __ballot(ok);
         const int p = before + __popcll(m & ((1ull << lane) - 1));
-        if (lane < PACK_ROWS) where[lane] = ok ? p : -1;
+        if (lane < rows) where[lane] = ok ? p : -1;
         if (in) pos[t] = ok ? p : -1;
         if (ok) {
             ptgt[p] = (int)y;
@@ -100,10 +102,10 @@ __global__ __launch_bounds__(256) void k_xent_pack(const typename E::st *__restr
                 pdl[p] = dloss[t];
             }
         }
-        if (lane == 0 && t0 + PACK_ROWS >= T) *nvalid = before + __popcll(m);
+        if (lane == 0 && t0 + rows >= T) *nvalid = before + __popcll(m);
     }
     __syncthreads();
-    for (int r = wave; r < PACK_ROWS; r += 4) {
+    for (int r = wave; r < rows; r += 4) {
         const int p = where[r];
         if (p >= 0) copy_row(H + (t0 + r) * ldh, Hp + (int64_t)p * dp, d, dp, vec != 0, lane);
     }
@@ -461,9 +463,10 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
 
 // ------------------------------------------------------------------ sizes
 
-// Bytes of a piece's gradient G.  Larger pieces add into the f32 partial dH less
+// Bytes of a piece's gradient G, and of its rows of W (copied where they are not
+// aligned).  Larger pieces add into the f32 partial dH less
 // often (100 MB read and written per piece at 6144 x 4096).
-constexpr int64_t XENT_G_BYTES = (int64_t)256 << 20;
+constexpr int64_t XENT_PIECE_BYTES = (int64_t)256 << 20;
 
 struct XentPlan {
     int64_t dp;      // row of packed H and W: d rounded up to 64 elements
@@ -483,7 +486,7 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t d, int t, bool grad)
     p.dp = up_h(d, 64);
     p.dk = up_h(d, 16 / es);
     const int64_t Tn = std::max<int64_t>(T, 1);
-    p.piece = std::max<int64_t>(2048, XENT_G_BYTES / (es * Tn) / 256 * 256);
+    p.piece = std::max<int64_t>(2048, XENT_PIECE_BYTES / (es * std::max(Tn, p.dp)) / 256 * 256);
     p.piece = std::min<int64_t>(p.piece, up_h(V, 256));
     p.most = (int)std::max<int64_t>(1, std::min<int64_t>(p.piece / 512, 64));
     p.big = cdiv_h(T, 256) * cdiv_h(d, 256) >= 128;  // fewer are split, and smaller ones split finer
@@ -520,9 +523,9 @@ hipError_t pack(hipStream_t stream, const XentPlan &pl, const void *H, int64_t l
 {
     using st = typename E::st;
     const int vec = (uintptr_t)H % 16 == 0 && ldh * sizeof(st) % 16 == 0 && d * sizeof(st) % 16 == 0;
-    hipLaunchKernelGGL(k_xent_pack<E>, dim3((unsigned)cdiv_h(T, PACK_ROWS)), dim3(256), 0, stream, (const st *)H, ldh, d,
+    hipLaunchKernelGGL(k_xent_pack<E>, dim3((unsigned)cdiv_h(T, pack_rows(T))), dim3(256), 0, stream, (const st *)H, ldh, d,
                        pl.dp, vec, target, is64, T, V, (st *)(ws + pl.hp), (int *)(ws + pl.pos), (int *)(ws + pl.row), (int *)(ws + pl.ptgt),
-                       lse, dloss, (float *)(ws + pl.plse), (float *)(ws + pl.pdl), (int *)(ws + pl.nvalid));
+                       lse, dloss, (float *)(ws + pl.plse), (float *)(ws + pl.pdl), (int *)(ws + pl.nvalid), pack_rows(T));
     return hipGetLastError();
 }
 
