@@ -551,11 +551,14 @@ hipError_t wpiece(hipStream_t stream, const XentPlan &pl, const typename E::st *
     return hipGetLastError();
 }
 
-// 256 x 256 tiles where they fill most of the CUs; 128 x 128 where there are
-// fewer (or 128 tokens leave half of a tile empty).
+// 256 x 256 tiles or 128 x 128: those with which the busiest of 256 CUs has less to
+// do, a small tile's results taking 1.28 (16 bits) or 1.03 (f32) times as long.
+template <typename E>
 inline bool big_tiles(int64_t rows, int64_t cols)
 {
-    return rows > 128 && cols > 128 && cdiv_h(rows, 256) * cdiv_h(cols, 256) >= 192;
+    const double per = sizeof(typename E::st) == 2 ? 1.28 : 1.03;
+    const auto most = [&](int64_t e) { return (double)cdiv_h(cdiv_h(rows, e) * cdiv_h(cols, e), 256) * (double)(e * e); };
+    return most(256) <= per * most(128);
 }
 
 // the logits of up to this many tokens take the tile for few rows
@@ -635,7 +638,7 @@ hipError_t xent_fwd(hipStream_t stream, const void *H, int64_t ldh, const void *
     const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, false);
     hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, nullptr, nullptr, T, V, d, ws);
     if (e != hipSuccess) return e;
-    const bool direct = direct_w<E>(W, ldw, d), big = big_tiles(T, V);
+    const bool direct = direct_w<E>(W, ldw, d), big = big_tiles<E>(T, V);
     const int64_t piece = direct ? V : pl.piece, ldpart = cdiv_h(V, big ? 256 : 128);
     for (int64_t v = 0; v < V; v += piece) {
         const int64_t vn = std::min(piece, V - v);
@@ -671,10 +674,10 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
         e = wpiece<E>(stream, pl, (const st *)W + v * ldw, ld, d, vn, direct, ws, Wv);
         if (e != hipSuccess) return e;
         e = T <= FEW_TOKENS      ? g_piece<E, TileRow>(stream, pl, Wv, ld, vn, v, T, scale, ws)
-            : big_tiles(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
+            : big_tiles<E>(T, vn) ? g_piece<E, Tile256>(stream, pl, Wv, ld, vn, v, T, scale, ws)
                                  : g_piece<E, Tile128>(stream, pl, Wv, ld, vn, v, T, scale, ws);
         if (e != hipSuccess) return e;
-        e = big_tiles(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, scale, dWv, lddw, beta, ws)
+        e = big_tiles<E>(vn, d) ? dw_piece<E, Tile256>(stream, pl, vn, d, scale, dWv, lddw, beta, ws)
                              : dw_piece<E, Tile128>(stream, pl, vn, d, scale, dWv, lddw, beta, ws);
         if (e != hipSuccess) return e;
         e = pl.big ? dh_piece<E, Tile256>(stream, pl, Wv, ld, vn, T, d, v == 0, ws)
