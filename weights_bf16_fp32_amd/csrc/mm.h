@@ -534,8 +534,9 @@ struct Tile32 {
     __shared__ float4 red_[1024];                                                                                 \
     const typename M::Lds lds{{P0, P1, P2, P3, P4, P5, P6, P7}, {Q0, Q1, Q2, Q3, Q4, Q5, Q6, Q7}, red_}
 
-// two waves per SIMD: one workgroup of Tile256 or two of the others per CU
-#define MM_BOUNDS(C) __launch_bounds__(C::NT, 2)
+// waves per SIMD that LDS leaves: one workgroup of Tile256 (eight waves) or of
+// Tile192 (four), two of the others (four each) per CU
+#define MM_BOUNDS(C) __launch_bounds__(C::NT, C::BP == 192 ? 1 : 2)
 
 // Calls f with the tile shape that takes the least time for the busiest CU:
 // count(edge) tiles dealt to 256 CUs, a tile's time being its area times what

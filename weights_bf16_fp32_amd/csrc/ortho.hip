@@ -26,7 +26,7 @@
 // A and B are symmetric: only tiles on and below the diagonal are computed, and
 // each is written to both places.
 //
-// Small bf16 matrices (shorter side up to 256) are bound by the number of
+// Small bf16 matrices (both sides up to 256) are bound by the number of
 // dependent launches, not by their products, and take one launch per step: a
 // workgroup computes 32 rows of the next X from the whole present one by
 //   E_i = offdiag(X_i X^T),  R_i = E_i X,  Z_i = A_i A = d_i E_i + R_i X^T + diag,
@@ -318,16 +318,12 @@ __global__ MM_BOUNDS(C) void k_ns_apply(
 struct ChainDims {
     int r, s, rp, sp;  // rp, sp: rounded up to 64
 };
-constexpr int CHAIN_R = 256, CHAIN_S = 1024;
-constexpr int CHAIN_WORK = 1 << 17;  // r s at most (see chain_fits)
+constexpr int CHAIN = 256;  // the longer side at most
 
-// The shorter side bounds the blocks a wave holds; the product r s the time of a
-// step, which at 256 x 512 is what the three launches of the other path take.
-inline bool chain_fits(int64_t m, int64_t n)
-{
-    const int64_t r = std::min(m, n), s = std::max(m, n);
-    return r <= CHAIN_R && s <= CHAIN_S && r * s <= CHAIN_WORK;
-}
+// Up to here a wave holds its blocks of both operands in registers, and a
+// matrix takes 43 us (128 x 128) to 70 us (256 x 256) against 94 to 100 us of the
+// other path from 256 x 512 on; with operands read from memory 256 x 512 took 143 us.
+inline bool chain_fits(int64_t m, int64_t n) { return m <= CHAIN && n <= CHAIN; }
 
 using h8 = f16x8_t;
 SPEC_DEVICE uint16_t f16_bits(float x) { return ElF16::round(x); }
@@ -338,13 +334,7 @@ SPEC_DEVICE int chain_at(int row, int k, int K)
     return (row >> 5) * 32 * K + (k >> 4) * 512 + ((row & 31) + 32 * ((k >> 3) & 1)) * 8 + (k & 7);
 }
 
-// a block of 32 rows of a product's operand in memory
-struct ChainRows {
-    const uint16_t *p;
-    SPEC_DEVICE ChainRows(const uint16_t *block, int, int lane) : p(block + lane * 8) {}
-    SPEC_DEVICE h8 at(int k) const { return *reinterpret_cast<const h8 *>(p + k * 32); }
-};
-// the same in registers, for K up to 256: read once, used by two products
+// a block of 32 rows of a product's operand, in registers: read once, used by two products
 struct ChainHeld {
     h8 a[16];
     SPEC_DEVICE ChainHeld(const uint16_t *block, int K, int lane)
@@ -364,25 +354,6 @@ SPEC_DEVICE f32x16_t chain_zero()
 
 // 32 x 32 block sum_k P[p][k] Q[q][k] with Q's rows in LDS; the sums of even and
 // odd groups of 16 apart, so that a product need not wait for the one before
-SPEC_DEVICE f32x16_t chain_product(const ChainRows &P, const uint16_t *Q, int K, int lane)
-{
-    f32x16_t s0 = chain_zero(), s1 = chain_zero();
-    const h8 *q = reinterpret_cast<const h8 *>(Q) + lane;
-#pragma unroll 2
-    for (int k = 0; k < K; k += 64) {
-        h8 a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = P.at(k + 16 * j);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = q[(k / 16 + j) * 64];
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            s0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j], b[j], s0, 0, 0, 0);
-            s1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[j + 1], b[j + 1], s1, 0, 0, 0);
-        }
-    }
-    return s0 + s1;
-}
 SPEC_DEVICE f32x16_t chain_product(const ChainHeld &P, const uint16_t *Q, int K, int lane)
 {
     f32x16_t s0 = chain_zero(), s1 = chain_zero();
@@ -403,7 +374,7 @@ SPEC_DEVICE f32x16_t chain_product(const ChainHeld &P, const uint16_t *Q, int K,
 }
 
 // grid (rp / 32, batch), 512 threads: X = G sx / (norm + eps).  Every workgroup
-// sums all squares itself (at most 256 KB from the L2).
+// sums all squares itself (at most 128 KB from the L2).
 __global__ __launch_bounds__(512) void k_chain_load(const uint16_t *__restrict__ G, int m, int n, int64_t ldg, int64_t sg,
                                                     int vec, ChainDims D, double eps, float sx, uint16_t *__restrict__ hi,
                                                     uint16_t *__restrict__ lo, uint16_t *__restrict__ tr)
@@ -463,61 +434,51 @@ struct ChainStep {
     float sa, sr, sz;   // of E, R and Z
 };
 
-// grid (rp / 32, batch), 512 threads; CB: blocks of 32 columns per wave
-template <int CB, bool LAST>
+// grid (rp / 32, batch), 512 threads: wave w has the rows j and the columns of block w
+template <bool LAST>
 __global__ __launch_bounds__(512, 2) void k_chain_step(const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
                                                     const uint16_t *__restrict__ tr, ChainDims D, ChainStep t,
                                                     uint16_t *__restrict__ hi1, uint16_t *__restrict__ lo1,
                                                     uint16_t *__restrict__ tr1, uint16_t *__restrict__ out, int64_t ldo,
                                                     int64_t so, int tall)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t Q[32 * CB * 256], Ez[32 * CHAIN_R];  // Q: X_i, then R_i
+    __shared__ __attribute__((aligned(16))) uint16_t Q[32 * CHAIN], Ez[32 * CHAIN];  // Q: X_i, then R_i
     __shared__ float dd[32], zz[32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, q = lane & 31;
     const int i0 = blockIdx.x * 32;
     const int64_t base = (int64_t)blockIdx.y * D.rp * D.sp;
     hi += base, lo += base, tr += base;
     const uint16_t *own_hi = hi + i0 * D.sp, *own_lo = lo + i0 * D.sp;  // this workgroup's rows
-    // X_i to LDS first, then everything that the first products take
-    uint4 mine[CB * 2];
+    // X_i to LDS first, then all operands and X, requested before the first product
+    uint4 mine[2];
 #pragma unroll
-    for (int k = 0; k < CB * 2; ++k)
+    for (int k = 0; k < 2; ++k)
         if (tid + 512 * k < 4 * D.sp) mine[k] = reinterpret_cast<const uint4 *>(own_hi)[tid + 512 * k];
-    const int jb = wave;  // this wave's block of 32 rows j, and its blocks wave, wave + 8, .. of 32 columns
-    const bool rows = jb * 32 < D.rp, own = jb == (int)blockIdx.x;
-    // one block of columns per wave: its operands and its X stay in registers,
-    // all requested before the first product
-    using Rows = typename std::conditional<CB == 1, ChainHeld, ChainRows>::type;
-    const bool held = wave * 32 < D.sp;
-    const Rows Pj(hi + (rows ? jb : 0) * 32 * D.sp, D.sp, lane);
-    const Rows Pc(tr + (held ? wave : 0) * 32 * D.rp, D.rp, lane);
+    const bool rows = wave * 32 < D.rp, columns = wave * 32 < D.sp, own = wave == (int)blockIdx.x;
+    const int c0 = wave * 32;
+    const ChainHeld Pj(hi + (rows ? c0 : 0) * D.sp, D.sp, lane), Pc(tr + (columns ? c0 : 0) * D.rp, D.rp, lane);
     // place of the four elements of row q at column c0 + 8 g + 4 h in a block
-    const auto place = [&](int c0, int g) { return (c0 / 16 + (g >> 1)) * 512 + (q + 32 * (g & 1)) * 8 + 4 * h; };
+    const auto place = [&](int g) { return (c0 / 16 + (g >> 1)) * 512 + (q + 32 * (g & 1)) * 8 + 4 * h; };
     Vec4<ElF16> xh[4], xl[4];
-    const auto fetch_x = [&](int c0) {
+    if (columns) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            xh[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_hi + place(c0, g));
-            xl[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_lo + place(c0, g));
+            xh[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_hi + place(g));
+            xl[g] = *reinterpret_cast<const Vec4<ElF16> *>(own_lo + place(g));
         }
-    };
-    if (CB == 1 && held) fetch_x(wave * 32);
-    const auto columns = [&](int k) {
-        if constexpr (CB == 1) return Pc;
-        else return ChainRows(tr + (wave + 8 * k) * 32 * D.rp, D.rp, lane);
-    };
+    }
 #pragma unroll
-    for (int k = 0; k < CB * 2; ++k)
+    for (int k = 0; k < 2; ++k)
         if (tid + 512 * k < 4 * D.sp) reinterpret_cast<uint4 *>(Q)[tid + 512 * k] = mine[k];
     __syncthreads();
     const float ex = 1.f / t.sx;
-    const auto four = [&](uint16_t *o, int c0, const f32x16_t &v, float scale) {
+    const auto four = [&](uint16_t *o, const f32x16_t &v, float scale) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             Vec4<ElF16> x;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x.v[e] = f16_bits(v[4 * g + e] * scale);
-            *reinterpret_cast<Vec4<ElF16> *>(o + place(c0, g)) = x;
+            *reinterpret_cast<Vec4<ElF16> *>(o + place(g)) = x;
         }
     };
     f32x16_t E;
@@ -531,19 +492,15 @@ __global__ __launch_bounds__(512, 2) void k_chain_step(const uint16_t *__restric
                 E[e] = 0.f;
             }
         }
-        four(Ez, jb * 32, E, t.sa);
+        four(Ez, E, t.sa);
     }
     __syncthreads();  // Q has been read, E and its diagonal are written
-    f32x16_t R[CB];
+    f32x16_t R;
+    if (columns) {
+        R = chain_product(Pc, Ez, D.rp, lane);
 #pragma unroll
-    for (int k = 0; k < CB; ++k) {
-        const int c0 = (wave + 8 * k) * 32;
-        if (c0 < D.sp) {
-            R[k] = chain_product(columns(k), Ez, D.rp, lane);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) R[k][e] *= ex / t.sa;
-            four(Q, c0, R[k], t.sr);
-        }
+        for (int e = 0; e < 16; ++e) R[e] *= ex / t.sa;
+        four(Q, R, t.sr);
     }
     __syncthreads();
     if (rows) {
@@ -560,38 +517,33 @@ __global__ __launch_bounds__(512, 2) void k_chain_step(const uint16_t *__restric
             }
             E[e] = z;
         }
-        four(Ez, jb * 32, E, t.sz);
+        four(Ez, E, t.sz);
     }
     __syncthreads();
+    if (!columns) return;
     const float f = t.a + t.b * dd[q] + t.c * zz[q];
     const int i = i0 + q;
+    const f32x16_t W = chain_product(Pc, Ez, D.rp, lane);
 #pragma unroll
-    for (int k = 0; k < CB; ++k) {
-        const int c0 = (wave + 8 * k) * 32;
-        if (c0 >= D.sp) continue;
-        const f32x16_t W = chain_product(columns(k), Ez, D.rp, lane);
-        if (CB > 1) fetch_x(c0);
+    for (int g = 0; g < 4; ++g) {
+        const int c = c0 + 8 * g + 4 * h;
+        float v[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int c = c0 + 8 * g + 4 * h;
-            float v[4];
+        for (int e = 0; e < 4; ++e) {
+            const float x = (ElF16::wide(xh[g].v[e]) + ElF16::wide(xl[g].v[e])) * ex;
+            v[e] = (f * x + t.b * R[4 * g + e] + t.c * (W[4 * g + e] * (ex / t.sz))) * t.sx1;
+        }
+        if (LAST) {
+            if (i < D.r) {
+                uint16_t *o = out + blockIdx.y * so;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = (ElF16::wide(xh[g].v[e]) + ElF16::wide(xl[g].v[e])) * ex;
-                v[e] = (f * x + t.b * R[k][4 * g + e] + t.c * (W[4 * g + e] * (ex / t.sz))) * t.sx1;
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < D.s) o[tall ? (c + e) * ldo + i : i * ldo + c + e] = ElBF16::round(v[e]);
             }
-            if (LAST) {
-                if (i < D.r) {
-                    uint16_t *o = out + blockIdx.y * so;
+        } else {
+            put_x<ElF16>(hi1 + base, lo1 + base, i0 * D.sp + place(g), v);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < D.s) o[tall ? (c + e) * ldo + i : i * ldo + c + e] = ElBF16::round(v[e]);
-                }
-            } else {
-                put_x<ElF16>(hi1 + base, lo1 + base, i0 * D.sp + place(c0, g), v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tr1[base + chain_at(c + e, i, D.rp)] = f16_bits(v[e]);
-            }
+            for (int e = 0; e < 4; ++e) tr1[base + chain_at(c + e, i, D.rp)] = f16_bits(v[e]);
         }
     }
 }
@@ -696,7 +648,6 @@ hipError_t chain_run(hipStream_t stream, const void *G, int64_t batch, int64_t m
     hipLaunchKernelGGL(k_chain_load, grid, dim3(512), 0, stream, (const uint16_t *)G, (int)m, (int)n, ldg, sg, vec, D, eps,
                        (float)sx, at(p.hi[0]), at(p.lo[0]), at(p.tr[0]));
     SPEC_LAUNCH_CHECK();
-    const int cb = (int)cdiv_h(D.sp, 256);
     for (int k = 0; k < steps; ++k) {
         const double *c = co + 3 * k;
         const double na = top * top, next = 1.02 * step_bound(c, top);
@@ -705,16 +656,9 @@ hipError_t chain_run(hipStream_t stream, const void *G, int64_t batch, int64_t m
                           (float)scale16(na, 16384.0), (float)scale16(2.0 * na * top, 16384.0),
                           (float)scale16(na * na, 16384.0)};
         const int a = k & 1, b = a ^ 1;
-#define CHAIN_STEP(CB, LAST)                                                                                           \
-    hipLaunchKernelGGL((k_chain_step<CB, LAST>), grid, dim3(512), 0, stream, at(p.hi[a]), at(p.lo[a]), at(p.tr[a]), D, t, \
-                       at(p.hi[b]), at(p.lo[b]), at(p.tr[b]), (uint16_t *)O, ldo, so, m > n)
-        if (cb == 1 && last) CHAIN_STEP(1, true);
-        else if (cb == 1) CHAIN_STEP(1, false);
-        else if (cb == 2 && last) CHAIN_STEP(2, true);
-        else if (cb == 2) CHAIN_STEP(2, false);
-        else if (last) CHAIN_STEP(4, true);
-        else CHAIN_STEP(4, false);
-#undef CHAIN_STEP
+        const auto step = last ? k_chain_step<true> : k_chain_step<false>;
+        hipLaunchKernelGGL(step, grid, dim3(512), 0, stream, at(p.hi[a]), at(p.lo[a]), at(p.tr[a]), D, t, at(p.hi[b]),
+                           at(p.lo[b]), at(p.tr[b]), (uint16_t *)O, ldo, so, m > n);
         SPEC_LAUNCH_CHECK();
         top = next;
         sx = t.sx1;
