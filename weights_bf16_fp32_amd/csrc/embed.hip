@@ -28,6 +28,7 @@
 //   k_eg_sum     sums over sorted positions; beside them, zeros in the other rows
 //   k_eg_join    sums of rows that cross shares
 #include <algorithm>
+#include <limits.h>
 
 #include "internal.h"
 #include "mm.h"
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(256) void k_sort_move(const int *__restrict__ keys,
 constexpr int ONE_MAX = 16384;  // positions
 constexpr int ONE_BITS = 9;     // of the key per pass
 
-struct OneLds {
+struct __attribute__((aligned(16))) OneLds {
     int cnt[16][1 << ONE_BITS];
     int buf[ONE_MAX];
     int wsum[8];
@@ -283,10 +284,29 @@ SPEC_DEVICE void sort_rounds(OneLds &s, const void *ids, int is64, int64_t V, in
     }
 }
 
+// Up to 256 positions: a thread's place is the number of keys before its own.
+SPEC_DEVICE void sort_few(OneLds &s, const void *ids, int is64, int64_t V, int n, int *okeys, int *oidx)
+{
+    const int tid = threadIdx.x;
+    const int key = tid < n ? first_key(ids, is64, tid, V) : INT_MAX;
+    if (tid < 256) s.buf[tid] = key;
+    __syncthreads();
+    if (tid >= n) return;
+    int at = 0;
+    for (int j = 0; j < n; j += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(&s.buf[j]);
+        at += (o.x < key || (o.x == key && j < tid)) + (o.y < key || (o.y == key && j + 1 < tid)) +
+              (o.z < key || (o.z == key && j + 2 < tid)) + (o.w < key || (o.w == key && j + 3 < tid));
+    }
+    okeys[at] = key;
+    oidx[at] = tid;
+}
+
 // (the rounds are a constant, so that the arrays are registers)
 SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n, int passes, int *okeys, int *oidx)
 {
-    if (n <= 2048) sort_rounds<2>(s, ids, is64, V, n, passes, okeys, oidx);
+    if (n <= 256) sort_few(s, ids, is64, V, n, okeys, oidx);
+    else if (n <= 2048) sort_rounds<2>(s, ids, is64, V, n, passes, okeys, oidx);
     else if (n <= 4096) sort_rounds<4>(s, ids, is64, V, n, passes, okeys, oidx);
     else if (n <= 8192) sort_rounds<8>(s, ids, is64, V, n, passes, okeys, oidx);
     else sort_rounds<ONE_MAX / 1024>(s, ids, is64, V, n, passes, okeys, oidx);
@@ -294,7 +314,9 @@ SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n
 
 // ------------------------------------------------------------------ sums
 
-constexpr int EG_SHARE = 32;  // sorted positions per workgroup
+// sorted positions per workgroup: few where there are few, so that they fill the
+// chip; more leave fewer rows to be joined
+inline int eg_share(int64_t n) { return n <= 8192 ? 8 : 32; }
 constexpr int EG_AHEAD = 8;   // rows in flight per thread
 
 // Workgroup 0 sorts (sort != 0); the others write zeros over dE's rows below
@@ -357,7 +379,7 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
                                                 const int *__restrict__ keys, const int *__restrict__ idx, int64_t n,
                                                 int64_t V, float scale, int add, typename O::st *__restrict__ dE,
                                                 int64_t ldd, float *__restrict__ head, float *__restrict__ tail,
-                                                int64_t sums, int cols, int64_t row0)
+                                                int64_t sums, int cols, int64_t row0, int len)
 {
     if (blockIdx.x >= sums) {
         eg_gaps<O, VEC, LINES>(keys, n, V, row0 + ((int64_t)blockIdx.x - sums) * 64, dE, d, ldd);
@@ -365,7 +387,7 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
     }
     const int64_t share = blockIdx.x / cols;
     using P = Pack<typename E::st, VEC>;
-    const int64_t b = share * EG_SHARE, e = min<int64_t>(n, b + EG_SHARE);
+    const int64_t b = share * len, e = min<int64_t>(n, b + len);
     const int64_t c = VEC * ((int64_t)(blockIdx.x % cols) * 256 + threadIdx.x);
     if (c >= d || keys[b] >= V) return;
     float s[VEC];
@@ -421,19 +443,19 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
 template <typename O, int VEC>
 __global__ __launch_bounds__(256) void k_eg_join(int64_t d, const int *__restrict__ keys, int64_t n, int64_t V,
                                                  float scale, int add, typename O::st *__restrict__ dE, int64_t ldd,
-                                                 const float *__restrict__ head, const float *__restrict__ tail)
+                                                 const float *__restrict__ head, const float *__restrict__ tail, int len)
 {
-    const int64_t b = (int64_t)blockIdx.x * EG_SHARE, e = b + EG_SHARE;
+    const int64_t b = (int64_t)blockIdx.x * len, e = b + len;
     const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
     if (c >= d || e >= n) return;
     const int key = keys[e - 1];
     if (key >= V || keys[e] != key) return;
     if (keys[b] == key && b > 0 && keys[b - 1] == key) return;  // began earlier
     // the shares it goes through: those whose first position still has its key
-    int64_t lo = blockIdx.x + 1, hi = (n - 1) / EG_SHARE;
+    int64_t lo = blockIdx.x + 1, hi = (n - 1) / len;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
-        if (keys[mid * EG_SHARE] == key)
+        if (keys[mid * len] == key)
             lo = mid;
         else
             hi = mid - 1;
@@ -475,8 +497,8 @@ EgPlan eg_plan(int64_t n, int64_t V, int64_t d)
         p.idx[i] = take(4 * nn);
     }
     p.hist = take((int64_t)4 * p.nshare << p.bits);
-    p.head = take(4 * cdiv_h(nn, EG_SHARE) * d);
-    p.tail = take(4 * cdiv_h(nn, EG_SHARE) * d);
+    p.head = take(4 * cdiv_h(nn, eg_share(n)) * d);
+    p.tail = take(4 * cdiv_h(nn, eg_share(n)) * d);
     p.total = o;
     return p;
 }
@@ -516,15 +538,16 @@ hipError_t eg_launch(hipStream_t stream, const void *dY, int64_t n, int64_t V, i
         SPEC_LAUNCH_CHECK();
     }
     const int *keys = okeys, *idx = oidx;
-    const int64_t shares = cdiv_h(n, EG_SHARE), cols = cdiv_h(d, 256 * VEC);
+    const int len = eg_share(n);
+    const int64_t shares = cdiv_h(n, len), cols = cdiv_h(d, 256 * VEC);
     const int64_t gaps = add ? 0 : cdiv_h(V - early, 64);
     float *head = (float *)(ws + p.head), *tail = (float *)(ws + p.tail);
     hipLaunchKernelGGL((k_eg_sum<E, O, VEC, LINES>), dim3((unsigned)(shares * cols + gaps)), dim3(256), 0, stream,
                        (const typename E::st *)dY, d, ldy, keys, idx, n, V, scale, add, out, ldd, head, tail, shares * cols,
-                       (int)cols, early);
+                       (int)cols, early, len);
     SPEC_LAUNCH_CHECK();
     hipLaunchKernelGGL((k_eg_join<O, VEC>), dim3((unsigned)shares, (unsigned)cols), dim3(256), 0, stream, d, keys, n, V,
-                       scale, add, out, ldd, head, tail);
+                       scale, add, out, ldd, head, tail, len);
     return hipGetLastError();
 }
 
