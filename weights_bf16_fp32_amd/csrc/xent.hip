@@ -645,7 +645,7 @@ hipError_t xent_fwd(hipStream_t stream, const void *H, int64_t ldh, const void *
     const XentPlan pl = xent_plan(T, V, d, sizeof(st) == 2 ? SPEC_BF16 : SPEC_F32, false);
     hipError_t e = pack<E>(stream, pl, H, ldh, target, is64, nullptr, nullptr, T, V, d, ws);
     if (e != hipSuccess) return e;
-    const bool direct = direct_w<E>(W, ldw, d), big = big_tiles<E>(T, V);
+    const bool direct = direct_w<E>(W, ldw, d), big = T > FEW_TOKENS && big_tiles<E>(T, V);
     const int64_t piece = direct ? V : pl.piece, ldpart = cdiv_h(V, big ? 256 : 128);
     for (int64_t v = 0; v < V; v += piece) {
         const int64_t vn = std::min(piece, V - v);
