@@ -63,24 +63,24 @@ SPEC_DEVICE void put_zero(S *p)
     }
 }
 
-// a wave per row
+// a wave per row, and on by the grid's rows where one launch does not hold them all
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_embed(const typename E::st *__restrict__ tab, int64_t V, int64_t d, int64_t lde,
                                                const void *__restrict__ ids, int is64, int64_t n, float scale,
                                                typename E::st *__restrict__ Y, int64_t ldy)
 {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= n) return;
-    const int64_t v = load_id(ids, is64, i);
-    const bool ok = v >= 0 && v < V;
-    const typename E::st *src = tab + (ok ? v : 0) * lde;
-    typename E::st *dst = Y + i * ldy;
-    for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64) {
-        Pack<typename E::st, VEC> x{};
-        if (ok) x = *reinterpret_cast<const Pack<typename E::st, VEC> *>(src + c);
+    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += 4 * (int64_t)gridDim.x) {
+        const int64_t v = load_id(ids, is64, i);
+        const bool ok = v >= 0 && v < V;
+        const typename E::st *src = tab + (ok ? v : 0) * lde;
+        typename E::st *dst = Y + i * ldy;
+        for (int64_t c = VEC * (threadIdx.x & 63); c < d; c += VEC * 64) {
+            Pack<typename E::st, VEC> x{};
+            if (ok) x = *reinterpret_cast<const Pack<typename E::st, VEC> *>(src + c);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x.v[e] = ok ? E::round(scale * E::wide(x.v[e])) : (typename E::st)0;
-        *reinterpret_cast<Pack<typename E::st, VEC> *>(dst + c) = x;
+            for (int e = 0; e < VEC; ++e) x.v[e] = ok ? E::round(scale * E::wide(x.v[e])) : (typename E::st)0;
+            *reinterpret_cast<Pack<typename E::st, VEC> *>(dst + c) = x;
+        }
     }
 }
 
@@ -568,7 +568,7 @@ hipError_t embed_run(hipStream_t stream, const void *tab, int64_t V, int64_t d, 
 {
     using st = typename E::st;
     constexpr int VEC = 16 / sizeof(st);
-    const dim3 grid((unsigned)cdiv_h(n, 4));
+    const dim3 grid((unsigned)std::min(cdiv_h(n, 4), LAUNCH_THREADS / 256));
     const bool vec = (uintptr_t)tab % 16 == 0 && (uintptr_t)Y % 16 == 0 && d % VEC == 0 && lde % VEC == 0 && ldy % VEC == 0;
     if (vec)
         hipLaunchKernelGGL((k_embed<E, VEC>), grid, dim3(256), 0, stream, (const st *)tab, V, d, lde, ids, is64, n, scale,

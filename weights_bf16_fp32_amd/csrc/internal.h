@@ -8,6 +8,10 @@
 
 #include "../../include/spec.h"
 
+// Threads per launch at most.  A grid holds fewer than 2^32 per dimension; one of
+// more is launched modulo 2^32, without an error, and leaves the rest undone.
+constexpr int64_t LAUNCH_THREADS = (int64_t)1 << 31;
+
 hipError_t launch_syrk(hipStream_t stream, const void *X, int xt, int64_t n, int64_t d, int64_t ldx, void *C, int ct,
                        int64_t ldc, double alpha, double beta);
 
