@@ -25,3 +25,30 @@ def test_embed_of_many_positions(spec):
     Y = spec.embed(E, ids)
     want = torch.cat([E[:, 0], torch.zeros(1, dtype=torch.bfloat16, device="cuda")])[ids.long()]
     assert torch.equal(Y[:, 0], want)
+
+
+def test_embed_grad_of_many_rows(spec):
+    """More rows of zeros than one launch writes."""
+    import torch
+    V = (1 << 30) + (1 << 25)
+    print_case("embed_grad_many_rows", n=3, V=V, d=1)
+    dE = torch.full((V, 1), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([V - 1, 5, V - 1], device="cuda")
+    spec.embed_grad(torch.tensor([[1.0], [2.0], [4.0]], device="cuda").bfloat16(), ids, V, dE=dE)
+    assert dE[V - 1].item() == 5.0 and dE[5].item() == 2.0 and torch.count_nonzero(dE).item() == 2
+
+
+def test_embed_grad_of_many_positions(spec):
+    """More shares of positions than one launch adds or joins; integers, so the sums are exact."""
+    import torch
+    V = 1024
+    k = (1 << 19) + 8  # positions of every row
+    n = k * V
+    print_case("embed_grad_many_positions", n=n, V=V, d=1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    dY = torch.randint(-1, 2, (k, V), generator=g, device="cuda", dtype=torch.int8)
+    want = dY.sum(0, dtype=torch.int64)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % V
+    dE = spec.embed_grad(dY.view(n, 1).bfloat16(), ids, V, dE=torch.full((V, 1), float("nan"), device="cuda"))
+    assert torch.equal(dE[:, 0].long(), want)

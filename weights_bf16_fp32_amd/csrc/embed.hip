@@ -370,8 +370,8 @@ SPEC_DEVICE void eg_gaps(const int *__restrict__ keys, int64_t n, int64_t V, int
                 put_zero<typename O::st, VEC, LINES>(dE + (v0 + r) * ldd + c);
 }
 
-// The first shares x cols workgroups (cols: column blocks of 256 VEC) add; the
-// others write the zero rows from row0 on.  head[share] / tail[share]: the sum
+// The first `sums` workgroups add, cols (column blocks of 256 VEC) of them per
+// share from share0 on; the others write the zero rows from row0 on.  head[share] / tail[share]: the sum
 // of the share's first / last row where it began before / goes on after.
 // Positions are taken EG_AHEAD at a time, their rows requested together.
 template <typename E, typename O, int VEC, bool LINES>
@@ -379,13 +379,13 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
                                                 const int *__restrict__ keys, const int *__restrict__ idx, int64_t n,
                                                 int64_t V, float scale, int add, typename O::st *__restrict__ dE,
                                                 int64_t ldd, float *__restrict__ head, float *__restrict__ tail,
-                                                int64_t sums, int cols, int64_t row0, int len)
+                                                int64_t share0, int64_t sums, int cols, int64_t row0, int len)
 {
     if (blockIdx.x >= sums) {
         eg_gaps<O, VEC, LINES>(keys, n, V, row0 + ((int64_t)blockIdx.x - sums) * 64, dE, d, ldd);
         return;
     }
-    const int64_t share = blockIdx.x / cols;
+    const int64_t share = share0 + blockIdx.x / cols;
     using P = Pack<typename E::st, VEC>;
     const int64_t b = share * len, e = min<int64_t>(n, b + len);
     const int64_t c = VEC * ((int64_t)(blockIdx.x % cols) * 256 + threadIdx.x);
@@ -443,16 +443,17 @@ __global__ __launch_bounds__(256) void k_eg_sum(const typename E::st *__restrict
 template <typename O, int VEC>
 __global__ __launch_bounds__(256) void k_eg_join(int64_t d, const int *__restrict__ keys, int64_t n, int64_t V,
                                                  float scale, int add, typename O::st *__restrict__ dE, int64_t ldd,
-                                                 const float *__restrict__ head, const float *__restrict__ tail, int len)
+                                                 const float *__restrict__ head, const float *__restrict__ tail,
+                                                 int64_t share0, int len)
 {
-    const int64_t b = (int64_t)blockIdx.x * len, e = b + len;
+    const int64_t share = share0 + blockIdx.x, b = share * len, e = b + len;
     const int64_t c = VEC * ((int64_t)blockIdx.y * 256 + threadIdx.x);
     if (c >= d || e >= n) return;
     const int key = keys[e - 1];
     if (key >= V || keys[e] != key) return;
     if (keys[b] == key && b > 0 && keys[b - 1] == key) return;  // began earlier
     // the shares it goes through: those whose first position still has its key
-    int64_t lo = blockIdx.x + 1, hi = (n - 1) / len;
+    int64_t lo = share + 1, hi = (n - 1) / len;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
         if (keys[mid * len] == key)
@@ -462,9 +463,9 @@ __global__ __launch_bounds__(256) void k_eg_join(int64_t d, const int *__restric
     }
     float s[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) s[k] = tail[(int64_t)blockIdx.x * d + c + k];
+    for (int k = 0; k < VEC; ++k) s[k] = tail[share * d + c + k];
 #pragma unroll 8
-    for (int64_t f = blockIdx.x + 1; f <= lo; ++f)
+    for (int64_t f = share + 1; f <= lo; ++f)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) s[k] += head[f * d + c + k];
     eg_put<O, VEC>(dE + key * ldd, c, s, scale, add);
@@ -542,13 +543,24 @@ hipError_t eg_launch(hipStream_t stream, const void *dY, int64_t n, int64_t V, i
     const int64_t shares = cdiv_h(n, len), cols = cdiv_h(d, 256 * VEC);
     const int64_t gaps = add ? 0 : cdiv_h(V - early, 64);
     float *head = (float *)(ws + p.head), *tail = (float *)(ws + p.tail);
-    hipLaunchKernelGGL((k_eg_sum<E, O, VEC, LINES>), dim3((unsigned)(shares * cols + gaps)), dim3(256), 0, stream,
-                       (const typename E::st *)dY, d, ldy, keys, idx, n, V, scale, add, out, ldd, head, tail, shares * cols,
-                       (int)cols, early, len);
-    SPEC_LAUNCH_CHECK();
-    hipLaunchKernelGGL((k_eg_join<O, VEC>), dim3((unsigned)shares, (unsigned)cols), dim3(256), 0, stream, d, keys, n, V,
-                       scale, add, out, ldd, head, tail, len);
-    return hipGetLastError();
+    // (one launch each unless there are more shares or zero rows than it holds)
+    constexpr int64_t most = LAUNCH_THREADS / 256;
+    for (int64_t share = 0, gap = 0; share < shares || gap < gaps;) {
+        const int64_t ns = std::min(shares - share, most / cols), ng = std::min(gaps - gap, most - ns * cols);
+        hipLaunchKernelGGL((k_eg_sum<E, O, VEC, LINES>), dim3((unsigned)(ns * cols + ng)), dim3(256), 0, stream,
+                           (const typename E::st *)dY, d, ldy, keys, idx, n, V, scale, add, out, ldd, head, tail, share,
+                           ns * cols, (int)cols, early + 64 * gap, len);
+        SPEC_LAUNCH_CHECK();
+        share += ns;
+        gap += ng;
+    }
+    for (int64_t share = 0; share < shares; share += most) {
+        const int64_t ns = std::min(shares - share, most);
+        hipLaunchKernelGGL((k_eg_join<O, VEC>), dim3((unsigned)ns, (unsigned)cols), dim3(256), 0, stream, d, keys, n, V,
+                           scale, add, out, ldd, head, tail, share, len);
+        SPEC_LAUNCH_CHECK();
+    }
+    return hipSuccess;
 }
 
 template <typename E, typename O, int VEC>
