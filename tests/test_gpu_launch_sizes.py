@@ -52,3 +52,25 @@ def test_embed_grad_of_many_positions(spec):
     ids = torch.arange(n, dtype=torch.int32, device="cuda") % V
     dE = spec.embed_grad(dY.view(n, 1).bfloat16(), ids, V, dE=torch.full((V, 1), float("nan"), device="cuda"))
     assert torch.equal(dE[:, 0].long(), want)
+
+
+def test_linear_xent_of_many_tiles(spec):
+    """2^23 and more tiles of 256 x 256 logits; the rows repeat, so a few stand for all."""
+    import torch
+    T, V, d, k = 1 << 16, (1 << 23) + 300, 8, 16
+    print_case("linear_xent_many_tiles", T=T, V=V, d=d)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    W = torch.randn(V, d, generator=g, device="cuda").bfloat16()
+    few = torch.randn(k, d, generator=g, device="cuda").bfloat16()
+    tgt = torch.randint(0, V, (k,), generator=g, device="cuda")
+    tgt[0], tgt[1], tgt[2] = V - 1, 0, -1
+    loss, lse = spec.linear_xent(few.repeat(T // k, 1), W, tgt.repeat(T // k))
+    z = few.double() @ W.double().t()
+    want = torch.where(tgt >= 0, torch.logsumexp(z, 1), 0.0)
+    want_loss = torch.where(tgt >= 0, want - z.gather(1, tgt.clamp(min=0)[:, None])[:, 0], 0.0)
+    # in units of 2^-24: (160 + V / 8192) for the sums, 16 for exp and log, 4 lse for its rounding, and (d + 3)
+    # |h| |w| < 1000 for a logit, in the lse and in the loss; together below 2^12
+    tol = 2.0 ** -12
+    assert ((lse.view(-1, k).double() - want).abs().max() <= tol) and ((loss.view(-1, k).double() - want_loss).abs().max() <= tol)
+    assert bool((lse.view(-1, k)[:, 2] == 0).all()) and bool((loss.view(-1, k)[:, 2] == 0).all())

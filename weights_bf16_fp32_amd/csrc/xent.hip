@@ -575,12 +575,19 @@ template <typename E, typename C>
 hipError_t fwd_piece(hipStream_t stream, const XentPlan &pl, const typename E::st *W, int64_t ldw, int64_t vn, int64_t v,
                      int64_t T, float scale, int64_t ldpart, char *ws)
 {
-    const int np = (int)cdiv_h(vn, C::BP), nq = (int)cdiv_h(T, C::BQ);
-    hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W, ldw,
-                       vn, v, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk, (const int *)(ws + pl.nvalid), np,
-                       scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt), (float2 *)(ws + pl.part), ldpart,
-                       (int)(v / C::BP));
-    return hipGetLastError();
+    // (one launch unless it would have more threads than a launch holds)
+    const int nq = (int)cdiv_h(T, C::BQ);
+    const int64_t most = LAUNCH_THREADS / C::NT / nq * C::BP;
+    for (int64_t v0 = 0; v0 < vn; v0 += most) {
+        const int64_t n = std::min(most, vn - v0);
+        const int np = (int)cdiv_h(n, C::BP);
+        hipLaunchKernelGGL((k_xent_fwd<E, C>), dim3((unsigned)((int64_t)np * nq)), dim3(C::NT), 0, stream, W + v0 * ldw,
+                           ldw, n, v + v0, (const typename E::st *)(ws + pl.hp), pl.dp, pl.dk,
+                           (const int *)(ws + pl.nvalid), np, scale, (const int *)(ws + pl.ptgt), (float *)(ws + pl.ztgt),
+                           (float2 *)(ws + pl.part), ldpart, (int)((v + v0) / C::BP));
+        SPEC_LAUNCH_CHECK();
+    }
+    return hipSuccess;
 }
 
 template <typename E, typename C>
