@@ -74,3 +74,15 @@ def test_linear_xent_of_many_tiles(spec):
     tol = 2.0 ** -12
     assert ((lse.view(-1, k).double() - want).abs().max() <= tol) and ((loss.view(-1, k).double() - want_loss).abs().max() <= tol)
     assert bool((lse.view(-1, k)[:, 2] == 0).all()) and bool((loss.view(-1, k)[:, 2] == 0).all())
+
+
+def test_linear_xent_grad_without_rows(spec):
+    """No row at all: dW is scaled, however many rows it has."""
+    import torch
+    V = (1 << 24) + 3
+    print_case("linear_xent_grad_without_rows", V=V, d=1)
+    W = torch.zeros(V, 1, dtype=torch.bfloat16, device="cuda")
+    dW = (torch.arange(V, device="cuda") % 100).bfloat16()[:, None]
+    none = torch.zeros(0, device="cuda")
+    got = spec.linear_xent_grad(W[:0], W, none.long(), none, none, beta=2.0, dW=dW.clone())[1]
+    assert torch.equal(got, dW * 2)

@@ -704,10 +704,13 @@ hipError_t xent_grad(hipStream_t stream, const void *H, int64_t ldh, const void 
 
 // dW <- beta dW where no token has a target to add
 template <typename E>
-__global__ __launch_bounds__(256) void k_xent_scale(typename E::st *__restrict__ dW, int64_t lddw, int64_t d, float beta)
+__global__ __launch_bounds__(256) void k_xent_scale(typename E::st *__restrict__ dW, int64_t lddw, int64_t V, int64_t d,
+                                                    float beta)
 {
-    typename E::st *r = dW + (int64_t)blockIdx.x * lddw;
-    for (int64_t c = threadIdx.x; c < d; c += 256) r[c] = E::round(beta != 0.f ? beta * E::wide(r[c]) : 0.f);
+    for (int64_t v = blockIdx.x; v < V; v += gridDim.x) {
+        typename E::st *r = dW + v * lddw;
+        for (int64_t c = threadIdx.x; c < d; c += 256) r[c] = E::round(beta != 0.f ? beta * E::wide(r[c]) : 0.f);
+    }
 }
 
 }  // namespace
@@ -737,10 +740,11 @@ hipError_t launch_linear_xent_grad(hipStream_t stream, const void *H, const void
                                    float beta, void *ws)
 {
     if (T == 0) {
+        const dim3 grid((unsigned)std::min(V, LAUNCH_THREADS / 256));
         if (t == SPEC_BF16)
-            hipLaunchKernelGGL(k_xent_scale<ElBF16>, dim3((unsigned)V), dim3(256), 0, stream, (uint16_t *)dW, lddw, d, beta);
+            hipLaunchKernelGGL(k_xent_scale<ElBF16>, grid, dim3(256), 0, stream, (uint16_t *)dW, lddw, V, d, beta);
         else
-            hipLaunchKernelGGL(k_xent_scale<ElF32>, dim3((unsigned)V), dim3(256), 0, stream, (float *)dW, lddw, d, beta);
+            hipLaunchKernelGGL(k_xent_scale<ElF32>, grid, dim3(256), 0, stream, (float *)dW, lddw, V, d, beta);
         return hipGetLastError();
     }
     return t == SPEC_BF16 ? xent_grad<ElBF16>(stream, H, ldh, W, ldw, target, is64, T, V, d, scale, lse, dloss, dH, lddh,
