@@ -195,3 +195,23 @@ def test_stream_and_graph(spec):
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, spec.orthogonalize(G)), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(65, 90), (300, 200)])
+def test_norms_at_the_ends_of_the_range(spec, dtype, m, n):
+    """1 / |G|_F need not be an f32: a zero G is zero with eps = 0 too, subnormal updates are not infinite, and a
+    power of two that no element overflows or underflows by changes no bit."""
+    import torch
+    print_case("orthogonalize_norms", m=m, n=n, dtype=dtype)
+    G = _update("flat", 1, m, n, dtype, 4)[0].clamp(-3.9, 3.9)
+    zero = torch.zeros_like(G)
+    for eps in (0.0, 1e-300, 1e-40):
+        assert not spec.orthogonalize(zero, eps=eps).any(), eps
+    O = spec.orthogonalize(G, eps=0.0)
+    three = spec.orthogonalize(torch.stack([G, zero, G]), eps=0.0)
+    assert torch.equal(three[0], O) and torch.equal(three[2], O) and not three[1].any()
+    assert torch.equal(spec.orthogonalize((G.double() * 2.0 ** 125).to(G.dtype), eps=0.0), O)
+    for f in (2.0 ** -120, 2.0 ** (-128 if dtype == "bf16" else -140)):
+        small = (G.double() * f).to(G.dtype)  # (what is left of its bits is the input)
+        assert _off(spec.orthogonalize(small, eps=0.0), _ref(small, [MUON] * 5, eps=0.0)) <= LIMIT[dtype], f
