@@ -93,6 +93,16 @@ def test_orthogonalize_validation(L):
         assert f(*_with(ok, **bad)) == EWORKSPACE, bad
 
 
+@pytest.mark.parametrize("c", [0.0, 1e-15, -1e-15, 1e-18, 1e-300, 1e-6, -1e-6])
+def test_orthogonalize_bound_with_a_small_quintic_term(L, c):
+    """40 s - 40 s^3 + c s^5 reaches 15.4 at s = 1 / sqrt(3) and is c at s = 1: past what f16 steps hold, whatever c;
+    2 s - 2 s^3 + c s^5 reaches 0.77 and is taken (up to the missing workspace)."""
+    for ab, status in ((40.0, EINVAL), (2.0, EWORKSPACE)):
+        co = (ctypes.c_double * 6)(ab, -ab, c, 3.0, -3.0, 1.0)
+        assert L.spec_orthogonalize(None, FAKE, spec.BF16, 1, 64, 32, 32, 2048, co, 2, 1e-7, 1.0, FAKE, 32, 2048, None,
+                                    0) == status
+
+
 def test_workspace_queries(L):
     import torch
     b = ctypes.c_size_t(0)

@@ -615,7 +615,8 @@ ChainPlan chain_plan(int64_t batch, int64_t m, int64_t n)
 }
 
 // largest |s (a + b s^2 + c s^4)| over 0 <= s <= top: at the end or at a root
-// of a + 3 b u + 5 c u^2, u = s^2
+// of a + 3 b u + 5 c u^2, u = s^2 (the larger root's numerator without a difference,
+// the other root from their product a / 5c: a small c does not cancel them)
 double step_bound(const double *co, double top)
 {
     const double a = co[0], b = co[1], c = co[2];
@@ -623,14 +624,11 @@ double step_bound(const double *co, double top)
     double best = f(top);
     double u[2];
     int nu = 0;
-    if (c != 0.0) {
-        const double q = 9.0 * b * b - 20.0 * a * c;
-        if (q >= 0.0) {
-            u[nu++] = (-3.0 * b + sqrt(q)) / (10.0 * c);
-            u[nu++] = (-3.0 * b - sqrt(q)) / (10.0 * c);
-        }
-    } else if (b != 0.0) {
-        u[nu++] = -a / (3.0 * b);
+    const double q = 9.0 * b * b - 20.0 * a * c;
+    if (q >= 0.0) {
+        const double w = -0.5 * (3.0 * b + copysign(sqrt(q), b));
+        if (c != 0.0) u[nu++] = w / (5.0 * c);
+        if (w != 0.0) u[nu++] = a / w;
     }
     for (int k = 0; k < nu; ++k)
         if (u[k] > 0.0 && u[k] < top * top) best = std::max(best, f(sqrt(u[k])));
