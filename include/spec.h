@@ -541,7 +541,8 @@ int spec_timing_read(int kernel, double *total_ms, int64_t *launches);
  * [0, V) is no token: padding, a masked prompt.  Its row of the lookup is zero,
  * its loss and lse are 0, and it adds to no gradient, whatever its rows of dY or
  * H hold (NaN included).  Results are the same in every run (no floating-point
- * atomics).
+ * atomics).  Factors (scale, beta, coefficients) are applied in f32 and have to be
+ * finite there, else SPEC_EINVAL; eps is used in f64.
  * ---------------------------------------------------------------------- */
 
 /* Embedding lookup:  Y[i] = scale * E[ids[i]]  (computed in f32, rounded once).
@@ -616,7 +617,7 @@ int spec_linear_xent_grad(void *stream, const void *H, const void *W, int t, int
  * (256-byte aligned).
  * Requires 1 <= m, n <= 65536 with min(m, n) <= 32768, 1 <= batch <= 65535, ldg, ldo >= n,
  * sg >= m*ldg and so >= m*ldo when batch > 1, 1 <= steps <= 32, eps >= 0,
- * finite coefficients and scale, and (SPEC_BF16) coefficients whose steps keep
+ * and (SPEC_BF16) coefficients whose steps keep
  * every s in [0, 1] below 11 and |b| s^2 + |c| s^4 below 2^14; else SPEC_EINVAL. */
 int spec_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int t, size_t *bytes);
 

@@ -93,6 +93,24 @@ def test_orthogonalize_validation(L):
         assert f(*_with(ok, **bad)) == EWORKSPACE, bad
 
 
+def test_factors_beyond_f32(L):
+    """Factors are applied in f32: 1e39 would make NaN of a zero there (and is no f32), 3e38 is one."""
+    three = ctypes.c_double * 3
+    for x, status in ((1e39, EINVAL), (-1e39, EINVAL), (1e308, EINVAL), (3e38, EWORKSPACE), (-3e38, EWORKSPACE)):
+        assert L.spec_embed(None, FAKE, spec.F32, 100, 64, 64, FAKE, spec.I64, 0, x, FAKE, 64) == (
+            EINVAL if status == EINVAL else 0)  # (no position: nothing is enqueued)
+        assert L.spec_embed_grad(None, FAKE, spec.F32, 10, 100, 64, 64, FAKE, spec.I64, x, 0.0, FAKE, spec.F32, 64, None,
+                                 0) == status
+        xent = dict(XENT, t=spec.F32, scale=x)
+        assert L.spec_linear_xent(*xent.values(), FAKE, FAKE, None, 0) == status
+        assert L.spec_linear_xent_grad(*xent.values(), FAKE, FAKE, 0.0, FAKE, 64, FAKE, 64, None, 0) == status
+        xent["scale"] = 1.0
+        assert L.spec_linear_xent_grad(*xent.values(), FAKE, FAKE, x, FAKE, 64, FAKE, 64, None, 0) == status
+        for co, scale in ((three(3.4445, -4.7750, 2.0315), x), (three(x, -4.7750, 2.0315), 1.0)):
+            assert L.spec_orthogonalize(None, FAKE, spec.F32, 1, 64, 32, 32, 2048, co, 1, 1e-7, scale, FAKE, 32, 2048,
+                                        None, 0) == status
+
+
 @pytest.mark.parametrize("c", [0.0, 1e-15, -1e-15, 1e-18, 1e-300, 1e-6, -1e-6])
 def test_orthogonalize_bound_with_a_small_quintic_term(L, c):
     """40 s - 40 s^3 + c s^5 reaches 15.4 at s = 1 / sqrt(3) and is c at s = 1: past what f16 steps hold, whatever c;

@@ -2,6 +2,7 @@
 // gfx950 kernels.  Every check runs on the host before anything is enqueued;
 // nothing here allocates device memory or synchronises.
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -44,6 +45,9 @@ int check_descriptors(const void *w, int wt, int64_t batch, int64_t r, int64_t l
     if (!aligned(w, elt_size(wt)) || !aligned(out, 8)) return SPEC_EINVAL;
     return SPEC_OK;
 }
+
+// whether a factor that the kernels apply in f32 is finite there
+inline bool finite32(double x) { return fabs(x) <= FLT_MAX; }
 
 // sizes shared by the vocabulary operators, and the type of a token id array
 int check_rows(int64_t n, int64_t V, int64_t d)
@@ -385,7 +389,7 @@ int spec_embed(void *stream, const void *E, int t, int64_t V, int64_t d, int64_t
     if (st != SPEC_OK) return st;
     st = check_ids(ids, idt, n);
     if (st != SPEC_OK) return st;
-    if (E == nullptr || (Y == nullptr && n > 0) || lde < d || ldy < d || !isfinite(scale)) return SPEC_EINVAL;
+    if (E == nullptr || (Y == nullptr && n > 0) || lde < d || ldy < d || !finite32(scale)) return SPEC_EINVAL;
     if (!aligned(E, elt_size(t)) || !aligned(Y, elt_size(t))) return SPEC_EINVAL;
     return from_hip(launch_embed((hipStream_t)stream, E, t, V, d, lde, ids, idt == SPEC_I64, n, (float)scale, Y, ldy));
 }
@@ -408,7 +412,7 @@ int spec_embed_grad(void *stream, const void *dY, int yt, int64_t n, int64_t V, 
     if (st != SPEC_OK) return st;
     st = check_ids(ids, idt, n);
     if (st != SPEC_OK) return st;
-    if (dE == nullptr || (dY == nullptr && n > 0) || ldy < d || ldd < d || !isfinite(scale)) return SPEC_EINVAL;
+    if (dE == nullptr || (dY == nullptr && n > 0) || ldy < d || ldd < d || !finite32(scale)) return SPEC_EINVAL;
     if (!aligned(dY, elt_size(yt)) || !aligned(dE, elt_size(et))) return SPEC_EINVAL;
     if (beta != 0.0 && beta != 1.0) return isfinite(beta) ? SPEC_EUNSUPPORTED : SPEC_EINVAL;
     if (ws == nullptr || ws_bytes < embed_grad_workspace_bytes(n, V, d)) return SPEC_EWORKSPACE;
@@ -435,7 +439,7 @@ static int check_xent(const void *H, const void *W, int t, int64_t T, int64_t V,
     st = check_ids(target, tt, T);
     if (st != SPEC_OK) return st;
     const int64_t most = ((int64_t)1 << 20) + 64;
-    if (W == nullptr || (H == nullptr && T > 0) || ldh < d || ldw < d || ldh > most || ldw > most || !isfinite(scale))
+    if (W == nullptr || (H == nullptr && T > 0) || ldh < d || ldw < d || ldh > most || ldw > most || !finite32(scale))
         return SPEC_EINVAL;
     if (!aligned(H, elt_size(t)) || !aligned(W, elt_size(t))) return SPEC_EINVAL;
     return SPEC_OK;
@@ -472,7 +476,7 @@ int spec_linear_xent_grad(void *stream, const void *H, const void *W, int t, int
     const int st = check_xent(H, W, t, T, V, d, ldh, ldw, target, tt, scale);
     if (st != SPEC_OK) return st;
     if (T > 0 && (lse == nullptr || dloss == nullptr || dH == nullptr)) return SPEC_EINVAL;
-    if (dW == nullptr || lddh < d || lddw < d || !isfinite(beta)) return SPEC_EINVAL;
+    if (dW == nullptr || lddh < d || lddw < d || !finite32(beta)) return SPEC_EINVAL;
     if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dH, elt_size(t)) || !aligned(dW, elt_size(t)))
         return SPEC_EINVAL;
     if (ws == nullptr || ws_bytes < linear_xent_grad_workspace_bytes(T, V, d, t)) return SPEC_EWORKSPACE;
@@ -498,9 +502,9 @@ int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_
     if (st != SPEC_OK) return st;
     if (G == nullptr || O == nullptr || coeffs == nullptr || ldg < n || ldo < n) return SPEC_EINVAL;
     if (batch > 1 && (sg < m * ldg || so < m * ldo)) return SPEC_EINVAL;
-    if (steps < 1 || steps > 32 || !(eps >= 0.0) || !isfinite(eps) || !isfinite(scale)) return SPEC_EINVAL;
+    if (steps < 1 || steps > 32 || !(eps >= 0.0) || !isfinite(eps) || !finite32(scale)) return SPEC_EINVAL;
     for (int i = 0; i < 3 * steps; ++i)
-        if (!isfinite(coeffs[i])) return SPEC_EINVAL;
+        if (!finite32(coeffs[i])) return SPEC_EINVAL;
     if (t == SPEC_BF16 && !orthogonalize_bounded(coeffs, steps)) return SPEC_EINVAL;
     if (!aligned(G, elt_size(t)) || !aligned(O, elt_size(t))) return SPEC_EINVAL;
     if (ws == nullptr || ws_bytes < orthogonalize_workspace_bytes(batch, m, n, t)) return SPEC_EWORKSPACE;
