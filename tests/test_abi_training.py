@@ -111,6 +111,14 @@ def test_factors_beyond_f32(L):
                                         None, 0) == status
 
 
+def test_orthogonalize_strides_past_64_bits(L):
+    """64 rows of 2^62 elements do not fit a stride of 0, though 64 * 2^62 is 0 in 64 bits."""
+    co = (ctypes.c_double * 3)(3.4445, -4.7750, 2.0315)
+    for ldg, sg, ldo, so in ((1 << 62, 0, 32, 2048), (32, 2048, 1 << 62, 0), (32, -2048, 32, 2048)):
+        assert L.spec_orthogonalize(None, FAKE, spec.BF16, 2, 64, 32, ldg, sg, co, 1, 1e-7, 1.0, FAKE, ldo, so, None,
+                                    0) == EINVAL
+
+
 @pytest.mark.parametrize("c", [0.0, 1e-15, -1e-15, 1e-18, 1e-300, 1e-6, -1e-6])
 def test_orthogonalize_bound_with_a_small_quintic_term(L, c):
     """40 s - 40 s^3 + c s^5 reaches 15.4 at s = 1 / sqrt(3) and is c at s = 1: past what f16 steps hold, whatever c;

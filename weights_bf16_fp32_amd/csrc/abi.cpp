@@ -501,7 +501,7 @@ int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_
     const int st = check_ortho_sizes(batch, m, n, t);
     if (st != SPEC_OK) return st;
     if (G == nullptr || O == nullptr || coeffs == nullptr || ldg < n || ldo < n) return SPEC_EINVAL;
-    if (batch > 1 && (sg < m * ldg || so < m * ldo)) return SPEC_EINVAL;
+    if (batch > 1 && (sg / m < ldg || so / m < ldo)) return SPEC_EINVAL;  // (m * ldg may not be an int64)
     if (steps < 1 || steps > 32 || !(eps >= 0.0) || !isfinite(eps) || !finite32(scale)) return SPEC_EINVAL;
     for (int i = 0; i < 3 * steps; ++i)
         if (!finite32(coeffs[i])) return SPEC_EINVAL;
