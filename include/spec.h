@@ -574,7 +574,8 @@ int spec_embed_grad(void *stream, const void *dY, int yt, int64_t n, int64_t V, 
  * accumulation) or SPEC_F32 (MFMA f32); target: ids [T]; loss, lse: f32 [T].
  * A row whose logits hold NaN or +inf has loss and lse NaN.
  * ws: device workspace of spec_linear_xent_workspace(T, V, d, t) bytes (256-byte
- * aligned): packed H, one (max, sum) pair per row and 128 logits.
+ * aligned): packed H, one (max, sum) pair per row and 128 logits, and room for a
+ * piece of W (up to 256 MB, or 2048 rows), used where W's rows are not aligned.
  * Requires 1 <= V < 2^31 - 1, 1 <= d <= 2^20, 0 <= T <= 2^22, ldh, ldw >= d and
  * <= 2^20 + 64 (else SPEC_EINVAL), and fewer than 2^30 tiles of 128 x 128 logits
  * (else SPEC_EUNSUPPORTED).  16-byte aligned rows of W are read in place,
@@ -591,7 +592,10 @@ int spec_linear_xent(void *stream, const void *H, const void *W, int t, int64_t 
  *   dH = G W,  dW = beta dW + G^T H
  * lse: as spec_linear_xent returned it for the same H, W, target and scale.
  * The vocabulary is taken in pieces whose T x piece matrix G (type t) is held in
- * the workspace; the logits are formed again, the sums are f32.
+ * the workspace (up to 256 MB, or 2048 entries per row of H, beside 64 MB of split
+ * sums); the logits are formed again, the sums are f32.  G is rounded to type t
+ * without the mantissa of the first counted row's scale * dloss, so which way a
+ * bf16 G rounds depends on that weight too.
  * dH: [T][lddh], dW: [V][lddw], type t; beta == 0 ignores dW's previous contents.
  * Outputs must not overlap inputs or ws.
  * ws: device workspace of spec_linear_xent_grad_workspace(T, V, d, t) bytes

@@ -608,6 +608,9 @@ def eigvalsh_batched_dense_desc(A, *, n_samples: int, p_dim: int, k: int = 1, w=
 
 
 # ---------------------------------------------------------------- training a projected student
+#
+# Gradients are calls of their own: none of these is recorded by autograd, and what
+# they return of tensors that require a gradient has none.
 
 #: Five equal steps a s + b s^3 + c s^5 that take singular values from (0, 1] to
 #: about 0.7 .. 1.2 (Muon's coefficients).

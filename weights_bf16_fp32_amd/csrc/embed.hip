@@ -14,10 +14,12 @@
 // share, and leaves the sums of the first and last row, where those continue
 // in a neighbour's share, to be joined by a second pass.
 //
-// Lookup of 8192 rows of 4096 bf16: 18.8 us, 7.0 TB/s (repeated ids come from the
+// Lookup of 8192 rows of 4096 bf16: 18.9 us, 7.0 TB/s (repeated ids come from the
 // caches); of 8 rows 4 us, a launch.  Gradient of 16384 rows into 131072 x 4096
-// bf16: 61 us for the sort and 0.33 GB of zeros, 160 us for the sums and the other
-// 0.75 GB (5.5 TB/s), 9 us for the joins.
+// bf16: 60 us for the sort and 0.33 GB of zeros, 161 us for the sums and the other
+// 0.75 GB (5.5 TB/s), 10 us for the joins.  The joins of one row follow each other in
+// one workgroup per 256 threads of columns: with one id in all of 8192 positions of
+// 4096 bf16, beta = 1 takes 194 us instead of 60, in all of 65536 428 instead of 327.
 //
 //   k_embed      lookup
 //   k_eg_start   up to 16384 positions sorted by one workgroup; beside it, zeros
@@ -184,7 +186,11 @@ __global__ __launch_bounds__(256) void k_sort_move(const int *__restrict__ keys,
 
 // ------------------------------------------------------------------ one workgroup's sort
 
-constexpr int ONE_MAX = 16384;  // positions
+// Positions at most: what its LDS holds.  Against the sort by many workgroups (three
+// launches a pass) the gradient takes, with beta = 1 and nothing to hide the sort behind,
+// 20 us for 41 at 1024 x 4096 bf16, 60 for 79 at 8192, 88 for 96 at 16384; into the 512
+// columns of a table of 4096 rows 18 for 36, 36 for 51, 58 for 57.
+constexpr int ONE_MAX = 16384;
 constexpr int ONE_BITS = 9;     // of the key per pass
 
 struct __attribute__((aligned(16))) OneLds {
@@ -314,8 +320,11 @@ SPEC_DEVICE void sort_one(OneLds &s, const void *ids, int is64, int64_t V, int n
 
 // ------------------------------------------------------------------ sums
 
-// sorted positions per workgroup: few where there are few, so that they fill the
-// chip; more leave fewer rows to be joined
+// Sorted positions per workgroup: few where there are few, so that they fill the
+// chip; more leave fewer rows to be joined.  With 8 and with 32, beta = 1, 4096 bf16 per
+// row: 2048 positions 26 and 37 us, 8192 62 and 61, 16384 102 and 88; 1000 per row: 21
+// and 33, 42 and 50, 68 and 73.  (Beside the zeros of 131072 rows 32 are better from 4096
+// positions on already: 217 and 205 us, at 8192 227 and 202.)
 inline int eg_share(int64_t n) { return n <= 8192 ? 8 : 32; }
 constexpr int EG_AHEAD = 8;   // rows in flight per thread
 

@@ -106,7 +106,7 @@ struct Mm {
     static SPEC_DEVICE int wave_q0(int wave) { return wave / WP % WQ * (BQ / WQ); }
 
     // slot permutation of row p of a Kc tile
-    static SPEC_DEVICE int kc_f(int p) { return ROW == 128 ? (p >> 1) & 7 : (p >> 2) & 3; }
+    static SPEC_DEVICE int kc_f(int p) { return (p >> 1) & 7; }
 
     // slot permutation of row k of a Ks tile with R columns
     template <int R>

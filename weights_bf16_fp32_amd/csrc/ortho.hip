@@ -34,12 +34,16 @@
 // which multiplies more (four products of 32 rows, no symmetry) but never
 // waits for another workgroup's A or B.
 //
-// 4096 x 4096 bf16, per step: 92 us for A (253 tiles of 192 x 192, one per CU), 118 us
-// for B (the same products, and A read for its epilogue), 150 us for X; the
-// products' share of the time, 30 to 43 % MFMA busy, is bounded by single rounds of
-// workgroups, whose first copies and last stores nothing hides.  256 x 256: 11 us per
-// step in one launch.  f32 is bound by the f32 MFMA rate (144 of 157 TFLOP/s at
-// 4096^3); three matrices of 333 x 1000 by the few tiles they have.
+// 4096 x 4096 bf16, per step: 93 us for A (253 tiles of 192 x 192, one per CU), 117 us
+// for B (the same products, and A read for its epilogue), 148 us for X; the
+// products' share of the time, 29 to 42 % MFMA busy, is bounded by single rounds of
+// workgroups, whose first copies and last stores nothing hides, and by one wave per
+// SIMD in the 192 x 192 tiles.  256 x 256: 16 us for the start and 11 to 12.5 us per step
+// in one launch, of which the products are about 2: the rest is reading X, which each of
+// the eight workgroups does whole on an XCD of its own, whose L2 holds little of what
+// the others wrote (22 of 36 thousand requests miss).  f32 is bound by the f32 MFMA
+// rate (144 of 157 TFLOP/s at 4096^3); three matrices of 333 x 1000 by the few tiles
+// they have.
 //
 //   k_ns_norm   partial sums of squares (f64)
 //   k_ns_load   X_0
@@ -338,7 +342,8 @@ struct ChainDims {
 };
 constexpr int CHAIN = 256;  // the longer side at most
 
-// Up to here a wave holds its blocks of both operands in registers, and a
+// Up to here a wave holds its blocks of both operands in registers (236 of 256, and 48
+// bytes of scratch per lane), and a
 // matrix takes 43 us (128 x 128) to 70 us (256 x 256) against 94 to 100 us of the
 // other path from 256 x 512 on; with operands read from memory 256 x 512 took 143 us.
 inline bool chain_fits(int64_t m, int64_t n) { return m <= CHAIN && n <= CHAIN; }

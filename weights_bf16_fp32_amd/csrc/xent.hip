@@ -3,8 +3,8 @@
 //   z_tv = scale <h_t, w_v>,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target
 //   g_tv = scale dloss_t (exp(z_tv - lse_t) - [v = target_t]),  dH = G W,  dW = beta dW + G^T H
 //
-// The T x V logits are never stored.  Forward: every 128 x 128 tile of logits is
-// reduced to one (maximum, sum of exponentials) per row while it is in the
+// The T x V logits are never stored.  Forward: every tile of logits (256 x 256, 128 x
+// 128, or 128 entries by 32 tokens) is reduced to one (maximum, sum of exponentials) per row while it is in the
 // accumulators, and the tiles' pairs are joined per row.  Backward: a piece of
 // the vocabulary at a time, the logits are formed again and leave as the bf16 (f32)
 // gradient G of that piece, which the two gradient products read back.
@@ -15,9 +15,10 @@
 // only: grids are sized for all of them, and the workgroups of the first tiles
 // (counted with the number left, so that they spread over the XCDs) do the work.
 //
-// Bound by the MFMAs (54 to 64 % busy at the clock that their power leaves): at
-// 6144 targets x 131072 x 4096 bf16 the forward takes 5.7 ms (1160 TFLOP/s), the
-// gradients 0.75 ms each of logits, dW and dH per piece of 16384 (1100 TFLOP/s).
+// Bound by the MFMAs (53 to 64 % busy at the clock that their power leaves): at
+// 6144 targets x 131072 x 4096 bf16 the forward takes 5.5 to 5.8 ms (1140 to 1190
+// TFLOP/s), the gradients 0.74 to 0.80 ms each of logits, dW and dH per piece of
+// 16384 (1030 to 1110 TFLOP/s).
 // Storing the logits would save the second forming of them, a quarter of the
 // operations, for T x V x 4 bytes.  Eight rows of 65536 x 4096 are bound by reading W:
 // 121 us, 4.4 TB/s.
@@ -474,7 +475,8 @@ __global__ __launch_bounds__(256) void k_xent_dh_out(const float *__restrict__ p
 // ------------------------------------------------------------------ sizes
 
 // Bytes of a piece's gradient G, and of its rows of W (copied where they are not
-// aligned).  Larger pieces add into the f32 partial dH less
+// aligned), at most, but no fewer than 2048 entries (or V): G is larger from 65536
+// bf16 rows on, 4 KB per row.  Larger pieces add into the f32 partial dH less
 // often (100 MB read and written per piece at 6144 x 4096).
 constexpr int64_t XENT_PIECE_BYTES = (int64_t)256 << 20;
 
@@ -571,7 +573,12 @@ inline bool big_tiles(int64_t rows, int64_t cols)
     return most(256) <= per * most(128);
 }
 
-// the logits of up to this many tokens take the tile for few rows
+// The logits of up to this many tokens take the tile for few rows.  In f32, bound
+// by the MFMAs over all of a tile's rows, it takes 207 us against 509 of the other
+// tiles for 8 tokens of 65536 x 4096, 351 against 514 for 64.  In bf16, bound by W,
+// 130 against 133 for 32; for 33 to 64 its two tiles per strip of W read it twice: 143
+// against 134, and 38 against 32 of 50021 x 1000, but 18 against 22 of 8192 x 1024
+// and 576 against 593 for the gradients of 64 tokens of 65536 x 4096.
 constexpr int64_t FEW_TOKENS = 64;
 
 template <typename E, typename C>
