@@ -629,6 +629,120 @@ int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_
                        const double *coeffs, int steps, double eps, double scale, void *O, int64_t ldo, int64_t so,
                        void *ws, size_t ws_bytes);
 
+/* ------------------------------------------------------------------------
+ * The residual blocks of a student, between the lookup and the head: the norms
+ * around a block with its gate and its sum, activations stored in 8 bits for the
+ * backward pass, products with matrices in 4 bits.
+ *
+ * Microscaled storage.  32 values along a row share a power of two, one byte b per
+ * block:  v = q 2^(b - 127)
+ *   SPEC_MX_INT8  q = i / 64, i a signed byte of -127 .. 127
+ *   SPEC_MX_FP4   q = +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}: 4 bits, bit 3 the sign, bits 0..2
+ *                 the index of the magnitude; two to a byte, the even column in the
+ *                 low half
+ * A matrix of `cols` columns has rows of ldq bytes of codes and of lds bytes of scales,
+ * whole blocks (32 or 16 bytes of codes) and whole groups of 16 scales; what lies past
+ * `cols` in them is zero (spec_mx_quantize writes it so, and a matrix from elsewhere
+ * has to hold it so).  Byte 255 makes a block NaN.
+ * q and s must be 16-byte aligned, ldq and lds multiples of 16, ldq and lds at least
+ * what spec_mx_row_bytes returns; else SPEC_EINVAL (SPEC_EUNSUPPORTED for other fmt).
+ * ---------------------------------------------------------------------- */
+enum { SPEC_MX_INT8 = 0, SPEC_MX_FP4 = 1 };
+
+typedef struct {
+    void *q;     /* codes  [rows][ldq] */
+    void *s;     /* scales [rows][lds] */
+    int64_t ldq, lds;
+    int32_t fmt;
+} spec_mx;
+
+/* Bytes of a row of codes and of scales.  Requires 1 <= cols <= 2^20. */
+int spec_mx_row_bytes(int fmt, int64_t cols, int64_t *codes, int64_t *scales);
+
+/* X [rows][ldx] of type t = SPEC_BF16 or SPEC_F32 into `out`.  b is the smallest at which the
+ * block's largest magnitude does not round past the largest q, from 0 to 254 (INT8) or
+ * 252 (FP4), where larger magnitudes are cut to the largest q; q is the nearest value,
+ * ties to even.  So v is off by half a step of q at most.  A block that holds NaN
+ * or an infinity is NaN (b = 255, codes zero).
+ * Requires 0 <= rows < 2^31, 1 <= cols <= 2^20, ldx >= cols; else SPEC_EINVAL. */
+int spec_mx_quantize(void *stream, const void *X, int t, int64_t rows, int64_t cols, int64_t ldx, const spec_mx *out);
+
+/* The values, to X of type t (exact in bf16 too; values below 2^-133 round there). */
+int spec_mx_dequantize(void *stream, const spec_mx *in, int64_t rows, int64_t cols, void *X, int t, int64_t ldx);
+
+/* Y[T][N] = X[T][K] W^T with W [N][K] in SPEC_MX_FP4 (else SPEC_EUNSUPPORTED), X and Y of type
+ * t = SPEC_BF16 (MFMA bf16, in which W is exact) or SPEC_F32 (MFMA f32), f32 sums.
+ * ws: device workspace of spec_mx_linear_workspace(T, N, K, t) bytes (256-byte aligned).
+ * Requires 0 <= T <= 2^22, 1 <= N, K <= 2^20, ldx >= K and <= 2^20 + 64, ldy >= N; else
+ * SPEC_EINVAL.  Y must not overlap X, W or ws.  Products of subnormal values may
+ * be taken as zero. */
+int spec_mx_linear_workspace(int64_t T, int64_t N, int64_t K, int t, size_t *bytes);
+
+int spec_mx_linear(void *stream, const void *X, int t, int64_t T, int64_t N, int64_t K, int64_t ldx, const spec_mx *W,
+                   void *Y, int64_t ldy, void *ws, size_t ws_bytes);
+
+/* The same with X [T][K] in SPEC_MX_FP4 too; Y of type yt = SPEC_BF16 or SPEC_F32. */
+int spec_mx_product_workspace(int64_t T, int64_t N, int64_t K, size_t *bytes);
+
+int spec_mx_product(void *stream, const spec_mx *X, const spec_mx *W, int64_t T, int64_t N, int64_t K, void *Y, int yt,
+                    int64_t ldy, void *ws, size_t ws_bytes);
+
+/* Weight gradient from activations stored in 8 bits:  dW[N][K] = beta dW + dY^T X with
+ * dY [T][N] and dW of type t = SPEC_BF16 (MFMA bf16, in which X is exact) or SPEC_F32, X
+ * [T][K] in SPEC_MX_INT8 (else SPEC_EUNSUPPORTED), f32 sums; beta (in f32) == 0 ignores dW's
+ * previous contents.
+ * ws: device workspace of spec_mx_weight_grad_workspace(T, N, K, t) bytes (256-byte
+ * aligned).  Requires the sizes of spec_mx_linear with ldy >= N, lddw >= K, ldy <= 2^20 + 64.
+ * dW must not overlap dY, X or ws. */
+int spec_mx_weight_grad_workspace(int64_t T, int64_t N, int64_t K, int t, size_t *bytes);
+
+int spec_mx_weight_grad(void *stream, const void *dY, int t, int64_t T, int64_t N, int64_t K, int64_t ldy,
+                        const spec_mx *X, double beta, void *dW, int64_t lddw, void *ws, size_t ws_bytes);
+
+/* The norms around a residual block, its gate and its sum, rows of d features:
+ *   u = Y r_post w_post,  r_post = (mean Y^2 + eps)^(-1/2)     (post == 0: u = Y)
+ *   Hout = alpha H + beta gate u
+ *   X = Hout r_pre w_pre,  r_pre = (mean Hout^2 + eps)^(-1/2)     (of Hout before it is rounded)
+ * Computed in f32, each output rounded once. */
+typedef struct {
+    int64_t n, d;
+    int32_t t;           /* SPEC_BF16 or SPEC_F32: matrices, weights and gate */
+    int32_t post;        /* whether Y is normed */
+    double alpha, beta;  /* finite in f32 */
+    double eps;          /* > 0 in f32 */
+    const void *w_post, *w_pre; /* [d], NULL: ones (w_post NULL where post == 0) */
+    const void *gate;    /* row i takes gate row i / gate_rows; NULL: ones */
+    int64_t ldg;         /* >= d where there are several gate rows */
+    int64_t gate_rows;   /* >= 1 where there is a gate */
+} spec_block;
+
+/* Y == NULL: the norm of H alone (Hout is H and not written).  Hout, X, r_post, r_pre (f32 [n])
+ * may each be NULL: not wanted.  y8, h8, x8 (SPEC_MX_INT8, NULL: not wanted) receive Y, Hout and X
+ * as spec_mx_quantize would store them.  Hout may be H, and X may be Y (same rows).
+ * Requires 0 <= n < 2^31, 1 <= d <= 16384, ld* >= d of the matrices given, Y where Hout, r_post, y8 or h8 is
+ * wanted; else SPEC_EINVAL. */
+int spec_block_norm(void *stream, const spec_block *b, const void *Y, int64_t ldy, const void *H, int64_t ldh,
+                    void *Hout, int64_t ldo, void *X, int64_t ldx, float *r_post, float *r_pre, const spec_mx *y8,
+                    const spec_mx *h8, const spec_mx *x8);
+
+/* Its gradients, from dX and what reaches Hout otherwise, dHout (either may be NULL: zero):
+ *   a = dX w_pre,  n2 = Hout r_pre,  G = dHout + r_pre (a - n2 mean(a n2)),  dH = alpha G
+ *   n1 = Y r_post,  c = beta gate w_post G,  dY = r_post (c - n1 mean(c n1))     (post == 0: n1 = Y, dY = c)
+ *   dw_pre = sum dX n2,  dw_post = sum beta gate G n1,  dgate = sum over the gate row's rows of beta w_post G n1
+ * Y and Hout are given as matrices or, where y8 / h8 is not NULL, as SPEC_MX_INT8; Hout is needed where dX is
+ * given; Y and y8 both NULL: no block (dY, dw_post, dgate not wanted).  r_post, r_pre as
+ * spec_block_norm returned them (r_post where post, r_pre where dX is given).
+ * dw_post, dw_pre: f32 [d], dgate: f32 [ceil(n / gate_rows)][d], written (zeros for n = 0; dw_pre
+ * only where dX is given).  Outputs may be NULL: not wanted.  dH may be dHout, and dY may be dX (same rows).
+ * The sums over rows are f32, in the same order in every run.
+ * ws: device workspace of spec_block_norm_grad_workspace(b) bytes (256-byte aligned). */
+int spec_block_norm_grad_workspace(const spec_block *b, size_t *bytes);
+
+int spec_block_norm_grad(void *stream, const spec_block *b, const void *Y, int64_t ldy, const spec_mx *y8,
+                         const void *Hout, int64_t ldo, const spec_mx *h8, const float *r_post, const float *r_pre,
+                         const void *dHout, int64_t lddo, const void *dX, int64_t lddx, void *dH, int64_t lddh, void *dY,
+                         int64_t lddy, float *dw_post, float *dw_pre, float *dgate, void *ws, size_t ws_bytes);
+
 #ifdef __cplusplus
 }
 #endif

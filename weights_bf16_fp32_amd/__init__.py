@@ -18,11 +18,16 @@ fallback of any kind.
     dH, dW = spec.linear_xent_grad(H, W, target, lse, dloss)  # its gradients
     spec.embed_grad(dX, ids, V, scale=d ** 0.5, beta=1.0, dE=dW)  # into a tied table's gradient
     O = spec.orthogonalize(G)                                 # Newton-Schulz: G with its singular values near one
+    h, x, r_post, r_pre = spec.block_norm(h, y, w_post=a, gate=g, w_pre=b)  # h + g norm(y) a, and its norm times b
+    q = spec.mx_quantize(x, spec.MX_INT8)                     # x in 8 bits for the backward pass
+    dW = spec.mx_weight_grad(dz, q)                           # dz^T x
+    y = spec.mx_linear(x, spec.mx_quantize(W, spec.MX_FP4))   # x W^T from W in 4 bits
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -33,12 +38,16 @@ __all__ = [
     "eigvecs_topk", "project_weight", "project_weight_workspace",
     "embed", "embed_grad", "embed_grad_workspace", "linear_xent", "linear_xent_workspace", "linear_xent_grad",
     "linear_xent_grad_workspace", "orthogonalize", "orthogonalize_workspace", "NS_COEFFS",
+    "Mx", "MX_INT8", "MX_FP4", "mx_empty", "mx_quantize", "mx_dequantize", "mx_linear", "mx_linear_workspace",
+    "mx_product", "mx_product_workspace", "mx_weight_grad", "mx_weight_grad_workspace", "block_norm", "block_norm_grad",
+    "block_norm_grad_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspec.so")
 
 BF16, F32, F64, I32, I64 = 0, 1, 2, 3, 4
+MX_INT8, MX_FP4 = 0, 1
 GRAM_BAND, GRAM_DENSE = 0, 1
 SRC_DENSE, SRC_BAND = 0, 1
 MODE_EIG, MODE_SINGULAR = 0, 1
@@ -100,6 +109,18 @@ class RobustParams(ctypes.Structure):
                 ("mad_k", ctypes.c_double)]
 
 
+class MxMatrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("lds", ctypes.c_int64),
+                ("fmt", ctypes.c_int32)]
+
+
+class Block(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("d", ctypes.c_int64), ("t", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("alpha", ctypes.c_double), ("beta", ctypes.c_double), ("eps", ctypes.c_double),
+                ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("ldg", ctypes.c_int64), ("gate_rows", ctypes.c_int64)]
+
+
 EXPORTS = ["spec_strerror", "spec_version", "spec_cov_accumulate", "spec_gram_window",
            "spec_eigvalsh_batched", "spec_eigvalsh_large_workspace", "spec_eigvalsh_large",
            "spec_descriptors_workspace", "spec_descriptors", "spec_desc_smooth", "spec_spectrum_robust",
@@ -108,7 +129,10 @@ EXPORTS = ["spec_strerror", "spec_version", "spec_cov_accumulate", "spec_gram_wi
            "spec_eigvalsh_sliding", "spec_eigh_large_workspace", "spec_eigh_large", "spec_eigh_batched",
            "spec_embed", "spec_embed_grad_workspace", "spec_embed_grad", "spec_linear_xent_workspace",
            "spec_linear_xent", "spec_linear_xent_grad_workspace", "spec_linear_xent_grad",
-           "spec_orthogonalize_workspace", "spec_orthogonalize"]
+           "spec_orthogonalize_workspace", "spec_orthogonalize",
+           "spec_mx_row_bytes", "spec_mx_quantize", "spec_mx_dequantize", "spec_mx_linear_workspace", "spec_mx_linear",
+           "spec_mx_product_workspace", "spec_mx_product", "spec_mx_weight_grad_workspace", "spec_mx_weight_grad",
+           "spec_block_norm", "spec_block_norm_grad_workspace", "spec_block_norm_grad"]
 
 _lib = None
 
@@ -162,6 +186,20 @@ def lib() -> ctypes.CDLL:
         L.spec_orthogonalize_workspace.argtypes = [i64, i64, i64, i32, szp]
         L.spec_orthogonalize.argtypes = [vp, vp, i32, i64, i64, i64, i64, i64, ctypes.POINTER(dbl), i32, dbl, dbl,
                                          vp, i64, i64, vp, sz]
+        mxp, blp, i64p = ctypes.POINTER(MxMatrix), ctypes.POINTER(Block), ctypes.POINTER(i64)
+        L.spec_mx_row_bytes.argtypes = [i32, i64, i64p, i64p]
+        L.spec_mx_quantize.argtypes = [vp, vp, i32, i64, i64, i64, mxp]
+        L.spec_mx_dequantize.argtypes = [vp, mxp, i64, i64, vp, i32, i64]
+        L.spec_mx_linear_workspace.argtypes = [i64, i64, i64, i32, szp]
+        L.spec_mx_linear.argtypes = [vp, vp, i32, i64, i64, i64, i64, mxp, vp, i64, vp, sz]
+        L.spec_mx_product_workspace.argtypes = [i64, i64, i64, szp]
+        L.spec_mx_product.argtypes = [vp, mxp, mxp, i64, i64, i64, vp, i32, i64, vp, sz]
+        L.spec_mx_weight_grad_workspace.argtypes = [i64, i64, i64, i32, szp]
+        L.spec_mx_weight_grad.argtypes = [vp, vp, i32, i64, i64, i64, i64, mxp, dbl, vp, i64, vp, sz]
+        L.spec_block_norm.argtypes = [vp, blp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, mxp, mxp, mxp]
+        L.spec_block_norm_grad_workspace.argtypes = [blp, szp]
+        L.spec_block_norm_grad.argtypes = [vp, blp, vp, i64, mxp, vp, i64, mxp, vp, vp, vp, i64, vp, i64, vp, i64, vp,
+                                           i64, vp, vp, vp, vp, sz]
         L.spec_timing_enable.argtypes = [ctypes.c_uint]
         L.spec_timing_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
         for f in EXPORTS[2:]:
@@ -780,3 +818,248 @@ def orthogonalize(G, coeffs=NS_COEFFS, eps: float = 1e-7, scale: float = 1.0, ou
     _check(lib().spec_orthogonalize(_stream(), _dev(G), t, batch, m, n, ldg, sg, co, steps, float(eps), float(scale),
                                     _dev(out), ldo, so, _dev(ws), ws.numel()))
     return out
+
+
+# ---------------------------------------------------------------- a student's residual blocks
+#
+# As above, gradients are calls of their own.  Tensors have to be on the current device.
+
+class Mx(NamedTuple):
+    """A microscaled matrix: codes uint8 [rows, ldq], scales uint8 [rows, lds] (contiguous
+    rows, a row's bytes as mx_empty gives them or more), its columns and its format."""
+    q: Any
+    s: Any
+    cols: int
+    fmt: int
+
+
+def _here(t):
+    """The address of a tensor, which must be on the current device."""
+    if not t.is_cuda:
+        raise SpecError(-1, "tensor must be on the GPU")
+    if t.get_device() != _torch().cuda.current_device():
+        raise SpecError(-1, "tensor must be on the current device")
+    return t.data_ptr()
+
+
+def _mx_rows(fmt, cols):
+    if fmt not in (MX_INT8, MX_FP4):
+        raise SpecError(-2, f"unsupported microscaled format {fmt}")
+    if cols < 1:
+        raise SpecError(-1, "a microscaled matrix has columns")
+    blocks = (cols + 31) // 32
+    return blocks * (32 if fmt == MX_INT8 else 16), (blocks + 15) // 16 * 16
+
+
+def _mx(m, rows=None, cols=None):
+    """The C descriptor of a microscaled matrix of these sizes."""
+    if not isinstance(m, Mx):
+        raise SpecError(-1, "a microscaled matrix (Mx) is needed")
+    torch = _torch()
+    q, s = m.q, m.s
+    if q.dtype != torch.uint8 or s.dtype != torch.uint8 or q.dim() != 2 or s.dim() != 2 or q.shape[0] != s.shape[0]:
+        raise SpecError(-1, "codes and scales must be uint8 [rows, bytes]")
+    lq, ls = _mx_rows(m.fmt, m.cols)
+    if q.shape[1] < lq or s.shape[1] < ls or q.stride(1) != 1 or s.stride(1) != 1:
+        raise SpecError(-1, f"rows of {m.cols} columns are {lq} contiguous bytes of codes and {ls} of scales")
+    if (rows is not None and q.shape[0] != rows) or (cols is not None and m.cols != cols):
+        raise SpecError(-1, f"the microscaled matrix must be {rows} x {cols}, not {q.shape[0]} x {m.cols}")
+    one = q.shape[0] <= 1
+    return MxMatrix(_here(q), _here(s), lq if one else q.stride(0), ls if one else s.stride(0), m.fmt)
+
+
+def mx_empty(rows: int, cols: int, fmt: int, device="cuda") -> Mx:
+    """Uninitialised storage of a microscaled matrix (mx_quantize and block_norm fill it)."""
+    torch = _torch()
+    lq, ls = _mx_rows(fmt, cols)
+    return Mx(torch.empty((rows, lq), dtype=torch.uint8, device=device),
+              torch.empty((rows, ls), dtype=torch.uint8, device=device), cols, fmt)
+
+
+def mx_quantize(X, fmt: int, out: Mx = None) -> Mx:
+    """X [rows, cols] (bfloat16 or float32) in microscaled storage, MX_INT8 or MX_FP4."""
+    _rows(X)
+    rows, cols = X.shape
+    if out is None:
+        out = mx_empty(rows, cols, fmt, X.device)
+    if out.fmt != fmt:
+        raise SpecError(-1, "out has another format")
+    o = _mx(out, rows, cols)
+    _check(lib().spec_mx_quantize(_stream(), _here(X), _dt(X), rows, cols, _ld(X), ctypes.byref(o)))
+    return out
+
+
+def mx_dequantize(m: Mx, dtype=None, out=None):
+    """The values of a microscaled matrix, bfloat16 (the default) or float32."""
+    torch = _torch()
+    d = _mx(m)
+    rows, cols = m.q.shape[0], m.cols
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=m.q.device)
+    _matrix(out, (rows, cols), dtype or out.dtype)
+    _check(lib().spec_mx_dequantize(_stream(), ctypes.byref(d), rows, cols, _here(out), _dt(out), _ld(out)))
+    return out
+
+
+def mx_linear_workspace(T: int, N: int, K: int, dtype) -> int:
+    return _bytes(lib().spec_mx_linear_workspace, T, N, K, _dt(_torch().empty(0, dtype=dtype)))
+
+
+def mx_linear(X, W: Mx, out=None, ws=None):
+    """X W^T [T, N] for X [T, K] (bfloat16 or float32) and W [N, K] in MX_FP4."""
+    _rows(X)
+    T, K = X.shape
+    w = _mx(W, None, K)
+    N, t = W.q.shape[0], _dt(X)
+    if out is None:
+        out = _torch().empty((T, N), dtype=X.dtype, device=X.device)
+    _matrix(out, (T, N), X.dtype)
+    ws = _ws(ws, _bytes(lib().spec_mx_linear_workspace, T, N, K, t), X.device)
+    _check(lib().spec_mx_linear(_stream(), _here(X), t, T, N, K, _ld(X), ctypes.byref(w), _here(out), _ld(out), _here(ws),
+                                ws.numel()))
+    return out
+
+
+def mx_product_workspace(T: int, N: int, K: int) -> int:
+    return _bytes(lib().spec_mx_product_workspace, T, N, K)
+
+
+def mx_product(X: Mx, W: Mx, dtype=None, out=None, ws=None):
+    """X W^T [T, N] in bfloat16 (the default) or float32 for X [T, K] and W [N, K] in MX_FP4."""
+    torch = _torch()
+    x = _mx(X)
+    w = _mx(W, None, X.cols)
+    T, N, K = X.q.shape[0], W.q.shape[0], X.cols
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype or torch.bfloat16, device=X.q.device)
+    _matrix(out, (T, N), dtype or out.dtype)
+    ws = _ws(ws, _bytes(lib().spec_mx_product_workspace, T, N, K), X.q.device)
+    _check(lib().spec_mx_product(_stream(), ctypes.byref(x), ctypes.byref(w), T, N, K, _here(out), _dt(out), _ld(out),
+                                 _here(ws), ws.numel()))
+    return out
+
+
+def mx_weight_grad_workspace(T: int, N: int, K: int, dtype) -> int:
+    return _bytes(lib().spec_mx_weight_grad_workspace, T, N, K, _dt(_torch().empty(0, dtype=dtype)))
+
+
+def mx_weight_grad(dY, X: Mx, beta: float = 0.0, dW=None, ws=None):
+    """dW = beta dW + dY^T X [N, K] in dY's type, for dY [T, N] (bfloat16 or float32) and
+    X [T, K] in MX_INT8."""
+    _rows(dY)
+    T, N = dY.shape
+    x = _mx(X, T)
+    K, t = X.cols, _dt(dY)
+    if dW is None:
+        if beta != 0.0:
+            raise SpecError(-1, "beta needs the dW to add to")
+        dW = _torch().empty((N, K), dtype=dY.dtype, device=dY.device)
+    _matrix(dW, (N, K), dY.dtype)
+    ws = _ws(ws, _bytes(lib().spec_mx_weight_grad_workspace, T, N, K, t), dY.device)
+    _check(lib().spec_mx_weight_grad(_stream(), _here(dY), t, T, N, K, _ld(dY), ctypes.byref(x), float(beta), _here(dW),
+                                     _ld(dW), _here(ws), ws.numel()))
+    return dW
+
+
+def _block(n, d, like, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps):
+    """The C descriptor of a block's norms: (Block, gate rows)."""
+    def vec(w):
+        if w is None:
+            return None
+        if w.dtype != like.dtype or tuple(w.shape) != (d,) or (w.stride(0) != 1 and d > 1):
+            raise SpecError(-1, f"weights must be contiguous [{d}] of {like.dtype}")
+        return _here(w)
+    ldg, gates = d, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate, gate_rows = gate.unsqueeze(0), max(n, 1)
+        _rows(gate)
+        gates = (n + gate_rows - 1) // gate_rows if gate_rows >= 1 else -1
+        if gate.dtype != like.dtype or gate.shape[1] != d or gates < 0 or gate.shape[0] < gates:
+            raise SpecError(-1, f"gate must be [rows / gate_rows, {d}] of {like.dtype}, or [{d}]")
+        ldg = _ld(gate)
+    return Block(n, d, _dt(like), 1 if post else 0, float(alpha), float(beta), float(eps), vec(w_post), vec(w_pre),
+                 None if gate is None else _here(gate), ldg, int(gate_rows)), gates
+
+
+def _opt(t, shape, dtype):
+    """(address, row stride) of an optional matrix."""
+    if t is None:
+        return None, 0
+    _matrix(t, shape, dtype)
+    return _here(t), _ld(t)
+
+
+def _opt8(m, n, d):
+    return None if m is None else ctypes.byref(_mx(m, n, d))
+
+
+def block_norm(H, Y=None, post: bool = True, w_post=None, w_pre=None, gate=None, gate_rows: int = 1, alpha: float = 1.0,
+               beta: float = 1.0, eps: float = 1e-6, Hout=None, X=None, y8: Mx = None, h8: Mx = None, x8: Mx = None):
+    """The norms around a residual block: u = norm(Y) w_post (post) or Y, Hout = alpha H + beta gate u,
+    X = norm(Hout) w_pre.  Returns (Hout, X, r_post, r_pre), r the rows' factors of the two norms
+    (None where there is none); without Y, Hout is H.  gate: [d], or [rows, d] of which
+    one row serves gate_rows rows of Y.  y8, h8, x8: MX_INT8 storage that
+    receives Y, Hout and X.  Hout may be H, X may be Y."""
+    torch = _torch()
+    _rows(H)
+    n, d = H.shape
+    b, _ = _block(n, d, H, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps)
+    if Y is not None and Hout is None:
+        Hout = torch.empty((n, d), dtype=H.dtype, device=H.device)
+    if X is None:
+        X = torch.empty((n, d), dtype=H.dtype, device=H.device)
+    r_post = torch.empty((n,), dtype=torch.float32, device=H.device) if Y is not None and post else None
+    r_pre = torch.empty((n,), dtype=torch.float32, device=H.device)
+    y, ho, x = (_opt(t, (n, d), H.dtype) for t in (Y, Hout, X))
+    _check(lib().spec_block_norm(_stream(), ctypes.byref(b), *y, _here(H), _ld(H), *ho, *x,
+                                 None if r_post is None else _here(r_post), _here(r_pre), _opt8(y8, n, d), _opt8(h8, n, d),
+                                 _opt8(x8, n, d)))
+    return H if Y is None else Hout, X, r_post, r_pre
+
+
+def block_norm_grad_workspace(n: int, d: int, dtype, gates: int = 0, gate_rows: int = 1) -> int:
+    """Workspace of block_norm_grad, with `gates` gate rows (0: no gate) of gate_rows rows each."""
+    b = Block(n, d, _dt(_torch().empty(0, dtype=dtype)), 0, 1.0, 1.0, 1e-6, None, None, 256 if gates else None, d, gate_rows)
+    return _bytes(lib().spec_block_norm_grad_workspace, ctypes.byref(b))
+
+
+def block_norm_grad(dX, dHout, Hout, Y, r_pre, r_post=None, post: bool = True, w_post=None, w_pre=None, gate=None,
+                    gate_rows: int = 1, alpha: float = 1.0, beta: float = 1.0, dH=None, dY=None, ws=None):
+    """Gradients of block_norm from those of its X and (otherwise than through X) of its Hout; either
+    may be None: zero.  Hout and Y as they were, or as stored in MX_INT8; Y None: no block.
+    Returns (dH, dY, dw_post, dw_pre, dgate), the last three float32, None for what was not given.
+    dH may be dHout, dY may be dX."""
+    torch = _torch()
+    like = dX if dX is not None else dHout
+    if like is None:
+        raise SpecError(-1, "a gradient of X or of Hout is needed")
+    n, d = like.shape
+    b, gates = _block(n, d, like, post and Y is not None, w_post if Y is not None else None, w_pre,
+                      gate if Y is not None else None, gate_rows, alpha, beta, 1e-6)
+
+    def stored(t):
+        """(address, stride, descriptor) of a matrix or of its checkpoint."""
+        return (None, 0, _opt8(t, n, d)) if isinstance(t, Mx) else (*_opt(t, (n, d), like.dtype), None)
+    y, ho = stored(Y), stored(Hout if dX is not None else None)
+    if dH is None:
+        dH = torch.empty((n, d), dtype=like.dtype, device=like.device)
+    if dY is None and Y is not None:
+        dY = torch.empty((n, d), dtype=like.dtype, device=like.device)
+
+    def f32(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+    def at(t):
+        return None if t is None else _here(t)
+    dw_post = f32(d) if b.post and w_post is not None else None
+    dw_pre = f32(d) if dX is not None and w_pre is not None else None
+    dgate = f32(gates, d) if gate is not None and Y is not None else None
+    ws = _ws(ws, _bytes(lib().spec_block_norm_grad_workspace, ctypes.byref(b)), like.device)
+    r1 = _vec32(r_post, n) if b.post and r_post is not None else None
+    r2 = _vec32(r_pre, n) if dX is not None and r_pre is not None else None
+    _check(lib().spec_block_norm_grad(_stream(), ctypes.byref(b), *y, *ho, r1, r2, *_opt(dHout, (n, d), like.dtype),
+                                      *_opt(dX, (n, d), like.dtype), *_opt(dH, (n, d), like.dtype),
+                                      *_opt(dY, (n, d), like.dtype), at(dw_post), at(dw_pre), at(dgate), _here(ws),
+                                      ws.numel()))
+    return dH, dY, dw_post, dw_pre, dgate if dgate is None or gate.dim() == 2 else dgate.view(d)

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "internal.h"
 
 namespace {
@@ -81,6 +83,61 @@ int check_ortho_sizes(int64_t batch, int64_t m, int64_t n, int t)
     if (batch < 1 || batch > 65535 || m < 1 || n < 1 || m > 65536 || n > 65536 || (m > 32768 && n > 32768))
         return SPEC_EINVAL;
     return SPEC_OK;
+}
+
+// a microscaled matrix of `rows` x `cols` (the sizes are checked)
+int check_mx(const spec_mx *m, int64_t rows, int64_t cols)
+{
+    if (m == nullptr) return SPEC_EINVAL;
+    if (m->fmt != SPEC_MX_INT8 && m->fmt != SPEC_MX_FP4) return SPEC_EUNSUPPORTED;
+    const int64_t blocks = (cols + 31) / 32;
+    if (m->ldq < blocks * (m->fmt == SPEC_MX_INT8 ? 32 : 16) || m->lds < (blocks + 15) / 16 * 16) return SPEC_EINVAL;
+    if (m->ldq > ((int64_t)1 << 22) || m->lds > ((int64_t)1 << 22)) return SPEC_EINVAL;
+    if (m->ldq % 16 != 0 || m->lds % 16 != 0 || !aligned(m->q, 16) || !aligned(m->s, 16)) return SPEC_EINVAL;
+    return rows > 0 && (m->q == nullptr || m->s == nullptr) ? SPEC_EINVAL : SPEC_OK;
+}
+
+int check_mx_matrix(const spec_mx *m, const void *X, int t, int64_t rows, int64_t cols, int64_t ldx)
+{
+    if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    if (rows < 0 || rows >= (int64_t)1 << 31 || cols < 1 || cols > ((int64_t)1 << 20)) return SPEC_EINVAL;
+    if ((X == nullptr && rows > 0) || ldx < cols || !aligned(X, elt_size(t))) return SPEC_EINVAL;
+    return check_mx(m, rows, cols);
+}
+
+int check_mx_sizes(int64_t T, int64_t N, int64_t K, int t)
+{
+    if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    const int64_t lim = (int64_t)1 << 20;
+    return T < 0 || T > 4 * lim || N < 1 || N > lim || K < 1 || K > lim ? SPEC_EINVAL : SPEC_OK;
+}
+
+// a checkpoint of the norms: absent, or INT8
+int check_stored(const spec_mx *m, int64_t n, int64_t d)
+{
+    if (m == nullptr) return SPEC_OK;
+    const int st = check_mx(m, n, d);
+    return st == SPEC_OK && m->fmt != SPEC_MX_INT8 ? SPEC_EUNSUPPORTED : st;
+}
+
+int check_block(const spec_block *b)
+{
+    if (b == nullptr) return SPEC_EINVAL;
+    if (b->t != SPEC_BF16 && b->t != SPEC_F32) return SPEC_EUNSUPPORTED;
+    if (b->n < 0 || b->n >= (int64_t)1 << 31 || b->d < 1 || b->d > BLOCK_MAX_D) return SPEC_EINVAL;
+    if (!finite32(b->alpha) || !finite32(b->beta) || !(b->eps >= FLT_MIN) || !finite32(b->eps)) return SPEC_EINVAL;
+    const size_t es = elt_size(b->t);
+    if (!aligned(b->w_post, es) || !aligned(b->w_pre, es) || !aligned(b->gate, es)) return SPEC_EINVAL;
+    if (b->post == 0 && b->w_post != nullptr) return SPEC_EINVAL;
+    if (b->gate != nullptr && (b->gate_rows < 1 || (b->gate_rows < b->n && b->ldg < b->d))) return SPEC_EINVAL;
+    return SPEC_OK;
+}
+
+// a matrix of the norms that is given (or has to be)
+bool block_matrix(const spec_block *b, const void *p, int64_t ld, bool needed = false)
+{
+    if (p == nullptr) return !needed;
+    return ld >= b->d && aligned(p, elt_size(b->t));
 }
 
 }  // namespace
@@ -511,6 +568,162 @@ int spec_orthogonalize(void *stream, const void *G, int t, int64_t batch, int64_
     if (!aligned(ws, 256)) return SPEC_EINVAL;
     return from_hip(launch_orthogonalize((hipStream_t)stream, G, t, batch, m, n, ldg, sg, coeffs, steps, eps, scale, O,
                                          ldo, so, ws));
+}
+
+int spec_mx_row_bytes(int fmt, int64_t cols, int64_t *codes, int64_t *scales)
+{
+    if (fmt != SPEC_MX_INT8 && fmt != SPEC_MX_FP4) return SPEC_EUNSUPPORTED;
+    if (codes == nullptr || scales == nullptr || cols < 1 || cols > ((int64_t)1 << 20)) return SPEC_EINVAL;
+    const int64_t blocks = (cols + 31) / 32;
+    *codes = blocks * (fmt == SPEC_MX_INT8 ? 32 : 16);
+    *scales = (blocks + 15) / 16 * 16;
+    return SPEC_OK;
+}
+
+int spec_mx_quantize(void *stream, const void *X, int t, int64_t rows, int64_t cols, int64_t ldx, const spec_mx *out)
+{
+    const int st = check_mx_matrix(out, X, t, rows, cols, ldx);
+    if (st != SPEC_OK) return st;
+    return from_hip(launch_mx_quantize((hipStream_t)stream, X, t, rows, cols, ldx, out));
+}
+
+int spec_mx_dequantize(void *stream, const spec_mx *in, int64_t rows, int64_t cols, void *X, int t, int64_t ldx)
+{
+    const int st = check_mx_matrix(in, X, t, rows, cols, ldx);
+    if (st != SPEC_OK) return st;
+    return from_hip(launch_mx_dequantize((hipStream_t)stream, in, rows, cols, cols, X, t, ldx));
+}
+
+int spec_mx_linear_workspace(int64_t T, int64_t N, int64_t K, int t, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_mx_sizes(T, N, K, t);
+    if (st != SPEC_OK) return st;
+    *bytes = mx_linear_workspace_bytes(T, N, K, t);
+    return SPEC_OK;
+}
+
+int spec_mx_linear(void *stream, const void *X, int t, int64_t T, int64_t N, int64_t K, int64_t ldx, const spec_mx *W,
+                   void *Y, int64_t ldy, void *ws, size_t ws_bytes)
+{
+    int st = check_mx_sizes(T, N, K, t);
+    if (st != SPEC_OK) return st;
+    if (T > 0 && (X == nullptr || Y == nullptr)) return SPEC_EINVAL;
+    if (ldx < K || ldx > ((int64_t)1 << 20) + 64 || ldy < N) return SPEC_EINVAL;
+    if (!aligned(X, elt_size(t)) || !aligned(Y, elt_size(t))) return SPEC_EINVAL;
+    st = check_mx(W, N, K);
+    if (st != SPEC_OK) return st;
+    if (W->fmt != SPEC_MX_FP4) return SPEC_EUNSUPPORTED;
+    if (ws == nullptr || ws_bytes < mx_linear_workspace_bytes(T, N, K, t)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_mx_linear((hipStream_t)stream, X, t, T, N, K, ldx, W, Y, ldy, ws));
+}
+
+int spec_mx_product_workspace(int64_t T, int64_t N, int64_t K, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_mx_sizes(T, N, K, SPEC_BF16);
+    if (st != SPEC_OK) return st;
+    *bytes = mx_product_workspace_bytes(T, N, K);
+    return SPEC_OK;
+}
+
+int spec_mx_product(void *stream, const spec_mx *X, const spec_mx *W, int64_t T, int64_t N, int64_t K, void *Y, int yt,
+                    int64_t ldy, void *ws, size_t ws_bytes)
+{
+    int st = check_mx_sizes(T, N, K, yt);
+    if (st != SPEC_OK) return st;
+    if ((Y == nullptr && T > 0) || ldy < N || !aligned(Y, elt_size(yt))) return SPEC_EINVAL;
+    st = check_mx(X, T, K);
+    if (st != SPEC_OK) return st;
+    st = check_mx(W, N, K);
+    if (st != SPEC_OK) return st;
+    if (X->fmt != SPEC_MX_FP4 || W->fmt != SPEC_MX_FP4) return SPEC_EUNSUPPORTED;
+    if (ws == nullptr || ws_bytes < mx_product_workspace_bytes(T, N, K)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_mx_product((hipStream_t)stream, X, W, T, N, K, Y, yt, ldy, ws));
+}
+
+int spec_mx_weight_grad_workspace(int64_t T, int64_t N, int64_t K, int t, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_mx_sizes(T, N, K, t);
+    if (st != SPEC_OK) return st;
+    *bytes = mx_weight_grad_workspace_bytes(T, N, K, t);
+    return SPEC_OK;
+}
+
+int spec_mx_weight_grad(void *stream, const void *dY, int t, int64_t T, int64_t N, int64_t K, int64_t ldy,
+                        const spec_mx *X, double beta, void *dW, int64_t lddw, void *ws, size_t ws_bytes)
+{
+    int st = check_mx_sizes(T, N, K, t);
+    if (st != SPEC_OK) return st;
+    if (dW == nullptr || (dY == nullptr && T > 0) || ldy < N || ldy > ((int64_t)1 << 20) + 64 || lddw < K)
+        return SPEC_EINVAL;
+    if (!aligned(dY, elt_size(t)) || !aligned(dW, elt_size(t)) || !finite32(beta)) return SPEC_EINVAL;
+    st = check_mx(X, T, K);
+    if (st != SPEC_OK) return st;
+    if (X->fmt != SPEC_MX_INT8) return SPEC_EUNSUPPORTED;
+    if (ws == nullptr || ws_bytes < mx_weight_grad_workspace_bytes(T, N, K, t)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_mx_weight_grad((hipStream_t)stream, dY, t, T, N, K, ldy, X, (float)beta, dW, lddw, ws));
+}
+
+int spec_block_norm(void *stream, const spec_block *b, const void *Y, int64_t ldy, const void *H, int64_t ldh,
+                    void *Hout, int64_t ldo, void *X, int64_t ldx, float *r_post, float *r_pre, const spec_mx *y8,
+                    const spec_mx *h8, const spec_mx *x8)
+{
+    int st = check_block(b);
+    if (st != SPEC_OK) return st;
+    const bool some = b->n > 0;
+    if (!block_matrix(b, H, ldh, some) || !block_matrix(b, Y, ldy) || !block_matrix(b, Hout, ldo) ||
+        !block_matrix(b, X, ldx) || !aligned(r_post, 4) || !aligned(r_pre, 4))
+        return SPEC_EINVAL;
+    if (some && Y == nullptr && (Hout != nullptr || r_post != nullptr || y8 != nullptr || h8 != nullptr)) return SPEC_EINVAL;
+    if (r_post != nullptr && b->post == 0) return SPEC_EINVAL;
+    for (const spec_mx *m : {y8, h8, x8}) {
+        st = check_stored(m, b->n, b->d);
+        if (st != SPEC_OK) return st;
+    }
+    return from_hip(launch_block_norm((hipStream_t)stream, b, Y, ldy, H, ldh, Hout, ldo, X, ldx, r_post, r_pre, y8, h8, x8));
+}
+
+int spec_block_norm_grad_workspace(const spec_block *b, size_t *bytes)
+{
+    if (bytes == nullptr) return SPEC_EINVAL;
+    const int st = check_block(b);
+    if (st != SPEC_OK) return st;
+    *bytes = block_norm_grad_workspace_bytes(b);
+    return SPEC_OK;
+}
+
+int spec_block_norm_grad(void *stream, const spec_block *b, const void *Y, int64_t ldy, const spec_mx *y8,
+                         const void *Hout, int64_t ldo, const spec_mx *h8, const float *r_post, const float *r_pre,
+                         const void *dHout, int64_t lddo, const void *dX, int64_t lddx, void *dH, int64_t lddh, void *dY,
+                         int64_t lddy, float *dw_post, float *dw_pre, float *dgate, void *ws, size_t ws_bytes)
+{
+    int st = check_block(b);
+    if (st != SPEC_OK) return st;
+    const bool some = b->n > 0;
+    if (!block_matrix(b, Y, ldy) || !block_matrix(b, Hout, ldo) || !block_matrix(b, dHout, lddo) ||
+        !block_matrix(b, dX, lddx) || !block_matrix(b, dH, lddh) || !block_matrix(b, dY, lddy))
+        return SPEC_EINVAL;
+    st = check_stored(y8, b->n, b->d);
+    if (st != SPEC_OK) return st;
+    st = check_stored(h8, b->n, b->d);
+    if (st != SPEC_OK) return st;
+    const bool hasY = Y != nullptr || y8 != nullptr;
+    if (some && !hasY && (dY != nullptr || dw_post != nullptr || dgate != nullptr)) return SPEC_EINVAL;
+    if (some && dX != nullptr && ((Hout == nullptr && h8 == nullptr) || r_pre == nullptr)) return SPEC_EINVAL;
+    if (some && dX == nullptr && dw_pre != nullptr) return SPEC_EINVAL;
+    if (some && hasY && b->post != 0 && r_post == nullptr) return SPEC_EINVAL;
+    if ((b->post == 0 && dw_post != nullptr) || (b->gate == nullptr && dgate != nullptr)) return SPEC_EINVAL;
+    for (const float *p : {r_post, r_pre, (const float *)dw_post, (const float *)dw_pre, (const float *)dgate})
+        if (!aligned(p, 4)) return SPEC_EINVAL;
+    if (ws == nullptr || ws_bytes < block_norm_grad_workspace_bytes(b)) return SPEC_EWORKSPACE;
+    if (!aligned(ws, 256)) return SPEC_EINVAL;
+    return from_hip(launch_block_norm_grad((hipStream_t)stream, b, Y, ldy, y8, Hout, ldo, h8, r_post, r_pre, dHout, lddo,
+                                           dX, lddx, dH, lddh, dY, lddy, dw_post, dw_pre, dgate, ws));
 }
 
 }  // extern "C"

@@ -108,6 +108,40 @@ hipError_t launch_orthogonalize(hipStream_t stream, const void *G, int t, int64_
                                 int64_t ldg, int64_t sg, const double *coeffs, int steps, double eps, double scale,
                                 void *O, int64_t ldo, int64_t so, void *ws);
 
+hipError_t launch_mx_quantize(hipStream_t stream, const void *X, int t, int64_t rows, int64_t cols, int64_t ldx,
+                              const spec_mx *out);
+
+// width: columns written, from cols to whole blocks (zeros past cols)
+hipError_t launch_mx_dequantize(hipStream_t stream, const spec_mx *in, int64_t rows, int64_t cols, int64_t width, void *X,
+                                int t, int64_t ldx);
+
+size_t mx_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int t);
+size_t mx_product_workspace_bytes(int64_t T, int64_t N, int64_t K);
+size_t mx_weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, int t);
+
+hipError_t launch_mx_linear(hipStream_t stream, const void *X, int t, int64_t T, int64_t N, int64_t K, int64_t ldx,
+                            const spec_mx *W, void *Y, int64_t ldy, void *ws);
+
+hipError_t launch_mx_product(hipStream_t stream, const spec_mx *X, const spec_mx *W, int64_t T, int64_t N, int64_t K,
+                             void *Y, int yt, int64_t ldy, void *ws);
+
+hipError_t launch_mx_weight_grad(hipStream_t stream, const void *dY, int t, int64_t T, int64_t N, int64_t K, int64_t ldy,
+                                 const spec_mx *X, float beta, void *dW, int64_t lddw, void *ws);
+
+// features of a row that the norms' kernels hold
+constexpr int64_t BLOCK_MAX_D = 16384;
+
+hipError_t launch_block_norm(hipStream_t stream, const spec_block *b, const void *Y, int64_t ldy, const void *H,
+                             int64_t ldh, void *O, int64_t ldo, void *X, int64_t ldx, float *r1, float *r2,
+                             const spec_mx *yq, const spec_mx *oq, const spec_mx *xq);
+
+size_t block_norm_grad_workspace_bytes(const spec_block *b);
+
+hipError_t launch_block_norm_grad(hipStream_t stream, const spec_block *b, const void *Y, int64_t ldy, const spec_mx *yq,
+                                  const void *O, int64_t ldo, const spec_mx *oq, const float *r1, const float *r2,
+                                  const void *dO, int64_t lddo, const void *dX, int64_t lddx, void *dH, int64_t lddh,
+                                  void *dY, int64_t lddy, float *dw1, float *dw2, float *dgate, void *ws);
+
 // Kernel timing brackets (timing.cpp): ktimer_begin returns a slot (or -1 when
 // the kernel is not being timed); ktimer_end records the matching end event.
 int ktimer_begin(hipStream_t stream, int id);
