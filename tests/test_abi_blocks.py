@@ -95,7 +95,7 @@ def test_linear_validation(L):
         assert f(*_with(ok, W=_mx(**mx))) == EINVAL, mx
     for bad in (dict(t=spec.F64), dict(W=_mx(fmt=spec.MX_INT8)), dict(W=_mx(fmt=7))):
         assert f(*_with(ok, **bad)) == EUNSUPPORTED, bad
-    for bad in (dict(ws=None), dict(ws_bytes=1000)):
+    for bad in (dict(ws=None), dict(ws_bytes=100)):
         assert f(*_with(ok, **bad)) == EWORKSPACE, bad
     assert f(*_with(ok, T=0, X=None, Y=None)) == 0
 

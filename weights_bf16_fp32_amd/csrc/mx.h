@@ -185,16 +185,31 @@ SPEC_DEVICE void mx_decode_int8(uint2 q, int b, float (&v)[8])
     }
 }
 
-SPEC_DEVICE void mx_decode_fp4(uint32_t q, int b, float (&v)[8])
+// The conversions from FP4 take b as the exponent bits of an f32: bytes 0 (2^-127) to
+// 254 and NaN for 255, exact as far as f32 (bf16) holds the values.
+SPEC_DEVICE float mx_factor(int b) { return __int_as_float(b << 23); }
+
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+SPEC_DEVICE void mx_decode_fp4(uint32_t q, float f, float (&v)[8])
 {
-    typedef float f32x2_t __attribute__((ext_vector_type(2)));
     f32x2_t p[4];
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, f, 0);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, f, 1);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, f, 2);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, f, 3);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = b == MX_NAN ? __builtin_nanf("") : __builtin_ldexpf(p[e >> 1][e & 1], b - 127);
+    for (int e = 0; e < 8; ++e) v[e] = p[e >> 1][e & 1];
+}
+
+// the same as eight bf16
+SPEC_DEVICE bf16x8_t mx_decode_fp4_bf16(uint32_t q, float f)
+{
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 1);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, f, 3);
+    return __builtin_shufflevector(__builtin_shufflevector(a, b, 0, 1, 2, 3), __builtin_shufflevector(c, d, 0, 1, 2, 3), 0, 1, 2,
+                                   3, 4, 5, 6, 7);
 }
 
 // values exact in type E (eight bits or fewer) without rounding: bf16 takes the upper halves

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t *__restrict
             if constexpr (FMT == SPEC_MX_INT8)
                 mx_decode_int8(q[u], b[u], v);
             else
-                mx_decode_fp4(q[u].x, b[u], v);
+                mx_decode_fp4(q[u].x, mx_factor(b[u]), v);
             if (c * 8 < width) store8<E>(X + r * ldx, c * 8, width, mx_raw<E>(v));
         }
     }
