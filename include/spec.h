@@ -725,7 +725,7 @@ int spec_block_norm(void *stream, const spec_block *b, const void *Y, int64_t ld
                     void *Hout, int64_t ldo, void *X, int64_t ldx, float *r_post, float *r_pre, const spec_mx *y8,
                     const spec_mx *h8, const spec_mx *x8);
 
-/* Its gradients, from dX and what reaches Hout otherwise, dHout (either may be NULL: zero):
+/* Its gradients, from dX and what reaches Hout otherwise, dHout (one of them may be NULL: zero):
  *   a = dX w_pre,  n2 = Hout r_pre,  G = dHout + r_pre (a - n2 mean(a n2)),  dH = alpha G
  *   n1 = Y r_post,  c = beta gate w_post G,  dY = r_post (c - n1 mean(c n1))     (post == 0: n1 = Y, dY = c)
  *   dw_pre = sum dX n2,  dw_post = sum beta gate G n1,  dgate = sum over the gate row's rows of beta w_post G n1

@@ -715,7 +715,7 @@ int spec_block_norm_grad(void *stream, const spec_block *b, const void *Y, int64
     const bool hasY = Y != nullptr || y8 != nullptr;
     if (some && !hasY && (dY != nullptr || dw_post != nullptr || dgate != nullptr)) return SPEC_EINVAL;
     if (some && dX != nullptr && ((Hout == nullptr && h8 == nullptr) || r_pre == nullptr)) return SPEC_EINVAL;
-    if (some && dX == nullptr && dw_pre != nullptr) return SPEC_EINVAL;
+    if (some && dX == nullptr && (dw_pre != nullptr || dHout == nullptr)) return SPEC_EINVAL;
     if (some && hasY && b->post != 0 && r_post == nullptr) return SPEC_EINVAL;
     if ((b->post == 0 && dw_post != nullptr) || (b->gate == nullptr && dgate != nullptr)) return SPEC_EINVAL;
     for (const float *p : {r_post, r_pre, (const float *)dw_post, (const float *)dw_pre, (const float *)dgate})

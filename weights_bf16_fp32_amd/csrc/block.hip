@@ -30,18 +30,41 @@ namespace {
 inline int64_t cdiv_h(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up_h(int64_t a, int64_t b) { return cdiv_h(a, b) * b; }
 
-// TPR threads hold a row, CH eights each: eight e of a thread lies at 8 (e TPR + thread).
-// Rows of up to 1024 take one wave (four rows to a workgroup).
-template <int TPR_, int CH_>
+// TPR threads hold a row, CH eights each: eight i of a thread lies at 8 (i TPR + thread).
+// Rows of one wave go four to a workgroup.
+// Rows of fewer than eight are TINY.
+template <int TPR_, int CH_, bool TINY_ = false>
 struct RowShape {
     static constexpr int TPR = TPR_, CH = CH_;
-    static constexpr int NT = TPR < 256 ? 256 : TPR;
+    static constexpr bool TINY = TINY_;
+    static constexpr int NT = TPR == 64 ? 256 : TPR;
     static constexpr int ROWS = NT / TPR;  // workers per workgroup
+    // this thread's eight i of a row: loaded, and then its elements in their places
+    template <typename E>
+    static SPEC_DEVICE Raw8<E> start(const typename E::st *row, int i, int d)
+    {
+        if constexpr (TINY) return load8_tiny<E>(row, at(i), d);
+        else return load8_start<E>(row, at(i), d);
+    }
+    template <typename E>
+    static SPEC_DEVICE void end(Raw8<E> &r, int i, int d)
+    {
+        if constexpr (!TINY) load8_end<E>(r, at(i), d);
+    }
+    static SPEC_DEVICE int at(int i) { return 8 * (i * TPR + thread()); }
+    static SPEC_DEVICE int thread() { return ROWS > 1 ? threadIdx.x % TPR : threadIdx.x; }
+    // the same in a wave, and known to be: its rows' addresses are scalars
+    static SPEC_DEVICE int64_t worker()
+    {
+        return ROWS > 1 ? (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR) : (int64_t)blockIdx.x;
+    }
 };
 
+// the forward's
 template <typename F>
-inline hipError_t pick_shape(int64_t d, F &&f)
+inline hipError_t pick_norm(int64_t d, F &&f)
 {
+    if (d < 8) return f(RowShape<64, 1, true>{});
     if (d <= 512) return f(RowShape<64, 1>{});
     if (d <= 1024) return f(RowShape<64, 2>{});
     if (d <= 2048) return f(RowShape<256, 1>{});
@@ -50,43 +73,58 @@ inline hipError_t pick_shape(int64_t d, F &&f)
     return f(RowShape<1024, 2>{});
 }
 
-// N sums over the threads of a row.  slot: LDS of two alternating places, so that one
-// barrier per call suffices.
+// The gradients': one eight per thread as far as a workgroup goes: the sums then fit 128
+// registers and the row's loads wait behind other waves' work.
+template <typename F>
+inline hipError_t pick_grad(int64_t d, F &&f)
+{
+    if (d < 8) return f(RowShape<64, 1, true>{});
+    if (d <= 512) return f(RowShape<64, 1>{});
+    if (d <= 1024) return f(RowShape<128, 1>{});
+    if (d <= 2048) return f(RowShape<256, 1>{});
+    if (d <= 4096) return f(RowShape<512, 1>{});
+    if (d <= 8192) return f(RowShape<1024, 1>{});
+    return f(RowShape<1024, 2>{});
+}
+
+// N sums over the threads of a row, the same in all of them.  LDS has two alternating
+// places, so that one barrier per call suffices.
 template <typename SH, int N>
 struct RowSum {
     static constexpr int W = SH::TPR / 64;
-    float part[2][W > 1 ? W : 1][N];
+    float4 part[2][W > 1 ? W : 1];
     SPEC_DEVICE void operator()(float (&v)[N], int turn)
     {
+        static_assert(N <= 4 && W <= 16, "a float4 per wave");
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+        for (int i = 0; i < N; ++i) v[i] = wave_sum<64>(v[i]);
         if constexpr (W > 1) {
-            const int wave = threadIdx.x >> 6;
-            if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) part[turn & 1][wave][i] = v[i];
-            }
+            const int lane = threadIdx.x & 63;
+            if (lane == 0) part[turn & 1][threadIdx.x >> 6] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f, 0.f);
             __syncthreads();
+            const float4 p = part[turn & 1][lane % W];  // every W lanes hold all waves' sums
+            const float o[3] = {p.x, p.y, p.z};
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                v[i] = part[turn & 1][0][i];
-#pragma unroll
-                for (int w = 1; w < W; ++w) v[i] += part[turn & 1][w][i];
-            }
+            for (int i = 0; i < N; ++i) v[i] = wave_sum<W>(o[i]);
         }
     }
+    // over each 2, 4, 8, 16 or all 64 lanes
+    template <int L>
     static SPEC_DEVICE float wave_sum(float x)
     {
         x += dpp<0xB1>(x);
-        x += dpp<0x4E>(x);
-        x += dpp<0x141>(x);
-        x += dpp<0x140>(x);
-        float y = x;
-        rowswap16(x, y);
-        x += y;
-        y = x;
-        halfswap32(x, y);
-        return x + y;
+        if (L >= 4) x += dpp<0x4E>(x);
+        if (L >= 8) x += dpp<0x141>(x);
+        if (L >= 16) x += dpp<0x140>(x);
+        if (L >= 64) {
+            float y = x;
+            rowswap16(x, y);
+            x += y;
+            y = x;
+            halfswap32(x, y);
+            x += y;
+        }
+        return x;
     }
 };
 
@@ -141,101 +179,103 @@ SPEC_DEVICE void put_stored_end(const Stored &o, int64_t row, int thread, int64_
     if (thread < scales - blocks) o.s[row * o.lds + blocks + thread] = 0;
 }
 
-template <typename E>
-SPEC_DEVICE Raw8<E> load_or_ones(const void *w, int64_t c, int64_t d)
+// a weight's or a gate row's eight i, ones where there is none
+template <typename E, typename SH>
+SPEC_DEVICE Raw8<E> load_or_ones(const void *w, int i, int d)
 {
-    if (w != nullptr) return load8<E>((const typename E::st *)w, c, d);
     Raw8<E> r;
-    float v[8];
+    if (w != nullptr) {
+        r = SH::template start<E>((const typename E::st *)w, i, d);
+        SH::template end<E>(r, i, d);
+    } else {
+        float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 1.f;
-    r.set(v);
+        for (int e = 0; e < 8; ++e) v[e] = 1.f;
+        r.set(v);
+    }
     return r;
 }
 
 // worker w of `workers` takes rows w, w + workers, ...
+// (Where there is no block, Y is H with beta = 0.)
 template <typename E, typename SH>
-__global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typename E::st *__restrict__ Y, int64_t ldy,
-                                                       const typename E::st *__restrict__ H, int64_t ldh,
-                                                       typename E::st *__restrict__ O, int64_t ldo,
-                                                       typename E::st *__restrict__ X, int64_t ldx,
-                                                       float *__restrict__ r1, float *__restrict__ r2, Stored yq,
-                                                       Stored oq, Stored xq, int64_t workers)
+__global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typename E::st *Y, int64_t ldy,
+                                                       const typename E::st *H, int64_t ldh, typename E::st *O, int64_t ldo,
+                                                       typename E::st *X, int64_t ldx, float *__restrict__ r1,
+                                                       float *__restrict__ r2, Stored yq, Stored oq, Stored xq,
+                                                       int64_t workers)
 {
-    constexpr int TPR = SH::TPR, CH = SH::CH;
+    constexpr int CH = SH::CH;
     __shared__ RowSum<SH, 1> sum;
-    const int thread = threadIdx.x % TPR;
-    const int64_t w = (int64_t)blockIdx.x * SH::ROWS + threadIdx.x / TPR;
-    Raw8<E> w1[CH], w2[CH], gt[CH];
+    const int thread = SH::thread(), d = (int)a.d;
+    const int64_t w = SH::worker();
+    Raw8<E> w1[CH], w2[CH], gt[CH], ny[CH], nh[CH];
+    const auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            ny[i] = SH::template start<E>(Y + row * ldy, i, d);
+            nh[i] = SH::template start<E>(H + row * ldh, i, d);
+        }
+    };
+    if (w < a.n) fetch(w);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int64_t c = 8 * (int64_t)(i * TPR + thread);
-        w1[i] = load_or_ones<E>(a.w1, c, a.d);
-        w2[i] = load_or_ones<E>(a.w2, c, a.d);
-        gt[i] = load_or_ones<E>(nullptr, c, a.d);
+        w1[i] = load_or_ones<E, SH>(a.w1, i, d);
+        w2[i] = load_or_ones<E, SH>(a.w2, i, d);
+        gt[i] = load_or_ones<E, SH>(nullptr, i, d);
     }
     int64_t gate_at = -1;
     int turn = 0;
     for (int64_t row = w; row < a.n; row += workers) {
         Raw8<E> y[CH], h[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int64_t c = 8 * (int64_t)(i * TPR + thread);
-            if (Y != nullptr) y[i] = load8<E>(Y + row * ldy, c, a.d);
-            h[i] = load8<E>(H + row * ldh, c, a.d);
-        }
+        for (int i = 0; i < CH; ++i) y[i] = ny[i], h[i] = nh[i];
+        if (row + workers < a.n) fetch(row + workers);
         if (a.gate != nullptr && row / a.gate_rows != gate_at) {
             gate_at = row / a.gate_rows;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                gt[i] = load8<E>((const typename E::st *)a.gate + gate_at * a.ldg, 8 * (int64_t)(i * TPR + thread), a.d);
+            for (int i = 0; i < CH; ++i) gt[i] = load_or_ones<E, SH>((const typename E::st *)a.gate + gate_at * a.ldg, i, d);
         }
         float v[8 * CH];
-        if (Y != nullptr) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+        for (int i = 0; i < CH; ++i) {
+            SH::template end<E>(y[i], i, d);
+            SH::template end<E>(h[i], i, d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * i + e] = y[i].get(e);
-            float r = 1.f;
-            if (a.post) {
-                r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
-                if (r1 != nullptr && thread == 0) r1[row] = r;
+            for (int e = 0; e < 8; ++e) v[8 * i + e] = y[i].get(e);
+        }
+        float r = 1.f;
+        if (a.post) {
+            r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
+            if (r1 != nullptr && thread == 0) r1[row] = r;
+        }
+        if (yq.q != nullptr) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) put_stored<E>(yq, row, i * SH::TPR + thread, a.d, y[i]);
+            put_stored_end(yq, row, thread, a.d);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float u = v[8 * i + e] * r * w1[i].get(e) * gt[i].get(e);
+                v[8 * i + e] = __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
             }
-            if (yq.q != nullptr) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) put_stored<E>(yq, row, i * TPR + thread, a.d, y[i]);
-                put_stored_end(yq, row, thread, a.d);
-            }
+        if (O != nullptr || oq.q != nullptr) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
+                Raw8<E> o;
+                float t[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = v[8 * i + e] * r * w1[i].get(e) * gt[i].get(e);
-                    v[8 * i + e] = __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
-                }
+                for (int e = 0; e < 8; ++e) t[e] = v[8 * i + e];
+                o.set(t);
+                if (O != nullptr && SH::at(i) < d) store8<E>(O + row * ldo, SH::at(i), a.d, o);
+                if (oq.q != nullptr) put_stored<E>(oq, row, i * SH::TPR + thread, a.d, o);
             }
-            if (O != nullptr || oq.q != nullptr) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    Raw8<E> o;
-                    float t[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[e] = v[8 * i + e];
-                    o.set(t);
-                    const int64_t c = i * TPR + thread;
-                    if (O != nullptr && 8 * c < a.d) store8<E>(O + row * ldo, 8 * c, a.d, o);
-                    if (oq.q != nullptr) put_stored<E>(oq, row, c, a.d, o);
-                }
-                if (oq.q != nullptr) put_stored_end(oq, row, thread, a.d);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * i + e] = h[i].get(e);
+            if (oq.q != nullptr) put_stored_end(oq, row, thread, a.d);
         }
         if (X != nullptr || xq.q != nullptr || r2 != nullptr) {
-            const float r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
+            r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
             if (r2 != nullptr && thread == 0) r2[row] = r;
             if (X != nullptr || xq.q != nullptr) {
 #pragma unroll
@@ -245,9 +285,8 @@ __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typena
 #pragma unroll
                     for (int e = 0; e < 8; ++e) t[e] = v[8 * i + e] * r * w2[i].get(e);
                     o.set(t);
-                    const int64_t c = i * TPR + thread;
-                    if (X != nullptr && 8 * c < a.d) store8<E>(X + row * ldx, 8 * c, a.d, o);
-                    if (xq.q != nullptr) put_stored<E>(xq, row, c, a.d, o);
+                    if (X != nullptr && SH::at(i) < d) store8<E>(X + row * ldx, SH::at(i), a.d, o);
+                    if (xq.q != nullptr) put_stored<E>(xq, row, i * SH::TPR + thread, a.d, o);
                 }
                 if (xq.q != nullptr) put_stored_end(xq, row, thread, a.d);
             }
@@ -280,34 +319,80 @@ struct GradIo {
     void *dH, *dY;
     int64_t lddh, lddy;
     float *dgate;
+    // all bits, or none where the matrix is not there (its place is taken by another)
+    uint32_t keepY, keepX, keepO;
 };
 
-// an eight of a row from the matrix itself or from its checkpoint
+// An eight of a row from the matrix itself, or from its checkpoint (codes in w[0] and
+// w[1], the scale in w[2]; past the row's codes those of its last eight).
+template <typename E, typename SH>
+SPEC_DEVICE Raw8<E> fetch8(const void *X, int64_t ld, const Stored &st, int64_t row, int i, int d)
+{
+    if (st.q == nullptr) return SH::template start<E>((const typename E::st *)X + row * ld, i, d);
+    Raw8<E> r;
+    const int c = min(SH::at(i) / 8, (d - 1) / 8);
+    const uint2 q = *reinterpret_cast<const uint2 *>(st.q + row * st.ldq + c * 8);
+    r.w[0] = q.x, r.w[1] = q.y, r.w[2] = st.s[row * st.lds + (c >> 2)], r.w[3] = 0;
+    return r;
+}
+
 template <typename E>
-struct Eight {
-    Raw8<E> raw;
-    uint2 q;
-    int b;
-    SPEC_DEVICE void fetch(const void *X, int64_t ld, const Stored &st, int64_t row, int64_t c, int64_t d)
+SPEC_DEVICE void values8(const Raw8<E> &r, const Stored &st, float (&v)[8])
+{
+    if (st.q != nullptr) {
+        mx_decode_int8(r.w[0], r.w[1], mx_unit_int8((int)r.w[2]), v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = r.get(e);
+    }
+}
+
+// What was computed from r so far is not kept: it is formed again from these registers,
+// half as many as its values in f32 would hold.
+template <typename E>
+SPEC_DEVICE void forget(Raw8<E> &r)
+{
+#pragma unroll
+    for (int k = 0; k < Raw8<E>::N; ++k) asm volatile("" : "+v"(r.w[k]));
+}
+
+// one row of the gradients' inputs, zeros where there is none and past d
+template <typename E, typename SH>
+struct GradRow {
+    static constexpr int CH = SH::CH;
+    Raw8<E> y[CH], o[CH], dx[CH], dO[CH];
+    float r1, r2;
+    SPEC_DEVICE void fetch(const BlockArgs &a, const GradIo &io, int64_t row)
     {
-        if (st.q != nullptr) {
-            q = make_uint2(0, 0);
-            b = 0;
-            if (c * 8 < d) {
-                q = *reinterpret_cast<const uint2 *>(st.q + row * st.ldq + c * 8);
-                b = st.s[row * st.lds + (c >> 2)];
-            }
-        } else {
-            raw = load8<E>((const typename E::st *)X + row * ld, c * 8, d);
+        using st = typename E::st;
+        const int d = (int)a.d;
+        r1 = io.r1 != nullptr ? io.r1[row] : 1.f;
+        r2 = io.r2 != nullptr ? io.r2[row] : 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            dx[i] = SH::template start<E>((const st *)io.dX + row * io.lddx, i, d);
+            dO[i] = SH::template start<E>((const st *)io.dO + row * io.lddo, i, d);
+            o[i] = fetch8<E, SH>(io.O, io.ldo, io.oq, row, i, d);
+            y[i] = fetch8<E, SH>(io.Y, io.ldy, io.yq, row, i, d);
         }
     }
-    SPEC_DEVICE void values(const Stored &st, float (&v)[8]) const
+    SPEC_DEVICE void settle(const BlockArgs &a, const GradIo &io)
     {
-        if (st.q != nullptr) {
-            mx_decode_int8(q, b, v);
-        } else {
+        const int d = (int)a.d;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = raw.get(e);
+        for (int i = 0; i < CH; ++i) {
+            SH::template end<E>(dx[i], i, d);
+            SH::template end<E>(dO[i], i, d);
+            if (io.oq.q == nullptr) SH::template end<E>(o[i], i, d);
+            if (io.yq.q == nullptr) SH::template end<E>(y[i], i, d);
+            const bool in = SH::at(i) < d;
+#pragma unroll
+            for (int k = 0; k < Raw8<E>::N; ++k) {
+                dx[i].w[k] &= io.keepX;
+                dO[i].w[k] &= io.keepO;
+                o[i].w[k] = in ? o[i].w[k] & io.keepX : 0;
+                y[i].w[k] = in ? y[i].w[k] & io.keepY : 0;
+            }
         }
     }
 };
@@ -325,127 +410,140 @@ SPEC_DEVICE void put_sums(float *__restrict__ row, const float (&v)[8 * CH], int
     }
 }
 
+// The registers of a workgroup of 512 threads: 128 let two of them share a CU (bf16;
+// f32 inputs alone are twice as many).
+template <typename E, typename SH>
+constexpr int grad_waves() { return sizeof(typename E::st) == 2 && SH::TPR == 512 ? 4 : 1; }
+
 template <typename E, typename SH, bool MANY>
-__global__ __launch_bounds__(SH::NT) void k_block_grad(BlockArgs a, GradIo io, GradPart part)
+__global__ __launch_bounds__(SH::NT, (grad_waves<E, SH>())) void k_block_grad(BlockArgs a, GradIo io, GradPart part)
 {
+    using st = typename E::st;
     constexpr int TPR = SH::TPR, CH = SH::CH;
+    // Rows of two eights per thread leave no room for the weights and the next row.
+    constexpr bool KEEP = CH == 1;
     __shared__ RowSum<SH, 3> sum;
-    const int thread = threadIdx.x % TPR;
-    const int64_t worker = (int64_t)blockIdx.x * SH::ROWS + threadIdx.x / TPR;
+    const int thread = SH::thread();
+    const int64_t worker = SH::worker();
     if (worker >= part.deal.workers) return;  // a whole row's threads
     const int64_t run = part.deal.run, share = part.deal.share;
+    const int d = (int)a.d;
     const int64_t r0 = MANY ? worker * run : worker / share * a.gate_rows + worker % share * run;
     const int64_t r1 = min(a.n, MANY ? r0 + run : min(r0 + run, (worker / share + 1) * a.gate_rows));
-    const bool hasY = io.Y != nullptr || io.yq.q != nullptr, hasX = io.dX != nullptr;
-    Raw8<E> w1[CH], w2[CH], gt[CH];
+    const auto at = [&](int i) { return SH::at(i); };
+    int64_t gate_at = -1;
+    const auto gate_row = [&](int i) {
+        return load_or_ones<E, SH>(a.gate != nullptr && gate_at >= 0 ? (const st *)a.gate + gate_at * a.ldg : nullptr, i, d);
+    };
+    Raw8<E> k1[KEEP ? CH : 1], k2[KEEP ? CH : 1], kg[KEEP ? CH : 1];
     float sw2[8 * CH], ss[8 * CH], sw1[8 * CH];
+    if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int64_t c = 8 * (int64_t)(i * TPR + thread);
-        w1[i] = load_or_ones<E>(a.w1, c, a.d);
-        w2[i] = load_or_ones<E>(a.w2, c, a.d);
-        gt[i] = load_or_ones<E>(nullptr, c, a.d);
+        for (int i = 0; i < CH; ++i) {
+            k1[i] = load_or_ones<E, SH>(a.w1, i, d);
+            k2[i] = load_or_ones<E, SH>(a.w2, i, d);
+            kg[i] = gate_row(i);
+        }
     }
+    // the weights and the gate row's, packed (not kept as values in f32 from row to row)
+    const auto w1_of = [&](int i) { if constexpr (KEEP) { forget(k1[i]); return k1[i]; } else return load_or_ones<E, SH>(a.w1, i, d); };
+    const auto w2_of = [&](int i) { if constexpr (KEEP) { forget(k2[i]); return k2[i]; } else return load_or_ones<E, SH>(a.w2, i, d); };
+    const auto gt_of = [&](int i) { if constexpr (KEEP) { forget(kg[i]); return kg[i]; } else return gate_row(i); };
 #pragma unroll
     for (int i = 0; i < 8 * CH; ++i) sw2[i] = ss[i] = sw1[i] = 0.f;
-    int64_t gate_at = -1;
     // the sums of gate row gate_at, which are complete: into dw1, and out
     const auto flush = [&]() {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int64_t c = 8 * (int64_t)(i * TPR + thread);
+            const Raw8<E> w1 = w1_of(i), gt = gt_of(i);
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float &s = ss[8 * i + e];
-                sw1[8 * i + e] = __builtin_fmaf(gt[i].get(e), s, sw1[8 * i + e]);
-                t[e] = w1[i].get(e) * s;
+                sw1[8 * i + e] = __builtin_fmaf(gt.get(e), s, sw1[8 * i + e]);
+                t[e] = w1.get(e) * s;
                 s = 0.f;
             }
             Raw8<ElF32> o;
             o.set(t);
-            if (io.dgate != nullptr && c < a.d) store8<ElF32>(io.dgate + gate_at * a.d, c, a.d, o);
+            if (io.dgate != nullptr && at(i) < a.d) store8<ElF32>(io.dgate + gate_at * a.d, at(i), a.d, o);
         }
     };
     int turn = 0;
+    GradRow<E, SH> next;
+    if (KEEP && r0 < r1) next.fetch(a, io, r0);
     for (int64_t row = r0; row < r1; ++row) {
-        Eight<E> y[CH], o[CH];
-        Raw8<E> dx[CH], dO[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int64_t c = i * TPR + thread;
-            if (hasX) {
-                o[i].fetch(io.O, io.ldo, io.oq, row, c, a.d);
-                dx[i] = load8<E>((const typename E::st *)io.dX + row * io.lddx, 8 * c, a.d);
-            }
-            if (io.dO != nullptr) dO[i] = load8<E>((const typename E::st *)io.dO + row * io.lddo, 8 * c, a.d);
-            if (hasY) y[i].fetch(io.Y, io.ldy, io.yq, row, c, a.d);
+        GradRow<E, SH> in;
+        if constexpr (KEEP) {
+            in = next;
+            if (row + 1 < r1) next.fetch(a, io, row + 1);
+        } else {
+            in.fetch(a, io, row);
         }
         if (a.gate != nullptr && row / a.gate_rows != gate_at) {
             if (MANY && gate_at >= 0) flush();
             gate_at = row / a.gate_rows;
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                gt[i] = load8<E>((const typename E::st *)a.gate + gate_at * a.ldg, 8 * (int64_t)(i * TPR + thread), a.d);
+                for (int i = 0; i < CH; ++i) kg[i] = gate_row(i);
+            }
         }
-        const float rho1 = hasY && a.post ? io.r1[row] : 1.f, rho2 = hasX ? io.r2[row] : 0.f;
-        // n2, n1, and base = dh' + r2 a of which the means take their part away
-        float n1[8 * CH], n2[8 * CH], base[8 * CH];
-        float t[3] = {0.f, 0.f, 0.f};  // sums of a n2, c base, c n2
+        in.settle(a, io);
+        const float rho1 = in.r1, rho2 = in.r2;
+        float t[3] = {0.f, 0.f, 0.f};  // sums of a n2, c base, c n2, with base = dh' + r2 a
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            const Raw8<E> w1 = w1_of(i), w2 = w2_of(i), gt = gt_of(i);
             float vo[8], vy[8];
-            if (hasX) o[i].values(io.oq, vo);
-            if (hasY) y[i].values(io.yq, vy);
+            values8<E>(in.o[i], io.oq, vo);
+            values8<E>(in.y[i], io.yq, vy);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int j = 8 * i + e;
-                base[j] = io.dO != nullptr ? dO[i].get(e) : 0.f;
-                n2[j] = 0.f;
-                n1[j] = hasY ? vy[e] * rho1 : 0.f;
-                if (hasX) {
-                    const float g = dx[i].get(e), aw = g * w2[i].get(e);
-                    n2[j] = vo[e] * rho2;
-                    sw2[j] = __builtin_fmaf(g, n2[j], sw2[j]);
-                    t[0] = __builtin_fmaf(aw, n2[j], t[0]);
-                    base[j] = __builtin_fmaf(rho2, aw, base[j]);
-                }
-                const float c = gt[i].get(e) * w1[i].get(e) * n1[j];
-                t[1] = __builtin_fmaf(c, base[j], t[1]);
-                t[2] = __builtin_fmaf(c, n2[j], t[2]);
+                const float g = in.dx[i].get(e), aw = g * w2.get(e);
+                const float n1 = vy[e] * rho1, n2 = vo[e] * rho2;
+                sw2[8 * i + e] = __builtin_fmaf(g, n2, sw2[8 * i + e]);
+                const float c = gt.get(e) * w1.get(e) * n1;
+                t[0] = __builtin_fmaf(aw, n2, t[0]);
+                t[1] = __builtin_fmaf(c, __builtin_fmaf(rho2, aw, in.dO[i].get(e)), t[1]);
+                t[2] = __builtin_fmaf(c, n2, t[2]);
             }
         }
         sum(t, turn++);
-        const float m = t[0] * a.inv_d, k2 = rho2 * m;
-        const float mb = a.post ? a.beta * a.inv_d * (t[1] - k2 * t[2]) : 0.f;
+        const float m = t[0] * a.inv_d, rm = rho2 * m;
+        const float mb = a.post ? a.beta * a.inv_d * (t[1] - rm * t[2]) : 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int64_t c = 8 * (int64_t)(i * TPR + thread);
-            float dh[8], dy[8];
+            forget(in.y[i]), forget(in.o[i]), forget(in.dx[i]), forget(in.dO[i]);
+            const Raw8<E> w1 = w1_of(i), w2 = w2_of(i), gt = gt_of(i);
+            float vo[8], vy[8], dh[8], dy[8];
+            values8<E>(in.o[i], io.oq, vo);
+            values8<E>(in.y[i], io.yq, vy);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int j = 8 * i + e;
-                const float G = __builtin_fmaf(-k2, n2[j], base[j]);
+                const float n1 = vy[e] * rho1, n2 = vo[e] * rho2;
+                const float base = __builtin_fmaf(rho2, in.dx[i].get(e) * w2.get(e), in.dO[i].get(e));
+                const float G = __builtin_fmaf(-rm, n2, base);
                 dh[e] = a.alpha * G;
                 const float bG = a.beta * G;
-                ss[j] = __builtin_fmaf(bG, n1[j], ss[j]);
-                dy[e] = rho1 * __builtin_fmaf(-mb, n1[j], bG * gt[i].get(e) * w1[i].get(e));
+                ss[8 * i + e] = __builtin_fmaf(bG, n1, ss[8 * i + e]);
+                dy[e] = rho1 * __builtin_fmaf(-mb, n1, bG * gt.get(e) * w1.get(e));
             }
-            if (c < a.d) {
+            const int c = at(i);
+            if (c < d) {
                 Raw8<E> r;
                 if (io.dH != nullptr) {
                     r.set(dh);
-                    store8<E>((typename E::st *)io.dH + row * io.lddh, c, a.d, r);
+                    store8<E>((st *)io.dH + row * io.lddh, c, a.d, r);
                 }
                 if (io.dY != nullptr) {
                     r.set(dy);
-                    store8<E>((typename E::st *)io.dY + row * io.lddy, c, a.d, r);
+                    store8<E>((st *)io.dY + row * io.lddy, c, a.d, r);
                 }
             }
         }
     }
-    if (hasX) put_sums<CH>(part.dw2 + worker * part.ld, sw2, TPR, thread, part.ld);
-    if (hasY) {
+    if (io.keepX) put_sums<CH>(part.dw2 + worker * part.ld, sw2, TPR, thread, part.ld);
+    if (io.keepY) {
         if (MANY) flush();
         put_sums<CH>(part.rest + worker * part.ld, MANY ? sw1 : ss, TPR, thread, part.ld);
     }
@@ -529,7 +627,7 @@ Stored stored(const spec_mx *m)
 // 512 workgroups of a run each where the rows suffice: every one leaves two rows of f32 sums.
 GradDeal grad_deal(int64_t n, int64_t d, int64_t gate_rows, bool gate)
 {
-    const int64_t per = d <= 1024 ? 4 : 1;  // workers to a workgroup (RowShape::ROWS)
+    const int64_t per = d <= 512 ? 4 : 1;  // workers to a workgroup (RowShape::ROWS)
     const int64_t run = std::max<int64_t>(1, cdiv_h(n, 512 * per));
     const int64_t rows = gate ? std::min(gate_rows, n) : n;
     GradDeal p{};
@@ -553,10 +651,15 @@ hipError_t block_norm(hipStream_t stream, const spec_block *b, const void *Y, in
                       const spec_mx *oq, const spec_mx *xq)
 {
     using st = typename E::st;
-    return pick_shape(b->d, [&](auto shape) {
+    BlockArgs a = block_args(b);
+    if (Y == nullptr) {  // h' = 1 h + 0 h
+        Y = H, ldy = ldh;
+        a.post = 0, a.w1 = a.gate = nullptr, a.alpha = 1.f, a.beta = 0.f;
+    }
+    return pick_norm(b->d, [&](auto shape) {
         using SH = decltype(shape);
         const int64_t grid = std::min<int64_t>(cdiv_h(b->n, SH::ROWS), 256 * 8 * 256 / SH::NT);
-        hipLaunchKernelGGL((k_block_norm<E, SH>), dim3((unsigned)grid), dim3(SH::NT), 0, stream, block_args(b),
+        hipLaunchKernelGGL((k_block_norm<E, SH>), dim3((unsigned)grid), dim3(SH::NT), 0, stream, a,
                            (const st *)Y, ldy, (const st *)H, ldh, (st *)O, ldo, (st *)X, ldx, r1, r2, stored(yq),
                            stored(oq), stored(xq), grid * SH::ROWS);
         return hipGetLastError();
@@ -566,10 +669,20 @@ hipError_t block_norm(hipStream_t stream, const spec_block *b, const void *Y, in
 template <typename E>
 hipError_t block_grad(hipStream_t stream, const spec_block *b, GradIo io, float *dw1, float *dw2, char *ws)
 {
-    const BlockArgs a = block_args(b);
+    BlockArgs a = block_args(b);
+    const bool hasY = io.Y != nullptr || io.yq.q != nullptr, hasX = io.dX != nullptr;
+    io.keepY = hasY ? ~0u : 0;
+    io.keepX = hasX ? ~0u : 0;
+    io.keepO = io.dO != nullptr ? ~0u : 0;
+    const void *any = hasX ? io.dX : io.dO;  // one of the two is there
+    const int64_t ldany = hasX ? io.lddx : io.lddo;
+    if (!hasX) io.dX = io.O = any, io.lddx = io.ldo = ldany, io.oq = Stored{}, io.r2 = nullptr;
+    if (!io.keepO) io.dO = any, io.lddo = ldany;
+    if (!hasY) io.Y = any, io.ldy = ldany, a.post = 0;
+    if (!a.post) io.r1 = nullptr;
     const GradDeal p = grad_deal(a.n, a.d, a.gate_rows, a.gate != nullptr);
     const GradPart part{(float *)ws, (float *)(ws + sums_bytes(p, a.d)), up_h(a.d, 8), p};
-    const hipError_t e = pick_shape(b->d, [&](auto shape) {
+    const hipError_t e = pick_grad(b->d, [&](auto shape) {
         using SH = decltype(shape);
         const dim3 grid((unsigned)cdiv_h(p.workers, SH::ROWS)), block(SH::NT);
         if (p.share == 0)
@@ -578,7 +691,6 @@ hipError_t block_grad(hipStream_t stream, const spec_block *b, GradIo io, float 
             hipLaunchKernelGGL((k_block_grad<E, SH, false>), grid, block, 0, stream, a, io, part);
         return hipGetLastError();
     });
-    const bool hasY = io.Y != nullptr || io.yq.q != nullptr, hasX = io.dX != nullptr;
     if (e != hipSuccess || !(hasX || hasY)) return e;
     const int64_t nc = cdiv_h(a.d, 32);
     const int64_t rows = !hasY || io.dgate == nullptr || p.share == 0 ? 0 : p.gates;

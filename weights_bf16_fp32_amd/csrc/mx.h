@@ -55,31 +55,72 @@ struct __attribute__((packed, aligned(alignof(S)))) Bytes16 {
     uint32_t w[4];
 };
 
-// elements c .. c + 7 of a row of d; those past d are zero
+// Elements c .. c + 7 of a row of d >= 8, those past d zero, in two parts.  The first
+// only loads, without a branch, so that the loads of several rows can be on their
+// way at once: where d ends before c + 8, the row's last eight.  The second, once
+// they are there, moves them to their places.
 template <typename E>
-SPEC_DEVICE Raw8<E> load8(const typename E::st *__restrict__ row, int64_t c, int64_t d)
+SPEC_DEVICE Raw8<E> load8_start(const typename E::st *__restrict__ row, int c, int d)
 {
-    using st = typename E::st;
     Raw8<E> r;
-    if (c + 8 <= d) {
+    const typename E::st *p = row + min(c, d - 8);
 #pragma unroll
-        for (int i = 0; i < Raw8<E>::N / 4; ++i) {
-            const Bytes16<st> b = reinterpret_cast<const Bytes16<st> *>(row + c)[i];
+    for (int i = 0; i < Raw8<E>::N / 4; ++i) {
+        const Bytes16<typename E::st> b = reinterpret_cast<const Bytes16<typename E::st> *>(p)[i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r.w[4 * i + j] = b.w[j];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < Raw8<E>::N; ++i) r.w[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < d) {
-                if constexpr (sizeof(st) == 4)
-                    r.w[e] = __float_as_uint(row[c + e]);
-                else
-                    r.w[e >> 1] |= (uint32_t)row[c + e] << 16 * (e & 1);
-            }
+        for (int j = 0; j < 4; ++j) r.w[4 * i + j] = b.w[j];
     }
+    return r;
+}
+
+template <typename E>
+SPEC_DEVICE void load8_end(Raw8<E> &r, int c, int d)
+{
+    constexpr int N = Raw8<E>::N, ONE = N / 4;  // words; words of two elements
+    const int by = c + 8 - d;
+    if (d % 8 != 0) {  // (the same in all lanes)
+        const int down = by > 0 ? by : 0;
+#pragma unroll
+        for (int k = 2; k >= 1; --k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t up = i + k * ONE < N ? r.w[i + k * ONE < N ? i + k * ONE : 0] : 0;
+                r.w[i] = down & 2 * k ? up : r.w[i];
+            }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t up = i + 1 < N ? r.w[i + 1 < N ? i + 1 : 0] : 0;
+            r.w[i] = !(down & 1) ? r.w[i] : N == 8 ? up : __builtin_amdgcn_alignbit(up, r.w[i], 16);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = by < 8 ? r.w[i] : 0;
+}
+
+// the same of a row of d < 8: element by element
+template <typename E>
+SPEC_DEVICE Raw8<E> load8_tiny(const typename E::st *__restrict__ row, int c, int d)
+{
+    Raw8<E> r;
+#pragma unroll
+    for (int i = 0; i < Raw8<E>::N; ++i) r.w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+        if (c != 0 || e >= d) continue;
+        if constexpr (Raw8<E>::N == 8)
+            r.w[e] = __float_as_uint(row[e]);
+        else
+            r.w[e >> 1] |= (uint32_t)row[e] << 16 * (e & 1);
+    }
+    return r;
+}
+
+template <typename E>
+SPEC_DEVICE Raw8<E> load8(const typename E::st *__restrict__ row, int c, int d)
+{
+    if (d < 8) return load8_tiny<E>(row, c, d);
+    Raw8<E> r = load8_start<E>(row, c, d);
+    load8_end<E>(r, c, d);
     return r;
 }
 
@@ -176,13 +217,16 @@ SPEC_DEVICE uint32_t mx_encode_fp4(const Raw8<E> &r, int b)
     return b == MX_NAN ? 0 : q;
 }
 
-SPEC_DEVICE void mx_decode_int8(uint2 q, int b, float (&v)[8])
+// 2^(b - 133), the worth of an INT8 code's unit; NaN for 255
+SPEC_DEVICE float mx_unit_int8(int b)
+{
+    return b == MX_NAN ? __builtin_nanf("") : __int_as_float(b >= 7 ? (b - 6) << 23 : 1 << (b + 16));
+}
+
+SPEC_DEVICE void mx_decode_int8(uint32_t q0, uint32_t q1, float unit, float (&v)[8])
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float i = (float)(int8_t)((e < 4 ? q.x : q.y) >> 8 * (e & 3));
-        v[e] = b == MX_NAN ? __builtin_nanf("") : __builtin_ldexpf(i, b - 133);
-    }
+    for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)((e < 4 ? q0 : q1) >> 8 * (e & 3)) * unit;
 }
 
 // The conversions from FP4 take b as the exponent bits of an f32: bytes 0 (2^-127) to

@@ -47,8 +47,16 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const typename E::st *__res
         if (r >= rows) continue;  // whole groups of four lanes
         const typename E::st *x = X + r * ldx;
         Raw8<E> v[UNITS];
+        const int e0 = (int)c0 * 8, d = (int)cols;
+        if (d >= 8) {
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) v[u] = load8<E>(x, (c0 + ((int64_t)u << lg)) * 8, cols);
+            for (int u = 0; u < UNITS; ++u) v[u] = load8_start<E>(x, e0 + (8 * u << lg), d);
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) load8_end<E>(v[u], e0 + (8 * u << lg), d);
+        } else {
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) v[u] = load8_tiny<E>(x, e0 + (8 * u << lg), d);
+        }
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
             const int64_t c = c0 + ((int64_t)u << lg);
@@ -99,7 +107,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t *__restrict
             const int64_t c = c0 + ((int64_t)u << lg);
             float v[8];
             if constexpr (FMT == SPEC_MX_INT8)
-                mx_decode_int8(q[u], b[u], v);
+                mx_decode_int8(q[u].x, q[u].y, mx_unit_int8(b[u]), v);
             else
                 mx_decode_fp4(q[u].x, mx_factor(b[u]), v);
             if (c * 8 < width) store8<E>(X + r * ldx, c * 8, width, mx_raw<E>(v));

@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void k_mx_pack(const typename E::st *__restric
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * eights; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / eights, e = 8 * (i % eights);
-        store8<E>(P + r * eights * 8, e, eights * 8, load8<E>(X + r * ldx, e, c));
+        store8<E>(P + r * eights * 8, e, eights * 8, load8<E>(X + r * ldx, (int)e, (int)c));
     }
 }
 
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_mx_few(const uint8_t *__rest
         sw[r] = SW + n * lds;
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) x[t] = X + min<int64_t>(16 * t + (lane & 15), T - 1) * ldx + 32 * g;
+    for (int t = 0; t < TT; ++t) x[t] = X + min<int64_t>(16 * t + (lane & 15), T - 1) * ldx;
     f32x4_t acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -313,8 +313,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_mx_few(const uint8_t *__rest
             for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t k = k0 + 128 * j + 8 * i;
-                    xv[t][i] = load8<E>(x[t], k, WHOLE ? k + 8 : K - 32 * g);
+                    const int k = (int)k0 + 128 * j + 8 * i + 32 * g;
+                    xv[t][i] = WHOLE ? load8_start<E>(x[t], k, k + 8) : load8<E>(x[t], k, (int)K);
                 }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
