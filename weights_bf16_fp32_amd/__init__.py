@@ -26,6 +26,7 @@ fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Any, NamedTuple
 
@@ -833,13 +834,61 @@ class Mx(NamedTuple):
     fmt: int
 
 
-def _here(t):
-    """The address of a tensor, which must be on the current device."""
+# The calls below are short on the GPU for a decode step, so their way there is kept
+# short too: sizes are looked at once, and what the call itself made not again.
+
+def _on(t):
+    """The device of a tensor, which must be the current one."""
     if not t.is_cuda:
         raise SpecError(-1, "tensor must be on the GPU")
-    if t.get_device() != _torch().cuda.current_device():
+    dev = t.get_device()
+    if dev != _torch()._C._cuda_getDevice():
         raise SpecError(-1, "tensor must be on the current device")
+    return dev
+
+
+def _at(t, dev):
+    """The address of a tensor, which must be on this device."""
+    if t.get_device() != dev:
+        raise SpecError(-1, "tensors must be on the current device")
     return t.data_ptr()
+
+
+def _mat(t, shape, dtype, dev):
+    """(address, row stride) of a matrix of this shape and type with contiguous rows."""
+    if t.shape != shape or t.dtype != dtype:
+        raise SpecError(-1, f"matrix must be {tuple(shape)} of {dtype}")
+    st = t.stride()
+    if st[1] != 1 and shape[1] != 1:
+        raise SpecError(-1, "matrices must have a contiguous inner dimension")
+    return _at(t, dev), st[0] if shape[0] > 1 else shape[1]
+
+
+def _shape(t):
+    if t.dim() != 2:
+        raise SpecError(-1, "matrices must be 2-D with a contiguous inner dimension")
+    return t.shape
+
+
+def _launch(f, dev, *args):
+    status = f(_torch()._C._cuda_getCurrentRawStream(dev), *args)
+    if status != 0:
+        _check(status)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(query, *sizes):
+    """Bytes of a workspace: a function of the sizes alone."""
+    return _bytes(getattr(lib(), query), *sizes)
+
+
+def _scratch(ws, size, dev):
+    """(address, bytes, the tensor itself, which has to live until the call returns)."""
+    if ws is None:
+        torch = _torch()
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), size, ws
+    return _at(ws, dev), ws.numel() * ws.element_size(), ws
 
 
 def _mx_rows(fmt, cols):
@@ -851,21 +900,22 @@ def _mx_rows(fmt, cols):
     return blocks * (32 if fmt == MX_INT8 else 16), (blocks + 15) // 16 * 16
 
 
-def _mx(m, rows=None, cols=None):
-    """The C descriptor of a microscaled matrix of these sizes."""
-    if not isinstance(m, Mx):
+def _mx(m, rows, cols, dev=None):
+    """The C descriptor of a microscaled matrix of these sizes (None: any)."""
+    if type(m) is not Mx:
         raise SpecError(-1, "a microscaled matrix (Mx) is needed")
-    torch = _torch()
-    q, s = m.q, m.s
-    if q.dtype != torch.uint8 or s.dtype != torch.uint8 or q.dim() != 2 or s.dim() != 2 or q.shape[0] != s.shape[0]:
+    u8, (q, s, c, fmt) = _torch().uint8, m
+    if q.dtype != u8 or s.dtype != u8 or q.dim() != 2 or s.dim() != 2:
         raise SpecError(-1, "codes and scales must be uint8 [rows, bytes]")
-    lq, ls = _mx_rows(m.fmt, m.cols)
-    if q.shape[1] < lq or s.shape[1] < ls or q.stride(1) != 1 or s.stride(1) != 1:
-        raise SpecError(-1, f"rows of {m.cols} columns are {lq} contiguous bytes of codes and {ls} of scales")
-    if (rows is not None and q.shape[0] != rows) or (cols is not None and m.cols != cols):
-        raise SpecError(-1, f"the microscaled matrix must be {rows} x {cols}, not {q.shape[0]} x {m.cols}")
-    one = q.shape[0] <= 1
-    return MxMatrix(_here(q), _here(s), lq if one else q.stride(0), ls if one else s.stride(0), m.fmt)
+    (n, wq), (ns, wsc), (ldq, iq), (lds, isc) = q.shape, s.shape, q.stride(), s.stride()
+    lq, ls = _mx_rows(fmt, c)
+    if n != ns or wq < lq or wsc < ls or iq != 1 or isc != 1:
+        raise SpecError(-1, f"rows of {c} columns are {lq} contiguous bytes of codes and {ls} of scales")
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        raise SpecError(-1, f"the microscaled matrix must be {rows} x {cols}, not {n} x {c}")
+    if dev is None:
+        dev = _on(q)
+    return MxMatrix(_at(q, dev), _at(s, dev), ldq if n > 1 else lq, lds if n > 1 else ls, fmt)
 
 
 def mx_empty(rows: int, cols: int, fmt: int, device="cuda") -> Mx:
@@ -878,120 +928,119 @@ def mx_empty(rows: int, cols: int, fmt: int, device="cuda") -> Mx:
 
 def mx_quantize(X, fmt: int, out: Mx = None) -> Mx:
     """X [rows, cols] (bfloat16 or float32) in microscaled storage, MX_INT8 or MX_FP4."""
-    _rows(X)
-    rows, cols = X.shape
-    if out is None:
-        out = mx_empty(rows, cols, fmt, X.device)
-    if out.fmt != fmt:
+    shape = rows, cols = _shape(X)
+    lq, ls = _mx_rows(fmt, cols)
+    if out is not None and out.fmt != fmt:
         raise SpecError(-1, "out has another format")
-    o = _mx(out, rows, cols)
-    _check(lib().spec_mx_quantize(_stream(), _here(X), _dt(X), rows, cols, _ld(X), ctypes.byref(o)))
+    dev = _on(X)
+    x, ldx = _mat(X, shape, X.dtype, dev)
+    if out is None:
+        out = mx_empty(rows, cols, fmt, dev)
+        o = MxMatrix(out.q.data_ptr(), out.s.data_ptr(), lq, ls, fmt)
+    else:
+        o = _mx(out, rows, cols, dev)
+    _launch(lib().spec_mx_quantize, dev, x, _dt(X), rows, cols, ldx, o)
     return out
 
 
 def mx_dequantize(m: Mx, dtype=None, out=None):
     """The values of a microscaled matrix, bfloat16 (the default) or float32."""
-    torch = _torch()
-    d = _mx(m)
-    rows, cols = m.q.shape[0], m.cols
+    d = _mx(m, None, None)
+    torch, dev, rows, cols = _torch(), m.q.get_device(), m.q.shape[0], m.cols
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=m.q.device)
-    _matrix(out, (rows, cols), dtype or out.dtype)
-    _check(lib().spec_mx_dequantize(_stream(), ctypes.byref(d), rows, cols, _here(out), _dt(out), _ld(out)))
+        out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=dev)
+        o = out.data_ptr(), cols
+    else:
+        o = _mat(out, (rows, cols), dtype or out.dtype, dev)
+    _launch(lib().spec_mx_dequantize, dev, d, rows, cols, o[0], _dt(out), o[1])
     return out
 
 
 def mx_linear_workspace(T: int, N: int, K: int, dtype) -> int:
-    return _bytes(lib().spec_mx_linear_workspace, T, N, K, _dt(_torch().empty(0, dtype=dtype)))
+    return _workspace("spec_mx_linear_workspace", T, N, K, _dt(_torch().empty(0, dtype=dtype)))
 
 
 def mx_linear(X, W: Mx, out=None, ws=None):
     """X W^T [T, N] for X [T, K] (bfloat16 or float32) and W [N, K] in MX_FP4."""
-    _rows(X)
-    T, K = X.shape
-    w = _mx(W, None, K)
-    N, t = W.q.shape[0], _dt(X)
+    shape = T, K = _shape(X)
+    t = _dt(X)
+    if type(W) is not Mx or W.cols != K:
+        raise SpecError(-1, f"W must be a microscaled matrix of {K} columns")
+    dev = _on(X)
+    w, N = _mx(W, None, K, dev), W.q.shape[0]
+    x, ldx = _mat(X, shape, X.dtype, dev)
     if out is None:
-        out = _torch().empty((T, N), dtype=X.dtype, device=X.device)
-    _matrix(out, (T, N), X.dtype)
-    ws = _ws(ws, _bytes(lib().spec_mx_linear_workspace, T, N, K, t), X.device)
-    _check(lib().spec_mx_linear(_stream(), _here(X), t, T, N, K, _ld(X), ctypes.byref(w), _here(out), _ld(out), _here(ws),
-                                ws.numel()))
+        out = _torch().empty((T, N), dtype=X.dtype, device=dev)
+        o = out.data_ptr(), N
+    else:
+        o = _mat(out, (T, N), X.dtype, dev)
+    p, size, ws = _scratch(ws, _workspace("spec_mx_linear_workspace", T, N, K, t), dev)
+    _launch(lib().spec_mx_linear, dev, x, t, T, N, K, ldx, w, *o, p, size)
     return out
 
 
 def mx_product_workspace(T: int, N: int, K: int) -> int:
-    return _bytes(lib().spec_mx_product_workspace, T, N, K)
+    return _workspace("spec_mx_product_workspace", T, N, K)
 
 
 def mx_product(X: Mx, W: Mx, dtype=None, out=None, ws=None):
     """X W^T [T, N] in bfloat16 (the default) or float32 for X [T, K] and W [N, K] in MX_FP4."""
-    torch = _torch()
-    x = _mx(X)
-    w = _mx(W, None, X.cols)
-    T, N, K = X.q.shape[0], W.q.shape[0], X.cols
+    x = _mx(X, None, None)
+    torch, dev, T, K = _torch(), X.q.get_device(), X.q.shape[0], X.cols
+    w, N = _mx(W, None, K, dev), W.q.shape[0]
     if out is None:
-        out = torch.empty((T, N), dtype=dtype or torch.bfloat16, device=X.q.device)
-    _matrix(out, (T, N), dtype or out.dtype)
-    ws = _ws(ws, _bytes(lib().spec_mx_product_workspace, T, N, K), X.q.device)
-    _check(lib().spec_mx_product(_stream(), ctypes.byref(x), ctypes.byref(w), T, N, K, _here(out), _dt(out), _ld(out),
-                                 _here(ws), ws.numel()))
+        out = torch.empty((T, N), dtype=dtype or torch.bfloat16, device=dev)
+        o = out.data_ptr(), N
+    else:
+        o = _mat(out, (T, N), dtype or out.dtype, dev)
+    p, size, ws = _scratch(ws, _workspace("spec_mx_product_workspace", T, N, K), dev)
+    _launch(lib().spec_mx_product, dev, x, w, T, N, K, o[0], _dt(out), o[1], p, size)
     return out
 
 
 def mx_weight_grad_workspace(T: int, N: int, K: int, dtype) -> int:
-    return _bytes(lib().spec_mx_weight_grad_workspace, T, N, K, _dt(_torch().empty(0, dtype=dtype)))
+    return _workspace("spec_mx_weight_grad_workspace", T, N, K, _dt(_torch().empty(0, dtype=dtype)))
 
 
 def mx_weight_grad(dY, X: Mx, beta: float = 0.0, dW=None, ws=None):
     """dW = beta dW + dY^T X [N, K] in dY's type, for dY [T, N] (bfloat16 or float32) and
     X [T, K] in MX_INT8."""
-    _rows(dY)
-    T, N = dY.shape
-    x = _mx(X, T)
-    K, t = X.cols, _dt(dY)
+    shape = T, N = _shape(dY)
+    t = _dt(dY)
+    if type(X) is not Mx or X.q.shape[0] != T:
+        raise SpecError(-1, f"X must be a microscaled matrix of {T} rows")
+    dev = _on(dY)
+    x, K = _mx(X, T, None, dev), X.cols
+    y, ldy = _mat(dY, shape, dY.dtype, dev)
     if dW is None:
         if beta != 0.0:
             raise SpecError(-1, "beta needs the dW to add to")
-        dW = _torch().empty((N, K), dtype=dY.dtype, device=dY.device)
-    _matrix(dW, (N, K), dY.dtype)
-    ws = _ws(ws, _bytes(lib().spec_mx_weight_grad_workspace, T, N, K, t), dY.device)
-    _check(lib().spec_mx_weight_grad(_stream(), _here(dY), t, T, N, K, _ld(dY), ctypes.byref(x), float(beta), _here(dW),
-                                     _ld(dW), _here(ws), ws.numel()))
+        dW = _torch().empty((N, K), dtype=dY.dtype, device=dev)
+        o = dW.data_ptr(), K
+    else:
+        o = _mat(dW, (N, K), dY.dtype, dev)
+    p, size, ws = _scratch(ws, _workspace("spec_mx_weight_grad_workspace", T, N, K, t), dev)
+    _launch(lib().spec_mx_weight_grad, dev, y, t, T, N, K, ldy, x, float(beta), *o, p, size)
     return dW
 
 
-def _block(n, d, like, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps):
+def _block(n, d, dtype, t, dev, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps):
     """The C descriptor of a block's norms: (Block, gate rows)."""
     def vec(w):
         if w is None:
             return None
-        if w.dtype != like.dtype or tuple(w.shape) != (d,) or (w.stride(0) != 1 and d > 1):
-            raise SpecError(-1, f"weights must be contiguous [{d}] of {like.dtype}")
-        return _here(w)
-    ldg, gates = d, 0
+        if w.dtype != dtype or w.shape != (d,) or (w.stride(0) != 1 and d > 1):
+            raise SpecError(-1, f"weights must be contiguous [{d}] of {dtype}")
+        return _at(w, dev)
+    ldg, gates, g = d, 0, None
     if gate is not None:
         if gate.dim() == 1:
             gate, gate_rows = gate.unsqueeze(0), max(n, 1)
-        _rows(gate)
         gates = (n + gate_rows - 1) // gate_rows if gate_rows >= 1 else -1
-        if gate.dtype != like.dtype or gate.shape[1] != d or gates < 0 or gate.shape[0] < gates:
-            raise SpecError(-1, f"gate must be [rows / gate_rows, {d}] of {like.dtype}, or [{d}]")
-        ldg = _ld(gate)
-    return Block(n, d, _dt(like), 1 if post else 0, float(alpha), float(beta), float(eps), vec(w_post), vec(w_pre),
-                 None if gate is None else _here(gate), ldg, int(gate_rows)), gates
-
-
-def _opt(t, shape, dtype):
-    """(address, row stride) of an optional matrix."""
-    if t is None:
-        return None, 0
-    _matrix(t, shape, dtype)
-    return _here(t), _ld(t)
-
-
-def _opt8(m, n, d):
-    return None if m is None else ctypes.byref(_mx(m, n, d))
+        if gate.dim() != 2 or gate.dtype != dtype or gate.shape[1] != d or gates < 0 or gate.shape[0] < gates:
+            raise SpecError(-1, f"gate must be [rows / gate_rows, {d}] of {dtype}, or [{d}]")
+        g, ldg = _mat(gate, gate.shape, dtype, dev)
+    return Block(n, d, t, 1 if post else 0, alpha, beta, eps, vec(w_post), vec(w_pre), g, ldg, gate_rows), gates
 
 
 def block_norm(H, Y=None, post: bool = True, w_post=None, w_pre=None, gate=None, gate_rows: int = 1, alpha: float = 1.0,
@@ -1001,65 +1050,97 @@ def block_norm(H, Y=None, post: bool = True, w_post=None, w_pre=None, gate=None,
     (None where there is none); without Y, Hout is H.  gate: [d], or [rows, d] of which
     one row serves gate_rows rows of Y.  y8, h8, x8: MX_INT8 storage that
     receives Y, Hout and X.  Hout may be H, X may be Y."""
-    torch = _torch()
-    _rows(H)
-    n, d = H.shape
-    b, _ = _block(n, d, H, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps)
-    if Y is not None and Hout is None:
-        Hout = torch.empty((n, d), dtype=H.dtype, device=H.device)
+    torch, dtype, t = _torch(), H.dtype, _dt(H)
+    shape = n, d = _shape(H)
+    dev = _on(H)
+    h, ldh = _mat(H, shape, dtype, dev)
+    b, _ = _block(n, d, dtype, t, dev, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps)
+    y = ho = (None, 0)
+    r_post = p_post = None
+    if Y is None:
+        Hout = H
+    else:
+        y = _mat(Y, shape, dtype, dev)
+        if Hout is None:
+            Hout = torch.empty(shape, dtype=dtype, device=dev)
+            ho = Hout.data_ptr(), d
+        else:
+            ho = _mat(Hout, shape, dtype, dev)
+        if post:
+            r_post = torch.empty(n, dtype=torch.float32, device=dev)
+            p_post = r_post.data_ptr()
     if X is None:
-        X = torch.empty((n, d), dtype=H.dtype, device=H.device)
-    r_post = torch.empty((n,), dtype=torch.float32, device=H.device) if Y is not None and post else None
-    r_pre = torch.empty((n,), dtype=torch.float32, device=H.device)
-    y, ho, x = (_opt(t, (n, d), H.dtype) for t in (Y, Hout, X))
-    _check(lib().spec_block_norm(_stream(), ctypes.byref(b), *y, _here(H), _ld(H), *ho, *x,
-                                 None if r_post is None else _here(r_post), _here(r_pre), _opt8(y8, n, d), _opt8(h8, n, d),
-                                 _opt8(x8, n, d)))
-    return H if Y is None else Hout, X, r_post, r_pre
+        X = torch.empty(shape, dtype=dtype, device=dev)
+        x = X.data_ptr(), d
+    else:
+        x = _mat(X, shape, dtype, dev)
+    r_pre = torch.empty(n, dtype=torch.float32, device=dev)
+    y8, h8, x8 = (None if m is None else _mx(m, n, d, dev) for m in (y8, h8, x8))
+    _launch(lib().spec_block_norm, dev, b, *y, h, ldh, *ho, *x, p_post, r_pre.data_ptr(), y8, h8, x8)
+    return Hout, X, r_post, r_pre
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_grad_workspace(n, d, t, gates, gate_rows):
+    b = Block(n, d, t, 0, 1.0, 1.0, 1e-6, None, None, 256 if gates else None, d, gate_rows)
+    return _bytes(lib().spec_block_norm_grad_workspace, b)
 
 
 def block_norm_grad_workspace(n: int, d: int, dtype, gates: int = 0, gate_rows: int = 1) -> int:
     """Workspace of block_norm_grad, with `gates` gate rows (0: no gate) of gate_rows rows each."""
-    b = Block(n, d, _dt(_torch().empty(0, dtype=dtype)), 0, 1.0, 1.0, 1e-6, None, None, 256 if gates else None, d, gate_rows)
-    return _bytes(lib().spec_block_norm_grad_workspace, ctypes.byref(b))
+    return _block_grad_workspace(n, d, _dt(_torch().empty(0, dtype=dtype)), gates, gate_rows)
 
 
 def block_norm_grad(dX, dHout, Hout, Y, r_pre, r_post=None, post: bool = True, w_post=None, w_pre=None, gate=None,
                     gate_rows: int = 1, alpha: float = 1.0, beta: float = 1.0, dH=None, dY=None, ws=None):
-    """Gradients of block_norm from those of its X and (otherwise than through X) of its Hout; either
-    may be None: zero.  Hout and Y as they were, or as stored in MX_INT8; Y None: no block.
+    """Gradients of block_norm from those of its X and (otherwise than through X) of its Hout; one
+    of them may be None: zero.  Hout and Y as they were, or as stored in MX_INT8; Y None: no block.
     Returns (dH, dY, dw_post, dw_pre, dgate), the last three float32, None for what was not given.
     dH may be dHout, dY may be dX."""
     torch = _torch()
     like = dX if dX is not None else dHout
     if like is None:
         raise SpecError(-1, "a gradient of X or of Hout is needed")
-    n, d = like.shape
-    b, gates = _block(n, d, like, post and Y is not None, w_post if Y is not None else None, w_pre,
-                      gate if Y is not None else None, gate_rows, alpha, beta, 1e-6)
+    dtype, t = like.dtype, _dt(like)
+    shape = n, d = _shape(like)
+    dev = _on(like)
+    if Y is None:
+        post, w_post, gate = False, None, None
+    b, gates = _block(n, d, dtype, t, dev, post, w_post, w_pre, gate, gate_rows, alpha, beta, 1e-6)
+    none = (None, 0)
 
-    def stored(t):
+    def given(m):
         """(address, stride, descriptor) of a matrix or of its checkpoint."""
-        return (None, 0, _opt8(t, n, d)) if isinstance(t, Mx) else (*_opt(t, (n, d), like.dtype), None)
-    y, ho = stored(Y), stored(Hout if dX is not None else None)
-    if dH is None:
-        dH = torch.empty((n, d), dtype=like.dtype, device=like.device)
-    if dY is None and Y is not None:
-        dY = torch.empty((n, d), dtype=like.dtype, device=like.device)
+        if type(m) is Mx:
+            return None, 0, _mx(m, n, d, dev)
+        return (*(none if m is None else _mat(m, shape, dtype, dev)), None)
 
-    def f32(*shape):
-        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    def result(m):
+        if m is None:
+            m = torch.empty(shape, dtype=dtype, device=dev)
+            return m, (m.data_ptr(), d)
+        return m, _mat(m, shape, dtype, dev)
 
-    def at(t):
-        return None if t is None else _here(t)
-    dw_post = f32(d) if b.post and w_post is not None else None
-    dw_pre = f32(d) if dX is not None and w_pre is not None else None
-    dgate = f32(gates, d) if gate is not None and Y is not None else None
-    ws = _ws(ws, _bytes(lib().spec_block_norm_grad_workspace, ctypes.byref(b)), like.device)
-    r1 = _vec32(r_post, n) if b.post and r_post is not None else None
-    r2 = _vec32(r_pre, n) if dX is not None and r_pre is not None else None
-    _check(lib().spec_block_norm_grad(_stream(), ctypes.byref(b), *y, *ho, r1, r2, *_opt(dHout, (n, d), like.dtype),
-                                      *_opt(dX, (n, d), like.dtype), *_opt(dH, (n, d), like.dtype),
-                                      *_opt(dY, (n, d), like.dtype), at(dw_post), at(dw_pre), at(dgate), _here(ws),
-                                      ws.numel()))
+    def sums(wanted, *size):
+        if not wanted:
+            return None, None
+        m = torch.empty(size, dtype=torch.float32, device=dev)
+        return m, m.data_ptr()
+
+    def factors(r):
+        if r.dtype != torch.float32 or r.shape != (n,) or (n > 1 and r.stride(0) != 1):
+            raise SpecError(-1, "per-row values must be a contiguous float32 vector, one per row")
+        return _at(r, dev)
+    y, ho = given(Y), given(Hout) if dX is not None else (None, 0, None)
+    dx, do = (none if m is None else _mat(m, shape, dtype, dev) for m in (dX, dHout))
+    dH, dh = result(dH)
+    dY, dy = (None, none) if Y is None else result(dY)
+    dw_post, p_post = sums(w_post is not None, d)
+    dw_pre, p_pre = sums(dX is not None and w_pre is not None, d)
+    dgate, p_gate = sums(gate is not None, gates, d)
+    r1 = factors(r_post) if post and r_post is not None else None
+    r2 = factors(r_pre) if dX is not None and r_pre is not None else None
+    # (a single gate row serves all rows)
+    p, size, ws = _scratch(ws, _block_grad_workspace(n, d, t, gates, b.gate_rows if gates else 1), dev)
+    _launch(lib().spec_block_norm_grad, dev, b, *y, *ho, r1, r2, *do, *dx, *dh, *dy, p_post, p_pre, p_gate, p, size)
     return dH, dY, dw_post, dw_pre, dgate if dgate is None or gate.dim() == 2 else dgate.view(d)

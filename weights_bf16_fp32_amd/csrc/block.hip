@@ -658,7 +658,7 @@ hipError_t block_norm(hipStream_t stream, const spec_block *b, const void *Y, in
     }
     return pick_norm(b->d, [&](auto shape) {
         using SH = decltype(shape);
-        const int64_t grid = std::min<int64_t>(cdiv_h(b->n, SH::ROWS), 256 * 8 * 256 / SH::NT);
+        const int64_t grid = std::min<int64_t>(cdiv_h(b->n, SH::ROWS), 256 * 6 * 256 / SH::NT);
         hipLaunchKernelGGL((k_block_norm<E, SH>), dim3((unsigned)grid), dim3(SH::NT), 0, stream, a,
                            (const st *)Y, ldy, (const st *)H, ldh, (st *)O, ldo, (st *)X, ldx, r1, r2, stored(yq),
                            stored(oq), stored(xq), grid * SH::ROWS);

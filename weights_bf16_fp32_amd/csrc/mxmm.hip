@@ -557,8 +557,13 @@ hipError_t few(hipStream_t stream, const void *X, int64_t ldx, int64_t T, int64_
                            ldy, vec);
         return hipGetLastError();
     };
-    const auto rows = [&](auto tt) {  // two row tiles share the fragments of X where every CU gets a workgroup
-        return N >= 32 * 256 ? go(std::integral_constant<int, 2>{}, tt) : go(std::integral_constant<int, 1>{}, tt);
+    // Row tiles of a workgroup share the fragments of X, whose reads from the L2 cost more than
+    // W's, as long as most CUs still get a workgroup: one, two and four tiles take 16.0, 12.4
+    // and 11.0 us for 8 x 14336 x 4096 bf16 (896, 448 and 224 workgroups).
+    const auto rows = [&](auto tt) {
+        return N >= 64 * 208   ? go(std::integral_constant<int, 4>{}, tt)
+               : N >= 32 * 208 ? go(std::integral_constant<int, 2>{}, tt)
+                               : go(std::integral_constant<int, 1>{}, tt);
     };
     return T <= 16 ? rows(std::integral_constant<int, 1>{})
            : T <= 32 ? rows(std::integral_constant<int, 2>{})
