@@ -584,7 +584,7 @@ __global__ __launch_bounds__(1024) void k_block_join(BlockArgs a, GradPart part,
     const bool gated = what == 1 && deal.share > 0 && a.gate != nullptr;  // sums s, not yet times their gate row
     float s = 0.f;
     if (c < a.d) {
-#pragma unroll 4
+#pragma unroll 16
         for (int64_t w = w0 + ty; w < w1; w += 32) {
             const float v = src[w * part.ld + c];
             s += gated ? v * weight(a.gate, w / deal.share * a.ldg, c) : v;

@@ -388,15 +388,22 @@ __global__ __launch_bounds__(256) void k_mx_join(MmOut o, int64_t np, int vec)
 constexpr int64_t PIECE_BYTES = (int64_t)256 << 20;  // of unpacked values at most, but no less than 256 rows of them
 constexpr int64_t SPLIT_BYTES = (int64_t)64 << 20;   // of the shares' sums
 
-// shares of k of a product of np x nq results: as many as give every CU a tile,
-// of 256 k at least, as far as their sums have room
-int split_ways(int64_t np, int64_t nq, int64_t K)
+// Shares of k of a product of np x nq results: as many as give every CU a tile, of
+// `least` k at least, as far as their sums have room.
+int split_ways(int64_t np, int64_t nq, int64_t K, int64_t edge, int64_t least)
 {
-    const int64_t tiles = cdiv_h(np, 128) * cdiv_h(std::max<int64_t>(nq, 1), 128);
-    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), K / 256);
+    const int64_t tiles = cdiv_h(np, edge) * cdiv_h(std::max<int64_t>(nq, 1), edge);
+    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), K / least);
     w = std::min<int64_t>(w, SPLIT_BYTES / (4 * up_h(np, 4) * std::max<int64_t>(nq, 1)));
     return (int)std::max<int64_t>(1, std::min<int64_t>(w, 64));
 }
+
+// bf16 and f32: a share of 256 k is four (eight) steps
+int ways_of(int64_t np, int64_t nq, int64_t K) { return split_ways(np, nq, K, 128, 256); }
+
+// FP4: 2048 k are eight steps.  Shorter shares cost more in the second launch than they
+// save: 333 x 1000 x 1000 took 9.4 us in three shares.
+int ways_of_fp4(int64_t N, int64_t T, int64_t K) { return split_ways(N, T, K, 64, 2048); }
 
 template <typename E, typename EO, bool S>
 hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int64_t np, const typename E::st *Q,
@@ -404,7 +411,7 @@ hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int
 {
     using st = typename EO::st;
     const int vec = (uintptr_t)out % (4 * sizeof(st)) == 0 && ldo % 4 == 0;
-    MmOut o{out, ldo, beta, part, up_h(np, 4), nq, split_ways(np, nq, K)};
+    MmOut o{out, ldo, beta, part, up_h(np, 4), nq, ways_of(np, nq, K)};
     const hipError_t e = mm_pick<E>([&](int64_t edge) { return cdiv_h(np, edge) * cdiv_h(nq, edge) * o.ways; }, [&](auto c) {
         using C = decltype(c);
         const int tp = (int)cdiv_h(np, C::BP), tq = (int)cdiv_h(nq, C::BQ);
@@ -599,7 +606,7 @@ hipError_t product4(hipStream_t stream, const spec_mx *X, const spec_mx *W, int6
     for (int64_t t0 = 0; t0 < T; t0 += MOST_T) {
         const int64_t tn = std::min(MOST_T, T - t0);
         const spec_mx x = rows_from(X, t0);
-        MmOut o{(st *)Y + t0 * ldy, ldy, 0.f, (float *)ws, up_h(N, 4), tn, split_ways(N, tn, K)};
+        MmOut o{(st *)Y + t0 * ldy, ldy, 0.f, (float *)ws, up_h(N, 4), tn, ways_of_fp4(N, tn, K)};
         hipError_t e = pick4(N, tn, o.ways, [&](auto c) {
             using C = decltype(c);
             const int tp = (int)cdiv_h(N, C::BP), tq = (int)cdiv_h(tn, C::BQ);
@@ -628,8 +635,8 @@ size_t mx_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int t)
 
 size_t mx_product_workspace_bytes(int64_t T, int64_t N, int64_t K)
 {
-    const int ways = split_ways(N, std::min(T, MOST_T), K);
-    return ways > 1 ? (size_t)ways * T * up_h(N, 4) * 4 : 256;
+    const int ways = ways_of_fp4(N, std::min(T, MOST_T), K);  // (a last, smaller piece may take more: SPLIT_BYTES)
+    return T > MOST_T ? (size_t)SPLIT_BYTES : ways > 1 ? (size_t)ways * T * up_h(N, 4) * 4 : 256;
 }
 
 size_t mx_weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, int t)
