@@ -389,11 +389,11 @@ constexpr int64_t PIECE_BYTES = (int64_t)256 << 20;  // of unpacked values at mo
 constexpr int64_t SPLIT_BYTES = (int64_t)64 << 20;   // of the shares' sums
 
 // Shares of k of a product of np x nq results: as many as give every CU a tile, of
-// `least` k at least, as far as their sums have room.
+// about `least` k or more, as far as their sums have room.
 int split_ways(int64_t np, int64_t nq, int64_t K, int64_t edge, int64_t least)
 {
     const int64_t tiles = cdiv_h(np, edge) * cdiv_h(std::max<int64_t>(nq, 1), edge);
-    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), K / least);
+    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), cdiv_h(K, least));
     w = std::min<int64_t>(w, SPLIT_BYTES / (4 * up_h(np, 4) * std::max<int64_t>(nq, 1)));
     return (int)std::max<int64_t>(1, std::min<int64_t>(w, 64));
 }
