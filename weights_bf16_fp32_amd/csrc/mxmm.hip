@@ -4,9 +4,29 @@
 //   product  the same, X in FP4 too
 //   wgrad    dW[n][k] = beta dW[n][k] + sum_t dY[t][n] X[t][k]     X in INT8, dY bf16 or f32
 //
-// A microscaled value has at most seven significant bits and a power of two, so it
-// is exact in bf16: the packed operand is unpacked into the workspace, and the
-// products are bf16 (f32) MFMA products with f32 sums.
+// product: both operands go to the scaled MFMA as they lie in memory, 32 codes and
+// their byte per lane (k_mx_fp4).  8192 x 14336 x 4096 takes 291 to 308 us, 3.1 to 3.3
+// PFLOP/s, bound as the bf16 core is: by the MFMAs' power and by the copies through the
+// L2, 64 KB of codes per CU and step of 256 k.  Unpacked to bf16 first it took 749 us.
+//
+// linear, few rows of X (a decode step): bound by reading W and by X's fragments, which
+// every workgroup reads from the L2 (k_mx_few).  1, 8, 16, 32 and 64 x 4096 x 4096 bf16
+// take 4.6, 6.0, 7.3, 11.1 and 19.4 us; 8 x 14336 x 4096 11.1 us, 2.8 TB/s of W.  Requesting
+// W or X a step ahead, X in whole 64-byte pieces turned between lanes, and 4 or 16 waves
+// instead of 8 changed these by less than 5 %.
+//
+// linear of more rows, and wgrad: a microscaled value has at most seven significant
+// bits and a power of two, so it is exact in bf16.  The packed operand is unpacked into
+// the workspace (22 to 30 us for 14336 x 4096, 16384 x 4096) and the products are those
+// of mm.h, bf16 or f32 MFMA with f32 sums: 2047 x 4096 x 14336 244 us of 985 TFLOP/s (one
+// round of 242 tiles), 16384 x 4096 x 4096 454 us, 1210 TFLOP/s.  Products with too few
+// tiles for the CUs are split along k and their sums joined by a second launch.
+//
+//   k_mx_pack   X or dY with 16-byte rows (only where they have none)
+//   k_mx_mm     bf16 or f32 tiles
+//   k_mx_fp4    FP4 tiles
+//   k_mx_few    few rows of X
+//   k_mx_join   the sums of shares of k
 #include <algorithm>
 
 #include "mx.h"
@@ -388,22 +408,61 @@ __global__ __launch_bounds__(256) void k_mx_join(MmOut o, int64_t np, int vec)
 constexpr int64_t PIECE_BYTES = (int64_t)256 << 20;  // of unpacked values at most, but no less than 256 rows of them
 constexpr int64_t SPLIT_BYTES = (int64_t)64 << 20;   // of the shares' sums
 
-// Shares of k of a product of np x nq results: as many as give every CU a tile, of
-// about `least` k or more, as far as their sums have room.
-int split_ways(int64_t np, int64_t nq, int64_t K, int64_t edge, int64_t least)
+// The tile and the shares of k of a bf16 or f32 product that take the least time: the
+// busiest of 256 CUs at the core's rate (4.7 TFLOP/s a CU in bf16, 0.6 in f32, for the
+// largest tile; per: the others' time per result, as in mm.h, the smallest's more, whose
+// rounds are short here), a microsecond per round, and for shares of k their
+// sums written and read again (8 TB/s, through the caches) and a launch.  Shares are of
+// about 256 k or more.
+struct MmPlan {
+    int edge, ways;
+};
+template <typename E>
+MmPlan mm_plan(int64_t np, int64_t nq, int64_t K)
 {
-    const int64_t tiles = cdiv_h(np, edge) * cdiv_h(std::max<int64_t>(nq, 1), edge);
-    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), cdiv_h(K, least));
-    w = std::min<int64_t>(w, SPLIT_BYTES / (4 * up_h(np, 4) * std::max<int64_t>(nq, 1)));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(w, 64));
+    constexpr bool H = sizeof(typename E::st) == 2;
+    const int edge[5] = {256, 192, 128, 64, 32};
+    const double per[5] = {1.0, 1.1, H ? 1.28 : 1.03, H ? 2.1 : 1.14, H ? 10.0 : 2.5};
+    const double rate = (H ? 4.7e6 : 0.6e6) / 2;  // products of a CU per us
+    const int64_t sums = 4 * up_h(np, 4) * std::max<int64_t>(nq, 1);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>({cdiv_h(K, 256), SPLIT_BYTES / sums, 64}));
+    MmPlan best{256, 1};
+    double least = 0.0;
+    for (int i = 0; i < 5; ++i)
+        for (int w = 1; w <= most; ++w) {
+            const int64_t tiles = cdiv_h(np, edge[i]) * cdiv_h(nq, edge[i]);
+            // (of the smaller shapes two workgroups share a CU, and one alone takes as long)
+            const double rounds = edge[i] > 128 ? (double)cdiv_h(tiles * w, 256) : 2.0 * cdiv_h(tiles * w, 512);
+            double t = rounds * edge[i] * edge[i] * per[i] * (double)cdiv_h(K, w) / rate;
+            t += (double)cdiv_h(tiles * w, edge[i] > 128 ? 256 : 512);  // a round's first copies and last stores
+            if (w > 1) t += 3.0 + 2.0 * w * (double)sums / 8e6;
+            if ((i == 0 && w == 1) || t < least) least = t, best = {edge[i], w};
+        }
+    return best;
 }
 
-// bf16 and f32: a share of 256 k is four (eight) steps
-int ways_of(int64_t np, int64_t nq, int64_t K) { return split_ways(np, nq, K, 128, 256); }
+template <typename F>
+hipError_t with_tile(int edge, F &&f)
+{
+    switch (edge) {
+    case 256: return f(Tile256{});
+    case 192: return f(Tile192{});
+    case 128: return f(Tile128{});
+    case 64: return f(Tile64{});
+    default: return f(Tile32{});
+    }
+}
 
-// FP4: 2048 k are eight steps.  Shorter shares cost more in the second launch than they
-// save: 333 x 1000 x 1000 took 9.4 us in three shares.
-int ways_of_fp4(int64_t N, int64_t T, int64_t K) { return split_ways(N, T, K, 64, 2048); }
+// FP4: as many shares as give every CU a tile of 64 x 64, of about 2048 k (eight steps) or
+// more.  Shorter ones cost more in the second launch than they save: 333 x 1000 x 1000
+// took 9.4 us in three shares, 6.1 in one.
+int ways_of_fp4(int64_t N, int64_t T, int64_t K)
+{
+    const int64_t tiles = cdiv_h(N, 64) * cdiv_h(std::max<int64_t>(T, 1), 64);
+    int64_t w = std::min<int64_t>(cdiv_h(256, tiles), cdiv_h(K, 2048));
+    w = std::min<int64_t>(w, SPLIT_BYTES / (4 * up_h(N, 4) * std::max<int64_t>(T, 1)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(w, 64));
+}
 
 template <typename E, typename EO, bool S>
 hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int64_t np, const typename E::st *Q,
@@ -411,8 +470,9 @@ hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int
 {
     using st = typename EO::st;
     const int vec = (uintptr_t)out % (4 * sizeof(st)) == 0 && ldo % 4 == 0;
-    MmOut o{out, ldo, beta, part, up_h(np, 4), nq, ways_of(np, nq, K)};
-    const hipError_t e = mm_pick<E>([&](int64_t edge) { return cdiv_h(np, edge) * cdiv_h(nq, edge) * o.ways; }, [&](auto c) {
+    const MmPlan plan = mm_plan<E>(np, nq, K);
+    MmOut o{out, ldo, beta, part, up_h(np, 4), nq, plan.ways};
+    const hipError_t e = with_tile(plan.edge, [&](auto c) {
         using C = decltype(c);
         const int tp = (int)cdiv_h(np, C::BP), tq = (int)cdiv_h(nq, C::BQ);
         hipLaunchKernelGGL((k_mx_mm<E, EO, C, S>), dim3((unsigned)((int64_t)tp * tq * o.ways)), dim3(C::NT), 0, stream, P,
@@ -456,7 +516,8 @@ spec_mx rows_from(const spec_mx *m, int64_t row)
     return r;
 }
 
-// X of up to this many rows goes by k_mx_few
+// X of up to this many rows goes by k_mx_few: 64 rows of 8192 x 8192 bf16 take 40 us, 65 by
+// the unpacked product 59; of 2048 x 2048 f32 18 and 32.
 constexpr int64_t FEW_ROWS = 64;
 
 constexpr int64_t MOST_T = 65536;  // rows of X per launch
@@ -577,7 +638,8 @@ hipError_t few(hipStream_t stream, const void *X, int64_t ldx, int64_t T, int64_
                      : rows(std::integral_constant<int, 4>{});
 }
 
-// The tile whose busiest CU has least to do; per: time per result against the largest tile's
+// The tile whose busiest CU has least to do.  per: time per result against the largest
+// tile's, the 16-bit core's ratios (steps are as many bytes and the rate follows the copies).
 template <typename F>
 hipError_t pick4(int64_t N, int64_t T, int ways, F &&f)
 {
