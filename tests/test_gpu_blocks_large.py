@@ -64,6 +64,24 @@ def test_products_in_pieces(spec):
     mx._close(spec.mx_weight_grad(dy, x8), dy.double().t().contiguous(), mx._values(spec, x8).t().contiguous(), "bf16")
 
 
+@pytest.mark.parametrize("dtype,a,b,k", [
+    ("bf16", 70, 80, 20), ("bf16", 70, 80, 666), ("bf16", 205, 4242, 2000), ("bf16", 915, 2239, 16), ("bf16", 71, 5724, 1957),
+    ("bf16", 2899, 3601, 16), ("bf16", 4096, 2047, 4200), ("f32", 70, 81, 16), ("f32", 70, 81, 356), ("f32", 2524, 202, 16),
+    ("f32", 2895, 85, 803), ("f32", 1706, 1241, 16), ("f32", 1327, 1595, 527), ("f32", 2925, 2849, 16), ("f32", 710, 2806, 774)])
+def test_products_of_every_tile(spec, dtype, a, b, k):
+    """Tiles of all sizes, with k whole and in shares: b rows of X by a of W, and as a weight gradient of b x a."""
+    import torch
+    import test_gpu_mx as mx
+    print_case("mx tiles", dtype=dtype, a=a, b=b, k=k)
+    g = mx._gen(a + b + k)
+    w = spec.mx_quantize(torch.randn(a, k, generator=g, device="cuda"), spec.MX_FP4)
+    x = torch.randn(b, k, generator=g, device="cuda").to(mx._dt(dtype))
+    mx._close(spec.mx_linear(x, w), x.double(), mx._values(spec, w), dtype)
+    x8 = spec.mx_quantize(torch.randn(k, a, generator=g, device="cuda"), spec.MX_INT8)
+    dy = torch.randn(k, b, generator=g, device="cuda").to(mx._dt(dtype))
+    mx._close(spec.mx_weight_grad(dy, x8), dy.double().t().contiguous(), mx._values(spec, x8).t().contiguous(), dtype)
+
+
 def test_norms_past_32_bits(spec):
     """Rows past 2^32 bytes and 2^31 elements."""
     import torch

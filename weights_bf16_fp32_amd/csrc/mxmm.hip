@@ -18,9 +18,9 @@
 // linear of more rows, and wgrad: a microscaled value has at most seven significant
 // bits and a power of two, so it is exact in bf16.  The packed operand is unpacked into
 // the workspace (22 to 30 us for 14336 x 4096, 16384 x 4096) and the products are those
-// of mm.h, bf16 or f32 MFMA with f32 sums: 2047 x 4096 x 14336 244 us of 985 TFLOP/s (one
-// round of 242 tiles), 16384 x 4096 x 4096 454 us, 1210 TFLOP/s.  Products with too few
-// tiles for the CUs are split along k and their sums joined by a second launch.
+// of mm.h, bf16 or f32 MFMA with f32 sums: 2047 x 4096 x 14336 191 us, 1260 TFLOP/s (one
+// round of 256 tiles, k in two shares, and 14 us to join them; unsplit 192 x 192 tiles
+// took 244), 16384 x 4096 x 4096 455 us, 1210 TFLOP/s.
 //
 //   k_mx_pack   X or dY with 16-byte rows (only where they have none)
 //   k_mx_mm     bf16 or f32 tiles
@@ -92,7 +92,7 @@ SPEC_DEVICE void put_tile(M &mm, const L &lds, const MmOut &o, int64_t p0, int64
 }
 
 // acc[q][p] = sum over k of P(p, k) Q(q, k), both operands with k contiguous (S false) or slow
-template <typename E, typename EO, typename C, bool S>
+template <typename E, typename C, bool S>
 __global__ MM_BOUNDS(C) void k_mx_mm(const typename E::st *__restrict__ P, int64_t ldp, int64_t np,
                                      const typename E::st *__restrict__ Q, int64_t ldq, int64_t nq, int64_t K,
                                      int tp_n, int tq_n, MmOut o, int vec)
@@ -109,7 +109,7 @@ __global__ MM_BOUNDS(C) void k_mx_mm(const typename E::st *__restrict__ P, int64
     const MmSrc sq{(const char *)(S ? Q + q0 : Q + q0 * ldq), ldq * M::SZ, (int)min<int64_t>(C::BQ, nq - q0), kp};
     M mm;
     mm.run(sp, sq, kb, ke, lds);
-    put_tile<EO>(mm, lds, o, p0, q0, sp.lim, sq.lim, share, vec);
+    put_tile<E>(mm, lds, o, p0, q0, sp.lim, sq.lim, share, vec);
 }
 
 // ------------------------------------------------------------------ both operands in FP4
@@ -422,13 +422,13 @@ MmPlan mm_plan(int64_t np, int64_t nq, int64_t K)
 {
     constexpr bool H = sizeof(typename E::st) == 2;
     const int edge[5] = {256, 192, 128, 64, 32};
-    const double per[5] = {1.0, 1.1, H ? 1.28 : 1.03, H ? 2.1 : 1.14, H ? 10.0 : 2.5};
+    const double per[5] = {1.0, 1.1, H ? 1.28 : 1.03, H ? 2.1 : 1.14, 2.5};
     const double rate = (H ? 4.7e6 : 0.6e6) / 2;  // products of a CU per us
     const int64_t sums = 4 * up_h(np, 4) * std::max<int64_t>(nq, 1);
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>({cdiv_h(K, 256), SPLIT_BYTES / sums, 64}));
     MmPlan best{256, 1};
     double least = 0.0;
-    for (int i = 0; i < 5; ++i)
+    for (int i = 0; i < (H ? 4 : 5); ++i)  // (in 16 bits the 64 x 64 tile is never slower than the 32 x 32)
         for (int w = 1; w <= most; ++w) {
             const int64_t tiles = cdiv_h(np, edge[i]) * cdiv_h(nq, edge[i]);
             // (of the smaller shapes two workgroups share a CU, and one alone takes as long)
@@ -441,7 +441,7 @@ MmPlan mm_plan(int64_t np, int64_t nq, int64_t K)
     return best;
 }
 
-template <typename F>
+template <typename E, typename F>
 hipError_t with_tile(int edge, F &&f)
 {
     switch (edge) {
@@ -449,7 +449,9 @@ hipError_t with_tile(int edge, F &&f)
     case 192: return f(Tile192{});
     case 128: return f(Tile128{});
     case 64: return f(Tile64{});
-    default: return f(Tile32{});
+    default:
+        if constexpr (sizeof(typename E::st) == 4) return f(Tile32{});
+        return hipErrorInvalidValue;  // (mm_plan gives no other)
     }
 }
 
@@ -464,23 +466,23 @@ int ways_of_fp4(int64_t N, int64_t T, int64_t K)
     return (int)std::max<int64_t>(1, std::min<int64_t>(w, 64));
 }
 
-template <typename E, typename EO, bool S>
+template <typename E, bool S>
 hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int64_t np, const typename E::st *Q,
                    int64_t ldq, int64_t nq, int64_t K, void *out, int64_t ldo, float beta, float *part)
 {
-    using st = typename EO::st;
+    using st = typename E::st;
     const int vec = (uintptr_t)out % (4 * sizeof(st)) == 0 && ldo % 4 == 0;
     const MmPlan plan = mm_plan<E>(np, nq, K);
     MmOut o{out, ldo, beta, part, up_h(np, 4), nq, plan.ways};
-    const hipError_t e = with_tile(plan.edge, [&](auto c) {
+    const hipError_t e = with_tile<E>(plan.edge, [&](auto c) {
         using C = decltype(c);
         const int tp = (int)cdiv_h(np, C::BP), tq = (int)cdiv_h(nq, C::BQ);
-        hipLaunchKernelGGL((k_mx_mm<E, EO, C, S>), dim3((unsigned)((int64_t)tp * tq * o.ways)), dim3(C::NT), 0, stream, P,
+        hipLaunchKernelGGL((k_mx_mm<E, C, S>), dim3((unsigned)((int64_t)tp * tq * o.ways)), dim3(C::NT), 0, stream, P,
                            ldp, np, Q, ldq, nq, K, tp, tq, o, vec);
         return hipGetLastError();
     });
     if (e != hipSuccess || o.ways == 1) return e;
-    hipLaunchKernelGGL(k_mx_join<EO>, dim3((unsigned)std::min<int64_t>(cdiv_h(o.rows * o.ldpart / 4, 256), 4096)), dim3(256),
+    hipLaunchKernelGGL(k_mx_join<E>, dim3((unsigned)std::min<int64_t>(cdiv_h(o.rows * o.ldpart / 4, 256), 4096)), dim3(256),
                        0, stream, o, np, vec);
     return hipGetLastError();
 }
@@ -560,7 +562,7 @@ hipError_t linear(hipStream_t stream, const void *X, int64_t ldx, int64_t T, int
             const st *x = (const st *)X + t0 * ldx;
             if (!in_place) e = pack<E>(stream, x, tn, K, ldx, xv);
             if (e == hipSuccess)
-                e = product<E, E, false>(stream, wv, p.kp, nn, in_place ? x : xv, in_place ? ldx : p.kp, tn, K,
+                e = product<E, false>(stream, wv, p.kp, nn, in_place ? x : xv, in_place ? ldx : p.kp, tn, K,
                                          (st *)Y + t0 * ldy + n, ldy, 0.f, (float *)(ws + p.part));
         }
         if (e != hipSuccess) return e;
@@ -607,7 +609,7 @@ hipError_t wgrad(hipStream_t stream, const void *dY, int64_t ldy, int64_t T, int
         x.s = (uint8_t *)X->s + c / 32;
         e = launch_mx_dequantize(stream, &x, T, cn, up_h(cn, 32), xv, t, p.cols);
         if (e == hipSuccess)
-            e = product<E, E, true>(stream, xv, p.cols, cn, dy, ldy, N, T, (st *)dW + c, lddw, beta, (float *)(ws + p.part));
+            e = product<E, true>(stream, xv, p.cols, cn, dy, ldy, N, T, (st *)dW + c, lddw, beta, (float *)(ws + p.part));
     }
     return e;
 }
