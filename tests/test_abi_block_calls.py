@@ -1,0 +1,40 @@
+"""Calls of the residual blocks' operators at the ends of their documented ranges, as far as the host
+decides them (no GPU needed)."""
+import ctypes
+import os
+
+import pytest
+
+import weights_bf16_fp32_amd as spec
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(spec.LIB_PATH):
+        from weights_bf16_fp32_amd import build
+        build.build()
+    return spec.lib()
+
+
+def test_no_workspace_is_empty(L):
+    """A workspace of no bytes has no address, which the entry points refuse: every size asks for some."""
+    b = ctypes.c_size_t()
+    for T in (0, 1, 5, 64, 65, 70000):
+        for N in (1, 70, 1000, 16384):
+            for K in (1, 64, 2049, 4096, 1 << 20):
+                assert L.spec_mx_product_workspace(T, N, K, b) == 0 and b.value > 0, (T, N, K)
+                for t in (spec.BF16, spec.F32):
+                    assert L.spec_mx_linear_workspace(T, N, K, t, b) == 0 and b.value > 0, (T, N, K)
+                    assert L.spec_mx_weight_grad_workspace(T, N, K, t, b) == 0 and b.value > 0, (T, N, K)
+
+
+def test_product_without_rows(L):
+    """T = 0 has nothing to do, whatever the other sizes: what the query asks for is enough."""
+    at = 1 << 20  # an aligned address; never dereferenced, because nothing is launched
+    b = ctypes.c_size_t()
+    for N, K in ((70, 64), (70, 4096), (1, 1 << 20), (14336, 4096)):
+        lq, ls = spec._mx_rows(spec.MX_FP4, K)
+        X, W = spec.MxMatrix(None, None, lq, ls, spec.MX_FP4), spec.MxMatrix(at, at, lq, ls, spec.MX_FP4)
+        assert L.spec_mx_product_workspace(0, N, K, b) == 0
+        ws = at if b.value else None
+        assert L.spec_mx_product(None, X, W, 0, N, K, None, spec.BF16, N, ws, b.value) == 0, (N, K)

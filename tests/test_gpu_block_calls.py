@@ -1,0 +1,30 @@
+"""Calls of the residual blocks' operators at the ends of their documented ranges: no rows, parts left
+out, values that leave f32's range."""
+import pytest
+
+from gpu_util import print_case
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def spec():
+    import torch
+    import weights_bf16_fp32_amd as spec
+    assert torch.cuda.is_available()
+    spec.lib()
+    return spec
+
+
+@pytest.mark.parametrize("N,K", [(70, 64), (70, 4096), (1000, 14336)])
+def test_product_without_rows(spec, N, K):
+    import torch
+    print_case("mx_product", T=0, N=N, K=K)
+    w = spec.mx_quantize(torch.randn(N, K, device="cuda"), spec.MX_FP4)
+    none = spec.mx_quantize(torch.empty(0, K, device="cuda"), spec.MX_FP4)
+    for dt in (torch.bfloat16, torch.float32):
+        y = spec.mx_product(none, w, dt)
+        assert y.shape == (0, N) and y.dtype == dt
+        assert spec.mx_linear(torch.empty(0, K, dtype=dt, device="cuda"), w).shape == (0, N)

@@ -700,7 +700,7 @@ size_t mx_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int t)
 size_t mx_product_workspace_bytes(int64_t T, int64_t N, int64_t K)
 {
     const int ways = ways_of_fp4(N, std::min(T, MOST_T), K);  // (a last, smaller piece may take more: SPLIT_BYTES)
-    return T > MOST_T ? (size_t)SPLIT_BYTES : ways > 1 ? (size_t)ways * T * up_h(N, 4) * 4 : 256;
+    return T > MOST_T ? (size_t)SPLIT_BYTES : ways > 1 && T > 0 ? (size_t)ways * T * up_h(N, 4) * 4 : 256;
 }
 
 size_t mx_weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, int t)
