@@ -28,3 +28,19 @@ def test_product_without_rows(spec, N, K):
         y = spec.mx_product(none, w, dt)
         assert y.shape == (0, N) and y.dtype == dt
         assert spec.mx_linear(torch.empty(0, K, dtype=dt, device="cuda"), w).shape == (0, N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("post", [True, False])
+def test_vector_gate_without_rows(spec, dtype, post):
+    """The gradient of a gate [d] is a sum over the rows: without rows zeros of [d], as the weights' are."""
+    import torch
+    print_case("block_norm_grad", n=0, dtype=dtype, post=post)
+    dt, d = torch.bfloat16 if dtype == "bf16" else torch.float32, 65
+    e, w = torch.empty(0, d, dtype=dt, device="cuda"), torch.randn(d, device="cuda").to(dt)
+    args = dict(post=post, w_post=w if post else None, w_pre=w, gate=w)
+    h, x, r_post, r_pre = spec.block_norm(e, e, **args)
+    dh, dy, dw_post, dw_pre, dgate = spec.block_norm_grad(e, e, h, e, r_pre, r_post, **args)
+    assert dh.shape == dy.shape == (0, d)
+    for g in (dw_pre, dgate) + ((dw_post,) if post else ()):
+        assert g.shape == (d,) and g.dtype == torch.float32 and not g.any()

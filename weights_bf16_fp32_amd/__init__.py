@@ -1143,4 +1143,6 @@ def block_norm_grad(dX, dHout, Hout, Y, r_pre, r_post=None, post: bool = True, w
     # (a single gate row serves all rows)
     p, size, ws = _scratch(ws, _block_grad_workspace(n, d, t, gates, b.gate_rows if gates else 1), dev)
     _launch(lib().spec_block_norm_grad, dev, b, *y, *ho, r1, r2, *do, *dx, *dh, *dy, p_post, p_pre, p_gate, p, size)
-    return dH, dY, dw_post, dw_pre, dgate if dgate is None or gate.dim() == 2 else dgate.view(d)
+    if gate is not None and gate.dim() == 1:
+        dgate = dgate.view(d) if n > 0 else torch.zeros(d, dtype=torch.float32, device=dev)  # (a sum over no rows)
+    return dH, dY, dw_post, dw_pre, dgate
