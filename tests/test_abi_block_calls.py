@@ -38,3 +38,16 @@ def test_product_without_rows(L):
         assert L.spec_mx_product_workspace(0, N, K, b) == 0
         ws = at if b.value else None
         assert L.spec_mx_product(None, X, W, 0, N, K, None, spec.BF16, N, ws, b.value) == 0, (N, K)
+
+
+def test_outputs_that_no_call_writes(L):
+    """Without Y there is no sum and no gradient of Y: what is passed to receive them is refused."""
+    import torch
+    X = torch.zeros(4, 64)
+    m = spec.mx_empty(4, 64, spec.MX_INT8, device="cpu")
+    for kw in (dict(Hout=X), dict(y8=m), dict(h8=m), dict(Hout=X, x8=m)):
+        with pytest.raises(spec.SpecError, match="without Y"):
+            spec.block_norm(X, **kw)
+    for args in ((X, None), (None, X), (X, X)):
+        with pytest.raises(spec.SpecError, match="without Y"):
+            spec.block_norm_grad(*args, X, None, torch.zeros(4), dY=X)

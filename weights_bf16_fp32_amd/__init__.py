@@ -1047,11 +1047,13 @@ def block_norm(H, Y=None, post: bool = True, w_post=None, w_pre=None, gate=None,
                beta: float = 1.0, eps: float = 1e-6, Hout=None, X=None, y8: Mx = None, h8: Mx = None, x8: Mx = None):
     """The norms around a residual block: u = norm(Y) w_post (post) or Y, Hout = alpha H + beta gate u,
     X = norm(Hout) w_pre.  Returns (Hout, X, r_post, r_pre), r the rows' factors of the two norms
-    (None where there is none); without Y, Hout is H.  gate: [d], or [rows, d] of which
-    one row serves gate_rows rows of Y.  y8, h8, x8: MX_INT8 storage that
+    (None where there is none); without Y, Hout is H (and cannot be passed).  gate: [d], or
+    [rows, d] of which one row serves gate_rows rows of Y.  y8, h8, x8: MX_INT8 storage that
     receives Y, Hout and X.  Hout may be H, X may be Y."""
     torch, dtype, t = _torch(), H.dtype, _dt(H)
     shape = n, d = _shape(H)
+    if Y is None and not (Hout is None and y8 is None and h8 is None):
+        raise SpecError(-1, "without Y there is no Hout, y8 or h8 to write")
     dev = _on(H)
     h, ldh = _mat(H, shape, dtype, dev)
     b, _ = _block(n, d, dtype, t, dev, post, w_post, w_pre, gate, gate_rows, alpha, beta, eps)
@@ -1103,9 +1105,11 @@ def block_norm_grad(dX, dHout, Hout, Y, r_pre, r_post=None, post: bool = True, w
         raise SpecError(-1, "a gradient of X or of Hout is needed")
     dtype, t = like.dtype, _dt(like)
     shape = n, d = _shape(like)
-    dev = _on(like)
     if Y is None:
+        if dY is not None:
+            raise SpecError(-1, "without Y there is no dY to write")
         post, w_post, gate = False, None, None
+    dev = _on(like)
     b, gates = _block(n, d, dtype, t, dev, post, w_post, w_pre, gate, gate_rows, alpha, beta, 1e-6)
     none = (None, 0)
 
