@@ -51,3 +51,15 @@ def test_outputs_that_no_call_writes(L):
     for args in ((X, None), (None, X), (X, X)):
         with pytest.raises(spec.SpecError, match="without Y"):
             spec.block_norm_grad(*args, X, None, torch.zeros(4), dY=X)
+
+
+def test_workspace_is_its_bytes(L):
+    """A workspace counts with the bytes that it has: one byte expanded to a thousand is refused."""
+    import torch
+    ws = torch.zeros(1000, dtype=torch.uint8)
+    at = spec._scratch(ws, 1000, -1)
+    assert at[:2] == (ws.data_ptr(), 1000)
+    assert spec._scratch(ws.view(torch.float32), 1000, -1)[1] == 1000
+    for bad in (ws[:1].expand(1000), ws[::2], ws.view(10, 100)[:, :50]):
+        with pytest.raises(spec.SpecError, match="contiguous"):
+            spec._scratch(bad, 500, -1)

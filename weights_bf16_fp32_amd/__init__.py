@@ -888,6 +888,8 @@ def _scratch(ws, size, dev):
         torch = _torch()
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
         return ws.data_ptr(), size, ws
+    if not ws.is_contiguous():  # its elements would not be its bytes (expand)
+        raise SpecError(-1, "a workspace must be contiguous")
     return _at(ws, dev), ws.numel() * ws.element_size(), ws
 
 
