@@ -716,9 +716,10 @@ typedef struct {
     int64_t gate_rows;   /* >= 1 where there is a gate */
 } spec_block;
 
-/* Y == NULL: the norm of H alone (Hout is H and not written).  Hout, X, r_post, r_pre (f32 [n])
- * may each be NULL: not wanted.  y8, h8, x8 (SPEC_MX_INT8, NULL: not wanted) receive Y, Hout and X
- * as spec_mx_quantize would store them.  Hout may be H, and X may be Y (same rows).
+/* Y == NULL: the norm of H alone (Hout is H and not written; alpha, beta, w_post and gate do
+ * not count).  Hout, X, r_post, r_pre (f32 [n]) may each be NULL: not wanted.  y8, h8, x8
+ * (SPEC_MX_INT8, NULL: not wanted) receive Y, Hout and X as spec_mx_quantize would store them.
+ * Hout may be H, and X may be Y (same rows).
  * Requires 0 <= n < 2^31, 1 <= d <= 16384, ld* >= d of the matrices given, Y where Hout, r_post, y8 or h8 is
  * wanted; else SPEC_EINVAL. */
 int spec_block_norm(void *stream, const spec_block *b, const void *Y, int64_t ldy, const void *H, int64_t ldh,
@@ -730,7 +731,7 @@ int spec_block_norm(void *stream, const spec_block *b, const void *Y, int64_t ld
  *   n1 = Y r_post,  c = beta gate w_post G,  dY = r_post (c - n1 mean(c n1))     (post == 0: n1 = Y, dY = c)
  *   dw_pre = sum dX n2,  dw_post = sum beta gate G n1,  dgate = sum over the gate row's rows of beta w_post G n1
  * Y and Hout are given as matrices or, where y8 / h8 is not NULL, as SPEC_MX_INT8; Hout is needed where dX is
- * given; Y and y8 both NULL: no block (dY, dw_post, dgate not wanted).  r_post, r_pre as
+ * given; Y and y8 both NULL: no block (dH = G; dY, dw_post, dgate not wanted).  r_post, r_pre as
  * spec_block_norm returned them (r_post where post, r_pre where dX is given).
  * dw_post, dw_pre: f32 [d], dgate: f32 [ceil(n / gate_rows)][d], written (zeros for n = 0; dw_pre
  * only where dX is given).  Outputs may be NULL: not wanted.  dH may be dHout, and dY may be dX (same rows).

@@ -44,3 +44,24 @@ def test_vector_gate_without_rows(spec, dtype, post):
     assert dh.shape == dy.shape == (0, d)
     for g in (dw_pre, dgate) + ((dw_post,) if post else ()):
         assert g.shape == (d,) and g.dtype == torch.float32 and not g.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_alone_has_no_scales(spec, dtype):
+    """Without a block the norm is that of H: alpha and beta scale neither it nor its gradient."""
+    import torch
+    print_case("block_norm alone", dtype=dtype)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    h, dx, dout = (torch.randn(19, 100, generator=g, device="cuda").to(dt) for _ in range(3))
+    w = torch.randn(100, generator=g, device="cuda").to(dt)
+    scales = dict(alpha=0.5, beta=3.0)
+    _, x, _, r = spec.block_norm(h, w_pre=w)
+    _, again, _, r2 = spec.block_norm(h, w_pre=w, **scales)
+    assert torch.equal(x, again) and torch.equal(r, r2)
+    for a, b in ((dx, dout), (dx, None), (None, dout)):
+        want = spec.block_norm_grad(a, b, h, None, r, w_pre=w)
+        got = spec.block_norm_grad(a, b, h, None, r, w_pre=w, **scales)
+        for s, t in zip(want, got):
+            assert (s is None and t is None) or torch.equal(s, t)

@@ -1098,7 +1098,8 @@ def block_norm_grad_workspace(n: int, d: int, dtype, gates: int = 0, gate_rows: 
 def block_norm_grad(dX, dHout, Hout, Y, r_pre, r_post=None, post: bool = True, w_post=None, w_pre=None, gate=None,
                     gate_rows: int = 1, alpha: float = 1.0, beta: float = 1.0, dH=None, dY=None, ws=None):
     """Gradients of block_norm from those of its X and (otherwise than through X) of its Hout; one
-    of them may be None: zero.  Hout and Y as they were, or as stored in MX_INT8; Y None: no block.
+    of them may be None: zero.  Hout and Y as they were, or as stored in MX_INT8; Y None: no block,
+    the gradients of the norm of Hout itself.
     Returns (dH, dY, dw_post, dw_pre, dgate), the last three float32, None for what was not given.
     dH may be dHout, dY may be dX."""
     torch = _torch()

@@ -688,7 +688,7 @@ hipError_t block_grad(hipStream_t stream, const spec_block *b, GradIo io, float 
     const int64_t ldany = hasX ? io.lddx : io.lddo;
     if (!hasX) io.dX = io.O = any, io.lddx = io.ldo = ldany, io.oq = Stored{}, io.r2 = nullptr;
     if (!io.keepO) io.dO = any, io.lddo = ldany;
-    if (!hasY) io.Y = any, io.ldy = ldany, a.post = 0;
+    if (!hasY) io.Y = any, io.ldy = ldany, a.post = 0, a.alpha = 1.f;  // (the norm of H itself)
     if (!a.post) io.r1 = nullptr;
     const GradDeal p = grad_deal(a.n, a.d, a.gate_rows, a.gate != nullptr);
     const GradPart part{(float *)ws, (float *)(ws + sums_bytes(p, a.d)), up_h(a.d, 8), p};
