@@ -65,3 +65,24 @@ def test_norm_alone_has_no_scales(spec, dtype):
         got = spec.block_norm_grad(a, b, h, None, r, w_pre=w, **scales)
         for s, t in zip(want, got):
             assert (s is None and t is None) or torch.equal(s, t)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_weight_of_an_absent_gradient(spec, bad):
+    """Without dX nothing comes through the second norm, whatever its weight holds."""
+    import torch
+    print_case("block_norm_grad without dX", bad=bad)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for d in (5, 100, 9000):
+        h, y, dout = (torch.randn(7, d, generator=g, device="cuda") for _ in range(3))
+        w = torch.randn(d, generator=g, device="cuda")
+        odd = w.clone()
+        odd[d // 2] = bad
+        _, _, r_post, r_pre = spec.block_norm(h, y, w_post=w, w_pre=w)
+        args = dict(w_post=w, gate=w, alpha=0.75)
+        want = spec.block_norm_grad(None, dout, h, y, r_pre, r_post, w_pre=w, **args)
+        got = spec.block_norm_grad(None, dout, h, y, r_pre, r_post, w_pre=odd, **args)
+        assert torch.equal(want[0], 0.75 * dout) and got[3] is None
+        for s, t in zip(want, got):
+            assert (s is None and t is None) or torch.equal(s, t)

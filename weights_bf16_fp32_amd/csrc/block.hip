@@ -686,7 +686,8 @@ hipError_t block_grad(hipStream_t stream, const spec_block *b, GradIo io, float 
     io.keepO = io.dO != nullptr ? ~0u : 0;
     const void *any = hasX ? io.dX : io.dO;  // one of the two is there
     const int64_t ldany = hasX ? io.lddx : io.lddo;
-    if (!hasX) io.dX = io.O = any, io.lddx = io.ldo = ldany, io.oq = Stored{}, io.r2 = nullptr;
+    // (w2 out of the way too: zero times one of its infinities would be NaN)
+    if (!hasX) io.dX = io.O = any, io.lddx = io.ldo = ldany, io.oq = Stored{}, io.r2 = nullptr, a.w2 = nullptr;
     if (!io.keepO) io.dO = any, io.lddo = ldany;
     if (!hasY) io.Y = any, io.ldy = ldany, a.post = 0, a.alpha = 1.f;  // (the norm of H itself)
     if (!a.post) io.r1 = nullptr;
