@@ -86,3 +86,21 @@ def test_weight_of_an_absent_gradient(spec, bad):
         assert torch.equal(want[0], 0.75 * dout) and got[3] is None
         for s, t in zip(want, got):
             assert (s is None and t is None) or torch.equal(s, t)
+
+
+@pytest.mark.parametrize("d", [3, 100, 1000, 4096, 9000])
+def test_norm_alone_of_infinities(spec, d):
+    """The mean square of a row with an infinity is infinite and its factor zero: zeros beside the
+    infinity, NaN (0 inf) at it.  A row with NaN is NaN."""
+    import torch
+    print_case("block_norm alone of infinities", d=d)
+    for dt in (torch.bfloat16, torch.float32):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(d)
+        h = torch.randn(6, d, generator=g, device="cuda").to(dt)
+        _, clean, _, r = spec.block_norm(h)
+        h[1, 0], h[3, d - 1], h[4, d // 2] = float("inf"), -float("inf"), float("nan")
+        _, x, _, r2 = spec.block_norm(h)
+        assert torch.equal(x[[0, 2, 5]], clean[[0, 2, 5]]) and torch.equal(r2[[0, 2, 5]], r[[0, 2, 5]])
+        assert r2[1] == 0 and r2[3] == 0 and r2[4].isnan() and x[4].isnan().all()
+        assert x[1, 0].isnan() and not x[1, 1:].any() and x[3, d - 1].isnan() and not x[3, :d - 1].any()

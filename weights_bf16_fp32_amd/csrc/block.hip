@@ -159,6 +159,7 @@ struct BlockArgs {
     int64_t n, d;
     float alpha, beta, eps, inv_d;
     int post;
+    int alone;  // no block: h' is h itself
     const void *w1, *w2, *gate;
     int64_t ldg, gate_rows;
 };
@@ -204,7 +205,7 @@ SPEC_DEVICE Raw8<E> load_or_ones(const void *w, int i, int d)
 }
 
 // worker w of `workers` takes rows w, w + workers, ...
-// (Where there is no block, Y is H with beta = 0.)
+// (Where there is no block, Y is H, read and not used: 0 times an infinity would be NaN.)
 template <typename E, typename SH>
 __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typename E::st *Y, int64_t ldy,
                                                        const typename E::st *H, int64_t ldh, typename E::st *O, int64_t ldo,
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typena
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float u = v[8 * i + e] * r * w1[i].get(e) * gt[i].get(e);
-                v[8 * i + e] = __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
+                v[8 * i + e] = a.alone ? h[i].get(e) : __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
             }
         if (O != nullptr || oq.q != nullptr) {
 #pragma unroll
@@ -660,9 +661,9 @@ hipError_t block_norm(hipStream_t stream, const spec_block *b, const void *Y, in
 {
     using st = typename E::st;
     BlockArgs a = block_args(b);
-    if (Y == nullptr) {  // h' = 1 h + 0 h
+    if (Y == nullptr) {
         Y = H, ldy = ldh;
-        a.post = 0, a.w1 = a.gate = nullptr, a.alpha = 1.f, a.beta = 0.f;
+        a.post = 0, a.w1 = a.gate = nullptr, a.alone = 1;
     }
     return pick_norm(b->d, [&](auto shape) {
         using SH = decltype(shape);
