@@ -104,3 +104,24 @@ def test_norm_alone_of_infinities(spec, d):
         assert torch.equal(x[[0, 2, 5]], clean[[0, 2, 5]]) and torch.equal(r2[[0, 2, 5]], r[[0, 2, 5]])
         assert r2[1] == 0 and r2[3] == 0 and r2[4].isnan() and x[4].isnan().all()
         assert x[1, 0].isnan() and not x[1, 1:].any() and x[3, d - 1].isnan() and not x[3, :d - 1].any()
+
+
+@pytest.mark.parametrize("d,v,eps", [(1, 1e19, 3e38), (100, 3e19, 3e38), (1000, 1e18, 1e38), (5000, 2e19, 1e37), (100, 1e25, 1e38),
+                                     (16384, 1e19, 3.3e38)])
+def test_large_eps_beside_large_values(spec, d, v, eps):
+    """eps counts as far as f32 holds it, where sums of squares or they and eps leave f32's range too.
+    r within (d / 2 + 8) u: half of the sum's error, the mean's, the sum's with eps, the root's."""
+    import torch
+    print_case("block_norm eps", d=d, v=v, eps=eps)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    h = (v * (1 + torch.rand(5, d, generator=g, device="cuda")))
+    eps32 = torch.tensor(eps).double().item()
+    hd = h.double()
+    want = ((hd * hd).mean(1) + eps32).rsqrt()
+    rel = (d / 2 + 8) * U
+    _, x, _, r = spec.block_norm(h, eps=eps)
+    assert bool(((r.double() - want).abs() <= rel * want).all())
+    assert bool(((x.double() - hd * want[:, None]).abs() <= (rel + 3 * U) * (hd * want[:, None])).all())
+    _, _, r_post, _ = spec.block_norm(torch.zeros_like(h), h, eps=eps)
+    assert bool(((r_post.double() - want).abs() <= rel * want).all())

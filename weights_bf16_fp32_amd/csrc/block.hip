@@ -135,8 +135,8 @@ struct RowSum {
     }
 };
 
-// (mean of v^2 + eps)^(-1/2) from the sum of squares.  A sum past f32's range is
-// formed again from values scaled by 2^-80 (all threads of the row agree on it).
+// (mean of v^2 + eps)^(-1/2) from the sum of squares.  What leaves f32's range, the sum or
+// the mean with eps, is formed again scaled by 2^-160 (all threads of the row agree on it).
 template <typename SH, int CH8>
 SPEC_DEVICE float inv_rms(const float (&v)[CH8], float inv_d, float eps, RowSum<SH, 1> &sum, int &turn)
 {
@@ -144,7 +144,8 @@ SPEC_DEVICE float inv_rms(const float (&v)[CH8], float inv_d, float eps, RowSum<
 #pragma unroll
     for (int i = 0; i < CH8; ++i) s[0] = __builtin_fmaf(v[i], v[i], s[0]);
     sum(s, turn++);
-    if (s[0] < INFINITY) return 1.f / __builtin_sqrtf(s[0] * inv_d + eps);
+    const float m = s[0] * inv_d + eps;
+    if (m < INFINITY) return 1.f / __builtin_sqrtf(m);
     float z[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < CH8; ++i) {
@@ -152,7 +153,7 @@ SPEC_DEVICE float inv_rms(const float (&v)[CH8], float inv_d, float eps, RowSum<
         z[0] = __builtin_fmaf(a, a, z[0]);
     }
     sum(z, turn++);
-    return 0x1p-80f / __builtin_sqrtf(z[0] * inv_d);
+    return 0x1p-80f / __builtin_sqrtf(z[0] * inv_d + eps * 0x1p-80f * 0x1p-80f);
 }
 
 struct BlockArgs {
