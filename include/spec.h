@@ -699,6 +699,14 @@ int spec_mx_weight_grad_workspace(int64_t T, int64_t N, int64_t K, int t, size_t
 int spec_mx_weight_grad(void *stream, const void *dY, int t, int64_t T, int64_t N, int64_t K, int64_t ldy,
                         const spec_mx *X, double beta, void *dW, int64_t lddw, void *ws, size_t ws_bytes);
 
+/* What a product of these sizes runs as (host only, for profiles and tests): the edge of its square
+ * tiles, 16 for a linear of few rows, and the shares that its sums' dimension is split into;
+ * where it is taken in pieces, of the first one.  t: the type given to the call (Y's for
+ * SPEC_MX_OP_PRODUCT).  Requires the sizes of that call. */
+enum { SPEC_MX_OP_LINEAR = 0, SPEC_MX_OP_PRODUCT = 1, SPEC_MX_OP_WEIGHT_GRAD = 2 };
+
+int spec_mx_plan(int op, int64_t T, int64_t N, int64_t K, int t, int *edge, int *shares);
+
 /* The norms around a residual block, its gate and its sum, rows of d features:
  *   u = Y r_post w_post,  r_post = (mean Y^2 + eps)^(-1/2)     (post == 0: u = Y)
  *   Hout = alpha H + beta gate u

@@ -63,3 +63,22 @@ def test_workspace_is_its_bytes(L):
     for bad in (ws[:1].expand(1000), ws[::2], ws.view(10, 100)[:, :50]):
         with pytest.raises(spec.SpecError, match="contiguous"):
             spec._scratch(bad, 500, -1)
+
+
+def test_plan(L):
+    """The query of a product's tile and shares: its refusals, and answers that the products can take."""
+    import torch
+    e, w = ctypes.c_int32(), ctypes.c_int32()
+    ok = (100, 1000, 500, spec.BF16)
+    assert L.spec_mx_plan(3, *ok, e, w) == -2 and L.spec_mx_plan(-1, *ok, e, w) == -2
+    assert L.spec_mx_plan(0, 100, 1000, 500, spec.F64, e, w) == -2
+    assert L.spec_mx_plan(0, *ok, None, w) == -1 and L.spec_mx_plan(0, *ok, e, None) == -1
+    for T, N, K in ((-1, 1, 1), ((1 << 22) + 1, 1, 1), (1, 0, 1), (1, 1, 0), (1, (1 << 20) + 1, 1), (1, 1, (1 << 20) + 1)):
+        assert L.spec_mx_plan(1, T, N, K, spec.F32, e, w) == -1
+    for op in (spec.MX_OP_LINEAR, spec.MX_OP_PRODUCT, spec.MX_OP_WEIGHT_GRAD):
+        for dt in (torch.bfloat16, torch.float32):
+            for T in (0, 1, 64, 65, 3000, 70000, 1 << 22):
+                for N, K in ((1, 1), (1000, 1000), (1 << 20, 33), (33, 1 << 20)):
+                    edge, shares = spec.mx_plan(op, T, N, K, dt)
+                    assert edge in ((16,) if op == spec.MX_OP_LINEAR and T <= 64 else (32, 64, 128, 192, 256))
+                    assert 1 <= shares <= 64

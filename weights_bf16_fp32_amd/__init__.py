@@ -40,6 +40,7 @@ __all__ = [
     "embed", "embed_grad", "embed_grad_workspace", "linear_xent", "linear_xent_workspace", "linear_xent_grad",
     "linear_xent_grad_workspace", "orthogonalize", "orthogonalize_workspace", "NS_COEFFS",
     "Mx", "MX_INT8", "MX_FP4", "mx_empty", "mx_quantize", "mx_dequantize", "mx_linear", "mx_linear_workspace",
+    "MX_OP_LINEAR", "MX_OP_PRODUCT", "MX_OP_WEIGHT_GRAD", "mx_plan",
     "mx_product", "mx_product_workspace", "mx_weight_grad", "mx_weight_grad_workspace", "block_norm", "block_norm_grad",
     "block_norm_grad_workspace",
 ]
@@ -49,6 +50,7 @@ LIB_PATH = os.path.join(_HERE, "libspec.so")
 
 BF16, F32, F64, I32, I64 = 0, 1, 2, 3, 4
 MX_INT8, MX_FP4 = 0, 1
+MX_OP_LINEAR, MX_OP_PRODUCT, MX_OP_WEIGHT_GRAD = 0, 1, 2
 GRAM_BAND, GRAM_DENSE = 0, 1
 SRC_DENSE, SRC_BAND = 0, 1
 MODE_EIG, MODE_SINGULAR = 0, 1
@@ -131,7 +133,8 @@ EXPORTS = ["spec_strerror", "spec_version", "spec_cov_accumulate", "spec_gram_wi
            "spec_embed", "spec_embed_grad_workspace", "spec_embed_grad", "spec_linear_xent_workspace",
            "spec_linear_xent", "spec_linear_xent_grad_workspace", "spec_linear_xent_grad",
            "spec_orthogonalize_workspace", "spec_orthogonalize",
-           "spec_mx_row_bytes", "spec_mx_quantize", "spec_mx_dequantize", "spec_mx_linear_workspace", "spec_mx_linear",
+           "spec_mx_row_bytes", "spec_mx_quantize", "spec_mx_dequantize", "spec_mx_plan", "spec_mx_linear_workspace",
+           "spec_mx_linear",
            "spec_mx_product_workspace", "spec_mx_product", "spec_mx_weight_grad_workspace", "spec_mx_weight_grad",
            "spec_block_norm", "spec_block_norm_grad_workspace", "spec_block_norm_grad"]
 
@@ -191,6 +194,7 @@ def lib() -> ctypes.CDLL:
         L.spec_mx_row_bytes.argtypes = [i32, i64, i64p, i64p]
         L.spec_mx_quantize.argtypes = [vp, vp, i32, i64, i64, i64, mxp]
         L.spec_mx_dequantize.argtypes = [vp, mxp, i64, i64, vp, i32, i64]
+        L.spec_mx_plan.argtypes = [i32, i64, i64, i64, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
         L.spec_mx_linear_workspace.argtypes = [i64, i64, i64, i32, szp]
         L.spec_mx_linear.argtypes = [vp, vp, i32, i64, i64, i64, i64, mxp, vp, i64, vp, sz]
         L.spec_mx_product_workspace.argtypes = [i64, i64, i64, szp]
@@ -956,6 +960,14 @@ def mx_dequantize(m: Mx, dtype=None, out=None):
         o = _mat(out, (rows, cols), dtype or out.dtype, dev)
     _launch(lib().spec_mx_dequantize, dev, d, rows, cols, o[0], _dt(out), o[1])
     return out
+
+
+def mx_plan(op: int, T: int, N: int, K: int, dtype):
+    """(edge of the tiles, shares of the sums' dimension) that mx_linear (MX_OP_LINEAR), mx_product
+    (MX_OP_PRODUCT) or mx_weight_grad (MX_OP_WEIGHT_GRAD) takes for these sizes."""
+    edge, shares = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().spec_mx_plan(op, T, N, K, _dt(_torch().empty(0, dtype=dtype)), edge, shares))
+    return edge.value, shares.value
 
 
 def mx_linear_workspace(T: int, N: int, K: int, dtype) -> int:

@@ -594,6 +594,16 @@ int spec_mx_dequantize(void *stream, const spec_mx *in, int64_t rows, int64_t co
     return from_hip(launch_mx_dequantize((hipStream_t)stream, in, rows, cols, cols, X, t, ldx));
 }
 
+int spec_mx_plan(int op, int64_t T, int64_t N, int64_t K, int t, int *edge, int *shares)
+{
+    if (op != SPEC_MX_OP_LINEAR && op != SPEC_MX_OP_PRODUCT && op != SPEC_MX_OP_WEIGHT_GRAD) return SPEC_EUNSUPPORTED;
+    if (edge == nullptr || shares == nullptr) return SPEC_EINVAL;
+    const int st = check_mx_sizes(T, N, K, t);
+    if (st != SPEC_OK) return st;
+    mx_plan(op, T, N, K, t, edge, shares);
+    return SPEC_OK;
+}
+
 int spec_mx_linear_workspace(int64_t T, int64_t N, int64_t K, int t, size_t *bytes)
 {
     if (bytes == nullptr) return SPEC_EINVAL;

@@ -115,6 +115,9 @@ hipError_t launch_mx_quantize(hipStream_t stream, const void *X, int t, int64_t 
 hipError_t launch_mx_dequantize(hipStream_t stream, const spec_mx *in, int64_t rows, int64_t cols, int64_t width, void *X,
                                 int t, int64_t ldx);
 
+// the tiles' edge and the shares of k of a product's first launch
+void mx_plan(int op, int64_t T, int64_t N, int64_t K, int t, int *edge, int *shares);
+
 size_t mx_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int t);
 size_t mx_product_workspace_bytes(int64_t T, int64_t N, int64_t K);
 size_t mx_weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, int t);

@@ -642,8 +642,7 @@ hipError_t few(hipStream_t stream, const void *X, int64_t ldx, int64_t T, int64_
 
 // The tile whose busiest CU has least to do.  per: time per result against the largest
 // tile's, the 16-bit core's ratios (steps are as many bytes and the rate follows the copies).
-template <typename F>
-hipError_t pick4(int64_t N, int64_t T, int ways, F &&f)
+int edge_of_fp4(int64_t N, int64_t T, int ways)
 {
     const int edge[4] = {256, 128, 64, 32};
     const double per[4] = {1.0, 1.3, 2.1, 6.0};
@@ -653,10 +652,16 @@ hipError_t pick4(int64_t N, int64_t T, int ways, F &&f)
         const double t = (double)cdiv_h(cdiv_h(N, edge[i]) * cdiv_h(T, edge[i]) * ways, 256) * edge[i] * edge[i] * per[i];
         if (i == 0 || t < least) least = t, best = i;
     }
-    switch (best) {
-    case 0: return f(Tile256{});
-    case 1: return f(Tile128{});
-    case 2: return f(MxTile64{});
+    return edge[best];
+}
+
+template <typename F>
+hipError_t with_tile4(int edge, F &&f)
+{
+    switch (edge) {
+    case 256: return f(Tile256{});
+    case 128: return f(Tile128{});
+    case 64: return f(MxTile64{});
     default: return f(MxTile32{});
     }
 }
@@ -671,7 +676,7 @@ hipError_t product4(hipStream_t stream, const spec_mx *X, const spec_mx *W, int6
         const int64_t tn = std::min(MOST_T, T - t0);
         const spec_mx x = rows_from(X, t0);
         MmOut o{(st *)Y + t0 * ldy, ldy, 0.f, (float *)ws, up_h(N, 4), tn, ways_of_fp4(N, tn, K)};
-        hipError_t e = pick4(N, tn, o.ways, [&](auto c) {
+        hipError_t e = with_tile4(edge_of_fp4(N, tn, o.ways), [&](auto c) {
             using C = decltype(c);
             const int tp = (int)cdiv_h(N, C::BP), tq = (int)cdiv_h(tn, C::BQ);
             hipLaunchKernelGGL((k_mx_fp4<EO, C>), dim3((unsigned)((int64_t)tp * tq * o.ways)), dim3(C::NT), 0, stream,
@@ -690,7 +695,34 @@ hipError_t product4(hipStream_t stream, const spec_mx *X, const spec_mx *W, int6
     return hipSuccess;
 }
 
+template <typename E>
+void plan(int op, int64_t T, int64_t N, int64_t K, int *edge, int *shares)
+{
+    constexpr int64_t es = sizeof(typename E::st);
+    MmPlan p;
+    if (op == SPEC_MX_OP_LINEAR && T <= FEW_ROWS)
+        p = {16, 1};
+    else if (op == SPEC_MX_OP_LINEAR)
+        p = mm_plan<E>(linear_plan(T, N, K, es).wrows, std::min(T, MOST_T), K);
+    else
+        p = mm_plan<E>(std::min(wgrad_plan(T, N, K, es).cols, K), N, T);
+    *edge = p.edge, *shares = p.ways;
+}
+
 }  // namespace
+
+void mx_plan(int op, int64_t T, int64_t N, int64_t K, int t, int *edge, int *shares)
+{
+    if (op == SPEC_MX_OP_PRODUCT) {
+        const int64_t tn = std::min(T, MOST_T);
+        *shares = ways_of_fp4(N, tn, K);
+        *edge = edge_of_fp4(N, tn, *shares);
+    } else if (t == SPEC_BF16) {
+        plan<ElBF16>(op, T, N, K, edge, shares);
+    } else {
+        plan<ElF32>(op, T, N, K, edge, shares);
+    }
+}
 
 size_t mx_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int t)
 {
