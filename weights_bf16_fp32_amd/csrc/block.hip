@@ -160,7 +160,6 @@ struct BlockArgs {
     int64_t n, d;
     float alpha, beta, eps, inv_d;
     int post;
-    int alone;  // no block: h' is h itself
     const void *w1, *w2, *gate;
     int64_t ldg, gate_rows;
 };
@@ -206,8 +205,8 @@ SPEC_DEVICE Raw8<E> load_or_ones(const void *w, int i, int d)
 }
 
 // worker w of `workers` takes rows w, w + workers, ...
-// (Where there is no block, Y is H, read and not used: 0 times an infinity would be NaN.)
-template <typename E, typename SH>
+// (ALONE: no block, and h' is h itself.)
+template <typename E, typename SH, bool ALONE>
 __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typename E::st *Y, int64_t ldy,
                                                        const typename E::st *H, int64_t ldh, typename E::st *O, int64_t ldo,
                                                        typename E::st *X, int64_t ldx, float *__restrict__ r1,
@@ -222,15 +221,16 @@ __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typena
     const auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            ny[i] = SH::template start<E>(Y + row * ldy, i, d);
+            if constexpr (!ALONE) ny[i] = SH::template start<E>(Y + row * ldy, i, d);
             nh[i] = SH::template start<E>(H + row * ldh, i, d);
         }
     };
     if (w < a.n) fetch(w);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        w1[i] = load_or_ones<E, SH>(a.w1, i, d);
         w2[i] = load_or_ones<E, SH>(a.w2, i, d);
+        if constexpr (ALONE) continue;
+        w1[i] = load_or_ones<E, SH>(a.w1, i, d);
         gt[i] = load_or_ones<E, SH>(nullptr, i, d);
     }
     int64_t gate_at = -1;
@@ -240,37 +240,45 @@ __global__ __launch_bounds__(SH::NT) void k_block_norm(BlockArgs a, const typena
 #pragma unroll
         for (int i = 0; i < CH; ++i) y[i] = ny[i], h[i] = nh[i];
         if (row + workers < a.n) fetch(row + workers);
-        if (a.gate != nullptr && row / a.gate_rows != gate_at) {
-            gate_at = row / a.gate_rows;
+        float v[8 * CH], r = 1.f;
+        if constexpr (ALONE) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) gt[i] = load_or_ones<E, SH>((const typename E::st *)a.gate + gate_at * a.ldg, i, d);
-        }
-        float v[8 * CH];
+            for (int i = 0; i < CH; ++i) {
+                SH::template end<E>(h[i], i, d);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            SH::template end<E>(y[i], i, d);
-            SH::template end<E>(h[i], i, d);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * i + e] = y[i].get(e);
-        }
-        float r = 1.f;
-        if (a.post) {
-            r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
-            if (r1 != nullptr && thread == 0) r1[row] = r;
-        }
-        if (yq.q != nullptr) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) put_stored<E>(yq, row, i * SH::TPR + thread, a.d, y[i]);
-            put_stored_end(yq, row, thread, a.d);
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = v[8 * i + e] * r * w1[i].get(e) * gt[i].get(e);
-                v[8 * i + e] = a.alone ? h[i].get(e) : __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
+                for (int e = 0; e < 8; ++e) v[8 * i + e] = h[i].get(e);
             }
-        if (O != nullptr || oq.q != nullptr) {
+        } else {
+            if (a.gate != nullptr && row / a.gate_rows != gate_at) {
+                gate_at = row / a.gate_rows;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) gt[i] = load_or_ones<E, SH>((const typename E::st *)a.gate + gate_at * a.ldg, i, d);
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                SH::template end<E>(y[i], i, d);
+                SH::template end<E>(h[i], i, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * i + e] = y[i].get(e);
+            }
+            if (a.post) {
+                r = inv_rms<SH, 8 * CH>(v, a.inv_d, a.eps, sum, turn);
+                if (r1 != nullptr && thread == 0) r1[row] = r;
+            }
+            if (yq.q != nullptr) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) put_stored<E>(yq, row, i * SH::TPR + thread, a.d, y[i]);
+                put_stored_end(yq, row, thread, a.d);
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float u = v[8 * i + e] * r * w1[i].get(e) * gt[i].get(e);
+                    v[8 * i + e] = __builtin_fmaf(a.beta, u, a.alpha * h[i].get(e));
+                }
+        }
+        if (!ALONE && (O != nullptr || oq.q != nullptr)) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 Raw8<E> o;
@@ -661,19 +669,21 @@ hipError_t block_norm(hipStream_t stream, const spec_block *b, const void *Y, in
                       const spec_mx *oq, const spec_mx *xq)
 {
     using st = typename E::st;
-    BlockArgs a = block_args(b);
-    if (Y == nullptr) {
-        Y = H, ldy = ldh;
-        a.post = 0, a.w1 = a.gate = nullptr, a.alone = 1;
-    }
+    const BlockArgs a = block_args(b);
     return pick_norm(b->d, [&](auto shape) {
         using SH = decltype(shape);
         // 16384 x 4096 bf16 with 3, 4, 6 and 8 workgroups of 256 threads per CU: 114, 125, 112
         // and 115 us; 8192 x 4097 f32 137, 114, 117 and 120
         const int64_t grid = std::min<int64_t>(cdiv_h(b->n, SH::ROWS), 256 * 6 * 256 / SH::NT);
-        hipLaunchKernelGGL((k_block_norm<E, SH>), dim3((unsigned)grid), dim3(SH::NT), 0, stream, a,
-                           (const st *)Y, ldy, (const st *)H, ldh, (st *)O, ldo, (st *)X, ldx, r1, r2, stored(yq),
-                           stored(oq), stored(xq), grid * SH::ROWS);
+        const auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(SH::NT), 0, stream, a, (const st *)Y, ldy, (const st *)H,
+                               ldh, (st *)O, ldo, (st *)X, ldx, r1, r2, stored(yq), stored(oq), stored(xq),
+                               grid * SH::ROWS);
+        };
+        if (Y == nullptr)
+            go(k_block_norm<E, SH, true>);
+        else
+            go(k_block_norm<E, SH, false>);
         return hipGetLastError();
     });
 }
