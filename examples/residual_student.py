@@ -1,12 +1,13 @@
-"""A student of residual blocks around projected layers: trained with its activations
-stored in 8 bits, answering from its layers in 4.
+"""A student of residual blocks: trained with its activations stored in 8 bits, scored from
+its layers in 4.
 
 Each block norms the residual stream, takes the norm through a layer, norms the
 result, gates it and adds it to the stream; the tied head reads the last norm.  The
 forward pass keeps, per block, the layer's input, its output and the new stream as
 MX_INT8 (a little over a byte per value); the gradients of the norms and of the layers are
-formed from those.  At the end the layers are packed into MX_FP4 and the same
-tokens scored with them.
+formed from those.  (The layers themselves, in bf16 while training, are random at first
+and multiplied by torch.)  At the end they are packed into MX_FP4 and the same tokens
+scored with them.
 
     python examples/residual_student.py [steps]
 """

@@ -667,7 +667,8 @@ int spec_mx_row_bytes(int fmt, int64_t cols, int64_t *codes, int64_t *scales);
  * Requires 0 <= rows < 2^31, 1 <= cols <= 2^20, ldx >= cols; else SPEC_EINVAL. */
 int spec_mx_quantize(void *stream, const void *X, int t, int64_t rows, int64_t cols, int64_t ldx, const spec_mx *out);
 
-/* The values, to X of type t (exact in bf16 too; values below 2^-133 round there). */
+/* The values, to X of type t: exact in both types.  (Bytes 253 and 254 of an FP4 block, which
+ * spec_mx_quantize does not write, put its largest values past both types' range: infinite.) */
 int spec_mx_dequantize(void *stream, const spec_mx *in, int64_t rows, int64_t cols, void *X, int t, int64_t ldx);
 
 /* Y[T][N] = X[T][K] W^T with W [N][K] in SPEC_MX_FP4 (else SPEC_EUNSUPPORTED), X and Y of type
@@ -717,7 +718,7 @@ typedef struct {
     int32_t t;           /* SPEC_BF16 or SPEC_F32: matrices, weights and gate */
     int32_t post;        /* whether Y is normed */
     double alpha, beta;  /* finite in f32 */
-    double eps;          /* > 0 in f32 */
+    double eps;          /* > 0 in f32, not subnormal there */
     const void *w_post, *w_pre; /* [d], NULL: ones (w_post NULL where post == 0) */
     const void *gate;    /* row i takes gate row i / gate_rows; NULL: ones */
     int64_t ldg;         /* >= d where there are several gate rows */

@@ -24,10 +24,14 @@
 //
 // A row is requested while the one before it is worked on, by loads without branches
 // (a branch around a load makes the compiler wait for it: 16384 x 4096 bf16 gradients took
-// 186 us so, 157 without).  Forward of 16384 x 4096 bf16 107 us, 5.0 TB/s; gradients from
-// 8-bit storage 149 us and 9 for the join, 4.3 TB/s, the vector work between the loads
-// in their way; 2047 x 1000 f32 gradients 17.5 us in all.  One eight of a row per thread
-// is slower in the forward (142 us), two are in the gradients (280 us: 256 registers).
+// 186 us so, 157 without).  16384 x 4096 bf16, a call among others: forward 107 us, 5.0 TB/s;
+// with all three matrices stored in 8 bits too 152 us, 4.9 TB/s; the norm alone 43 us, 6.2 TB/s
+// (H partly from the caches); gradients from the matrices 180 us, 4.5 TB/s, from 8-bit storage 156 us,
+// 4.3 TB/s, the vector work between the loads in their way, 8.5 us of each the join.
+// 2047 x 1000 f32 gradients are 14.7 and 4.0 us of kernels.  One eight of a row per thread is slower
+// in the forward (142 us), two are in the gradients (280 us: 256 registers).  Gradients of
+// f32 rows past 4096 features and of all past 8192 spill: 8192 x 4097 f32 494 us, 1.6 TB/s,
+// 4096 x 16384 bf16 490 to 540 us, 1.6 TB/s.
 #include <algorithm>
 
 #include "mx.h"

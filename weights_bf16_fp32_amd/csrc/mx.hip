@@ -1,11 +1,13 @@
 // Microscaled storage of matrices and back, gfx950 (the format: mx.h).
 //
 // Both directions are bound by memory: one read and one write per element, 3.03 bytes
-// (bf16 and int8) to 5.03 (f32).  16384 x 4096 bf16 to int8 36 us (5.6 TB/s), back 32 us
-// (6.3 TB/s, the codes partly from the caches); 1000 x 333 f32 to FP4 and back 3.8 and 3.5 us.  Four lanes hold a block of 32, eight values each (one
-// 16-byte load of bf16), so the block's largest value takes two lane exchanges
-// and nothing goes through LDS.  A row is given to as many lanes as it has eights
-// (a power of two, at most 256), several rows of a short kind to a workgroup.
+// (bf16 and int8) to 5.03 (f32).  Medians: 16384 x 4096 bf16 to int8 and back 39 and 39 us over
+// four matrices in turn (5.2 TB/s), 40 and 33 over one (the codes partly from the caches); 14336 x
+// 4096 bf16 to FP4 and back 30 and 30 us (5.0 and 4.9 TB/s), 1000 x 333 f32 4.4 and 3.5 us.
+// Four lanes hold a block of 32, eight values each (one 16-byte load of bf16), so the
+// block's largest value takes two lane exchanges and nothing goes through LDS.  A row is
+// given to as many lanes as it has eights (a power of two, at most 256), several rows of a
+// short kind to a workgroup.
 #include <algorithm>
 
 #include "mx.h"

@@ -5,22 +5,29 @@
 //   wgrad    dW[n][k] = beta dW[n][k] + sum_t dY[t][n] X[t][k]     X in INT8, dY bf16 or f32
 //
 // product: both operands go to the scaled MFMA as they lie in memory, 32 codes and
-// their byte per lane (k_mx_fp4).  8192 x 14336 x 4096 takes 291 to 308 us, 3.1 to 3.3
-// PFLOP/s, bound as the bf16 core is: by the MFMAs' power and by the copies through the
-// L2, 64 KB of codes per CU and step of 256 k.  Unpacked to bf16 first it took 749 us.
+// their byte per lane (k_mx_fp4).  8192 x 14336 x 4096 takes 299 us, 3.2 PFLOP/s, in seven
+// rounds of 256 tiles.  From k = 4096 on every step of 256 k adds 1.9 us to a tile (the bf16
+// core's step of 64 k, as many bytes and MFMA cycles, 1.6); the 16 steps here are 30 of a tile's
+// 41 us.  The other 11 are its first copies and its results, which nothing overlaps with one
+// workgroup to a CU: the share that the bf16 core spreads over four times as many steps.
+// The MFMAs are busy for 0.37 of the cycles (bf16 0.62), at 2.0 GHz (1.9).  32768 k reach
+// 4.4 PFLOP/s.  Unpacked to bf16 first it took 749 us.
 //
 // linear, few rows of X (a decode step): bound by reading W and by X's fragments, which
-// every workgroup reads from the L2 (k_mx_few).  1, 8, 16, 32 and 64 x 4096 x 4096 bf16
-// take 4.6, 6.0, 7.3, 11.1 and 19.4 us; 8 x 14336 x 4096 11.1 us, 2.8 TB/s of W.  Requesting
-// W or X a step ahead, X in whole 64-byte pieces turned between lanes, and 4 or 16 waves
-// instead of 8 changed these by less than 5 %.
+// every workgroup reads from the L2 (k_mx_few).  1, 8, 16, 32 and 64 x 4096 x 4096 bf16 take
+// 7.1, 7.0, 7.7, 11.9 and 20.4 us with W taken in turn from 600 MB of matrices, as the layers
+// of a model are, and 4.3, 5.6, 6.9, 10.7 and 19.2 us where the same W stays in the caches;
+// 8 x 14336 x 4096 13.2 us, 2.4 TB/s of W, and 11.0; f32 26.0 and 24.6.  Requesting W or X a
+// step ahead, X in whole 64-byte pieces turned between lanes, and 4 or 16 waves instead of 8
+// changed these by less than 5 %.
 //
 // linear of more rows, and wgrad: a microscaled value has at most seven significant
 // bits and a power of two, so it is exact in bf16.  The packed operand is unpacked into
-// the workspace (22 to 30 us for 14336 x 4096, 16384 x 4096) and the products are those
-// of mm.h, bf16 or f32 MFMA with f32 sums: 2047 x 4096 x 14336 191 us, 1260 TFLOP/s (one
+// the workspace (26 and 33 us for 14336 x 4096 FP4, 16384 x 4096 int8) and the products are
+// those of mm.h, bf16 or f32 MFMA with f32 sums: 2047 x 4096 x 14336 197 us, 1220 TFLOP/s (one
 // round of 256 tiles, k in two shares, and 14 us to join them; unsplit 192 x 192 tiles
-// took 244), 16384 x 4096 x 4096 455 us, 1210 TFLOP/s.
+// took 244), 224 us the whole call; 16384 x 4096 x 4096 468 us, 1170 TFLOP/s, 474 us the whole
+// call.  (Kernels: medians of a trace, whose passes lie apart; calls: among others.)
 //
 //   k_mx_pack   X or dY with 16-byte rows (only where they have none)
 //   k_mx_mm     bf16 or f32 tiles
@@ -487,8 +494,8 @@ hipError_t product(hipStream_t stream, const typename E::st *P, int64_t ldp, int
     return hipGetLastError();
 }
 
-// Packed matrices are unpacked a piece of rows (linear, product) or of columns
-// (wgrad, whose rows are the sums' k) at a time; rows of up_h(c, 32) values.
+// Packed matrices are unpacked a piece of rows (linear) or of columns (wgrad, whose rows
+// are the sums' k) at a time; rows of up_h(c, 32) values.
 int64_t piece_rows(int64_t rows, int64_t row_bytes)
 {
     return std::min(rows, std::max<int64_t>(256, PIECE_BYTES / row_bytes / 256 * 256));
